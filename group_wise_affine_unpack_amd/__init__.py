@@ -7,10 +7,13 @@ CPU fallback: if the library is missing this module raises on first use.
 
 Functions mirror the C entry points:
     qmm_affine, qgemv_affine, qgemv_affine_grouped, qmm_gptq, qgemm_w4a8,
-    gptq_to_affine_repack, quantize_pack_affine
+    gptq_to_affine_repack, quantize_pack_affine, rmsnorm, rmsnorm_w4a8,
+    qgemm_w4a8_codes, kv_cache_append_affine, kv_cache_read_affine,
+    paged_attention_affine
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Optional
@@ -19,7 +22,9 @@ import torch
 
 __all__ = ["QaffError", "qmm_affine", "qmm_affine_noalloc", "qgemv_affine", "qgemv_affine_grouped", "GroupedGemv", "qmm_gptq", "qgemm_w4a8", "qgemm_w4a8_tiled", "gptq_to_affine_repack",
            "quantize_pack_affine", "dequantize_affine", "qgemv_affine_silu_gate", "smoothquant_factors",
-           "w4a8_quantize_weights", "qgemm_w4a8_smooth", "release_workspaces", "GemvChain", "library_path", "lib",
+           "w4a8_quantize_weights", "qgemm_w4a8_smooth", "qgemm_w4a8_codes", "rmsnorm", "rmsnorm_w4a8", "AffineKVCache",
+           "kv_cache_append_affine", "kv_cache_read_affine", "paged_attention_affine",
+           "release_workspaces", "GemvChain", "library_path", "lib",
            "STATUS", "DTYPE"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +51,13 @@ _SIGS = {
     "smoothquant_factors": [_VP, _VP, _I32, C.c_double, _VP, _I64, _I64, _VP],
     "w4a8_quantize_weights": [_VP, _I32, _VP, _VP, _VP, _I64, _I64, _VP],
     "qgemm_w4a8_smooth": [_VP] * 8 + [_I64] * 3 + [_VP],
+    "qgemm_w4a8_codes": [_VP] * 6 + [_I64] * 3 + [_VP],
+    "rmsnorm": [_VP] * 3 + [C.c_double] + [_VP] * 2 + [_I64] * 5 + [_I32] * 2 + [_VP],
+    "rmsnorm_w4a8": [_VP] * 3 + [C.c_double] + [_VP] * 3 + [_I64] * 5 + [_I32] * 2 + [_VP],
+    "kv_cache_append_affine": [_VP] * 3 + [_I64] * 4 + [_VP, _I64, _VP],
+    "kv_cache_read_affine": [_VP] * 4 + [_I64, _VP],
+    "paged_attention_affine": [_VP, _VP] + [_I64] * 2 + [_VP] + [_I64] * 2 + [_VP] * 2 + [_I64, _I32, C.c_double, _I64,
+                                                                                       _VP],
     "qaff_stream_read": [_VP, C.c_uint64, _VP, _I32, _VP],
     "qgemv_affine_chain_plan": [_VP, _I32, _I32, _I32, _I32, C.POINTER(_VP)],
     "qgemv_affine_chain_run": [_VP, _VP],
@@ -64,6 +76,13 @@ class ChainLinear(C.Structure):
     """qaff_chain_linear (include/qaff.h)."""
     _fields_ = [("x", _VP), ("gate", _VP), ("resid", _VP), ("w_packed", _VP), ("scales", _VP), ("biases", _VP),
                 ("y", _VP), ("N", _I64), ("K", _I64), ("stage", _I32)]
+
+
+class KVCacheArrays(C.Structure):
+    """qaff_kv_cache (include/qaff.h)."""
+    _fields_ = [(n, _VP) for n in ("k_packed", "k_scales", "k_biases", "v_packed", "v_scales", "v_biases")] + \
+               [("num_pages", _I64)] + \
+               [(n, _I32) for n in ("page_size", "kv_heads", "head_dim", "group_size", "bits", "dtype")]
 
 
 class QaffError(RuntimeError):
@@ -129,6 +148,45 @@ def _u32(t: torch.Tensor) -> torch.Tensor:
     if t.dtype not in (torch.int32, torch.uint32):
         raise ValueError("packed words must be an int32/uint32 tensor")
     return t
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(device):
+    """The context in which `device` is the current one (a launch goes to the current device)."""
+    return _HERE_ALREADY if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _same(first: torch.Tensor, **others):
+    """Checks that (tensor, shape) pairs have their shapes and lie on the device of `first`."""
+    for name, (t, shape) in others.items():
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _out(out: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or out.dtype != dtype or out.device != device:
+        raise ValueError(f"out must be a {tuple(shape)} tensor of {dtype} on {device}")
+    return out
+
+
+def _row_ptr(t: torch.Tensor) -> int:
+    """Address of a tensor whose last dimension is dense; the others go by their strides."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _stride(t: torch.Tensor, dim: int) -> int:
+    """Stride of a dimension; 0 where it has one entry, whose stride means nothing."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
 
 
 def _affine(fn: str, x, w_packed, scales, biases, group_size, bits, k_perm, out):
@@ -356,6 +414,155 @@ def qgemm_w4a8_smooth(x: torch.Tensor, smooth: torch.Tensor, w_q4: torch.Tensor,
                                  _ptr(acc), M, N, K, _stream(dev))
     _check(st, "qgemm_w4a8_smooth")
     return y, x_q, s_x, acc
+
+
+def qgemm_w4a8_codes(x_q: torch.Tensor, s_x: torch.Tensor, w_q4: torch.Tensor, s_w: torch.Tensor,
+                     want_acc: bool = False, out: Optional[torch.Tensor] = None):
+    """qgemm_w4a8 from int8 codes x_q [M, K] and scales s_x [M] (rmsnorm_w4a8): (y f16 [M, N], acc int32 or None)."""
+    M, K = x_q.shape
+    N = w_q4.shape[0]
+    dev = x_q.device
+    if x_q.dtype != torch.int8 or s_x.dtype != torch.float32 or s_w.dtype != torch.float16:
+        raise ValueError("x_q must be int8, s_x float32 and s_w float16")
+    _same(x_q, s_x=(s_x, (M,)), w_q4=(w_q4, (N, K // 8)), s_w=(s_w, (N,)))
+    y = _out(out, (M, N), torch.float16, dev)
+    acc = torch.empty((M, N), dtype=torch.int32, device=dev) if want_acc else None
+    with _on(dev):
+        st = lib().qgemm_w4a8_codes(_ptr(x_q), _ptr(s_x), _ptr(_u32(w_q4)), _ptr(s_w), _ptr(y), _ptr(acc), M, N, K,
+                                    _stream(dev))
+    _check(st, "qgemm_w4a8_codes")
+    return y, acc
+
+
+def _norm(fn: str, x, weight, eps, resid, resid_out, outputs):
+    M, K = x.shape
+    _same(x, weight=(weight, (K,)))
+
+    def stride(t):
+        return t.stride(0) if M > 1 else K
+
+    h, ld = x, [stride(x), K, K]
+    if resid is not None:
+        _same(x, resid=(resid, (M, K)))
+        h = torch.empty((M, K), dtype=x.dtype, device=x.device) if resid_out is None else resid_out
+        _same(x, resid_out=(h, (M, K)))
+        if resid.dtype != x.dtype or h.dtype != x.dtype:
+            raise ValueError("x, resid and resid_out must have one dtype")
+        ld = [stride(x), stride(resid), stride(h)]
+    elif resid_out is not None:
+        raise ValueError("resid_out without resid")
+    with _on(x.device):
+        st = getattr(lib(), fn)(_row_ptr(x), None if resid is None else _row_ptr(resid), _ptr(weight), eps,
+                                None if resid is None else _row_ptr(h), *[_ptr(t) for t in outputs], M, K, *ld, _dt(x),
+                                _dt(weight), _stream(x.device))
+    _check(st, fn)
+    return h
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid: Optional[torch.Tensor] = None,
+            resid_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """(y, h): h = x + resid (x without resid), y = h / rms(h) * weight; x, resid, resid_out [M, K] with dense rows."""
+    y = _out(out, x.shape, x.dtype, x.device)
+    return y, _norm("rmsnorm", x, weight, eps, resid, resid_out, (y,))
+
+
+def rmsnorm_w4a8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid: Optional[torch.Tensor] = None,
+                 resid_out: Optional[torch.Tensor] = None):
+    """(x_q int8 [M, K], s_x f32 [M], h): rmsnorm's value quantized per row, for qgemm_w4a8_codes."""
+    x_q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    s_x = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    return x_q, s_x, _norm("rmsnorm_w4a8", x, weight, eps, resid, resid_out, (x_q, s_x))
+
+
+class AffineKVCache:
+    """A paged key-value cache in the affine layout (qaff_kv_cache).
+
+    `k` and `v` are triples (packed, scales, biases) of the caller's tensors:
+    packed [num_pages, kv_heads, page_size, head_dim * bits / 32] int32,
+    scales and biases [num_pages, kv_heads, page_size, head_dim / group_size]
+    in bf16 or f16, the type of the keys, values and queries.  Holds
+    references to them.  `AffineKVCache.empty` allocates them.
+    """
+
+    def __init__(self, k, v, group_size: int, bits: int):
+        self.k, self.v = tuple(k), tuple(v)
+        packed, scales = self.k[:2]
+        if bits not in (2, 4, 8):
+            raise ValueError("bits must be 2, 4 or 8")
+        pages, heads, size, words = packed.shape
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, words * 32 // bits
+        self.group_size, self.bits, self.dtype, self.device = group_size, bits, scales.dtype, packed.device
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("scales must be bfloat16 or float16")
+        rows = (pages, heads, size)
+        for name, (p, s, b) in (("k", self.k), ("v", self.v)):
+            _same(packed, **{name + " packed": (_u32(p), (*rows, words)),
+                             name + " scales": (s, (*rows, self.head_dim // group_size)),
+                             name + " biases": (b, (*rows, self.head_dim // group_size))})
+            if s.dtype != self.dtype or b.dtype != self.dtype:
+                raise ValueError("scales and biases must have one dtype")
+        self.arrays = KVCacheArrays(*[_ptr(t) for t in self.k + self.v], pages, size, heads, self.head_dim, group_size,
+                                    bits, DTYPE[self.dtype])
+        self.ref = C.addressof(self.arrays)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int = 64, bits: int = 4,
+              dtype=torch.bfloat16, device="cuda") -> "AffineKVCache":
+        """A cache of zeros."""
+        rows = (num_pages, kv_heads, page_size)
+        k, v = ((torch.zeros((*rows, head_dim * bits // 32), dtype=torch.int32, device=device),
+                 torch.zeros((*rows, head_dim // group_size), dtype=dtype, device=device),
+                 torch.zeros((*rows, head_dim // group_size), dtype=dtype, device=device)) for _ in range(2))
+        return cls(k, v, group_size, bits)
+
+
+def kv_cache_append_affine(cache: AffineKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize k, v [T, kv_heads, head_dim] (rows dense) into slots [T] int64 of the cache; a slot outside is skipped."""
+    T = slots.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    _same(cache.k[0], k=(k, shape), v=(v, shape), slots=(slots, (T,)))
+    if k.dtype != cache.dtype or v.dtype != cache.dtype or slots.dtype != torch.int64:
+        raise ValueError(f"k and v must be {cache.dtype}, slots int64")
+    with _on(cache.device):
+        st = lib().kv_cache_append_affine(cache.ref, _row_ptr(k), _row_ptr(v), _stride(k, 0), _stride(k, 1),
+                                          _stride(v, 0), _stride(v, 1), _ptr(slots), T, _stream(cache.device))
+    _check(st, "kv_cache_append_affine")
+
+
+def kv_cache_read_affine(cache: AffineKVCache, slots: torch.Tensor, out=None):
+    """(k, v) [T, kv_heads, head_dim] of slots [T] int64; a slot outside the cache reads as zeros."""
+    T = slots.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    _same(cache.k[0], slots=(slots, (T,)))
+    if slots.dtype != torch.int64:
+        raise ValueError("slots must be int64")
+    k, v = (_out(o, shape, cache.dtype, cache.device) for o in (out or (None, None)))
+    with _on(cache.device):
+        st = lib().kv_cache_read_affine(cache.ref, _ptr(slots), _ptr(k), _ptr(v), T, _stream(cache.device))
+    _check(st, "kv_cache_read_affine")
+    return k, v
+
+
+def paged_attention_affine(q: torch.Tensor, cache: AffineKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                           scale: Optional[float] = None, window: int = 0,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of one new token a sequence, q [B, heads, head_dim] (rows dense), over the cached tokens.
+
+    page_table [B, max_pages] int32 (rows dense), seq_lens [B] int32; scale
+    defaults to head_dim ** -0.5; window > 0 keeps the last `window` tokens.
+    """
+    B, heads, D = q.shape
+    _same(cache.k[0], q=(q, (B, heads, cache.head_dim)), page_table=(page_table, (B, page_table.shape[-1])),
+          seq_lens=(seq_lens, (B,)))
+    if q.dtype != cache.dtype or page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise ValueError(f"q must be {cache.dtype}, page_table and seq_lens int32")
+    o = _out(out, q.shape, q.dtype, q.device)
+    with _on(cache.device):
+        st = lib().paged_attention_affine(cache.ref, _row_ptr(q), _stride(q, 0), _stride(q, 1), _row_ptr(page_table),
+                                          _stride(page_table, 0), page_table.shape[1], _ptr(seq_lens), _ptr(o), B,
+                                          heads, D ** -0.5 if scale is None else scale, window, _stream(cache.device))
+    _check(st, "paged_attention_affine")
+    return o
 
 
 def gptq_to_affine_repack(qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tensor,

@@ -177,6 +177,8 @@ struct W4A8Args {
 hipError_t launch_w4a8(const W4A8Args& a, hipStream_t s);
 // the integer product and epilogue of W4A8 from x_q and s_x already written
 hipError_t launch_w4a8_product(const W4A8Args& a, hipStream_t s);
+// the same after the shape check of launch_w4a8
+hipError_t launch_w4a8_codes(const W4A8Args& a, hipStream_t s);
 // M > 16 with a chosen lowering (staged: quantize inside the GEMM; else the
 // quantize kernel, then the full-K GEMM) and tile bm x bn
 hipError_t launch_w4a8_config(const W4A8Args& a, int staged, int bm, int bn, hipStream_t s);
@@ -190,6 +192,61 @@ hipError_t launch_smooth_quant(const void* x, const float* smooth, int64_t M, in
 
 hipError_t launch_dequant(const uint32_t* w, const void* s, const void* b, void* out, int64_t N, int64_t K, int G,
                           int bits, int sdt, int bdt, int odt, hipStream_t st);
+
+// ---- operators between the linears of a decoder layer --------------------
+
+// quotient of a number below 2^31 by d in [1, 2^31): a multiply and a shift
+struct FastDiv {
+  uint32_t d, mul, shift;
+  explicit FastDiv(uint32_t div) : d(div), shift(0) {
+    // mul = ceil(2^(31 + shift) / d) with 2^shift >= d: below 2^32, and the
+    // excess n * (mul * d - 2^(31 + shift)) < 2^31 * d leaves the quotient
+    while ((1u << shift) < div) ++shift;
+    mul = (uint32_t)(((uint64_t(1) << (31 + shift)) + div - 1) / div);
+  }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> 31 >> shift);
+  }
+};
+
+struct NormArgs {
+  const void* x;      // [M, K], row stride ldx
+  const void* resid;  // [M, K], row stride ldr, or null
+  const void* w;      // [K]
+  void* h_out;        // [M, K], row stride ldh; null without resid
+  void* y;            // [M, K] dense output, or null
+  int8_t* x_q;        // [M, K] codes, or null
+  float* s_x;         // [M]
+  int64_t M, K, ldx, ldr, ldh;
+  double eps;
+  int act_dt, w_dt;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s);
+
+struct KvCache {
+  uint32_t *k_packed, *v_packed;                          // [pages, heads, page_size, D*bits/32]
+  uint16_t *k_scales, *k_biases, *v_scales, *v_biases;    // [pages, heads, page_size, D/G]
+  int64_t num_pages, num_slots;                           // num_slots = num_pages * page_size < 2^31
+  int page_size, kv_heads, head_dim, G, bits, dt;
+};
+struct KvRows {
+  const void *k, *v;         // [T, heads, D]
+  int64_t kts, khs, vts, vhs;  // token and head strides in elements
+};
+hipError_t launch_kv_append(const KvCache& c, const KvRows& r, const int64_t* slots, int64_t T, hipStream_t s);
+hipError_t launch_kv_read(const KvCache& c, const int64_t* slots, void* k, void* v, int64_t T, hipStream_t s);
+
+struct PagedAttnArgs {
+  KvCache c;
+  const void* q;          // [B, heads, D], strides qts (sequence), qhs (head)
+  const int32_t* table;   // [B, max_pages], row stride table_stride
+  const int32_t* seq_lens;
+  void* out;              // [B, heads, D]
+  int64_t qts, qhs, table_stride, window, B;
+  int heads, max_pages;
+  float scale;
+};
+hipError_t launch_paged_attention(const PagedAttnArgs& a, hipStream_t s);
 
 // streaming read of `bytes` (a multiple of 16) by `blocks` x 256 threads;
 // sink holds blocks*256 words

@@ -3,6 +3,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <string>
 #include <vector>
 
@@ -413,6 +414,228 @@ int w4a8_quantize_weights(const void* w, int32_t w_dtype, const float* smooth, u
   hipError_t e = qaff::launch_w4a8_weights(w, w_dtype, smooth, N, K, w_q4_out, static_cast<uint16_t*>(s_w_out),
                                            static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "w4a8 weight quantization launch");
+  return ok();
+}
+
+int qgemm_w4a8_codes(const int8_t* x_q, const float* s_x, const uint32_t* w_q4, const void* s_w, void* y,
+                     int32_t* acc_out, int64_t M, int64_t N, int64_t K, void* stream) {
+  if (M < 0 || N <= 0 || K <= 0) return fail(QAFF_E_INVAL, "sizes must satisfy M >= 0, N > 0, K > 0");
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(QAFF_E_UNSUPPORTED, "dimension above 2^30");
+  if (K % 32) return fail(QAFF_E_INVAL, "K must be a multiple of 32 (got %lld)", (long long)K);
+  if (K > (int64_t(1) << 17)) return fail(QAFF_E_UNSUPPORTED, "K above 131072 could overflow the int32 accumulator");
+  if (M == 0) return ok();
+  if (!x_q || !s_x || !w_q4 || !s_w || !y) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(w_q4) || !aligned16(x_q)) return fail(QAFF_E_ALIGN, "w_q4 and x_q must be 16-byte aligned");
+  qaff::W4A8Args a;
+  a.x = nullptr;
+  a.w = w_q4;
+  a.s_w = s_w;
+  a.y = y;
+  a.x_q = const_cast<int8_t*>(x_q);  // read only: the product takes them as written
+  a.s_x = const_cast<float*>(s_x);
+  a.acc = acc_out;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  (void)hipGetLastError();
+  hipError_t e = qaff::launch_w4a8_codes(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "this shape has no kernel");
+  if (e != hipSuccess) return hip_fail(e, "w4a8 product launch");
+  return ok();
+}
+
+static int check_rmsnorm(const void* x, const void* resid, const void* weight, double eps, const void* h_out,
+                         int64_t M, int64_t K, int64_t ldx, int64_t ldr, int64_t ldh, int act_dt, int w_dt) {
+  if (M < 0 || K <= 0) return fail(QAFF_E_INVAL, "sizes must satisfy M >= 0, K > 0 (got %lld, %lld)", (long long)M, (long long)K);
+  if (M > kMaxDim || K > kMaxDim) return fail(QAFF_E_UNSUPPORTED, "dimension above 2^30");
+  if (!act_dtype_ok(act_dt)) return fail(QAFF_E_INVAL, "act_dtype must be QAFF_BF16 or QAFF_F16 (got %d)", act_dt);
+  if (!sb_dtype_ok(w_dt)) return fail(QAFF_E_INVAL, "w_dtype must be BF16, F16 or F32 (got %d)", w_dt);
+  if (!(eps >= 0.0 && eps < 1e300)) return fail(QAFF_E_INVAL, "eps must be finite and >= 0");
+  if (M == 0) return QAFF_OK;
+  if (!x || !weight) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if ((resid != nullptr) != (h_out != nullptr)) return fail(QAFF_E_INVAL, "h_out is required with resid, and only then");
+  if (ldx < K || (resid && (ldr < K || ldh < K))) return fail(QAFF_E_INVAL, "a row stride is below K=%lld", (long long)K);
+  const int64_t ld = std::max(ldx, resid ? std::max(ldr, ldh) : ldx);
+  if (ld > (int64_t(1) << 40)) return fail(QAFF_E_UNSUPPORTED, "row stride above 2^40");
+  const uintptr_t odd = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(resid) | reinterpret_cast<uintptr_t>(h_out);
+  if (odd & 1u) return fail(QAFF_E_ALIGN, "x, resid and h_out must be 2-byte aligned");
+  if (reinterpret_cast<uintptr_t>(weight) & (w_dt == QAFF_F32 ? 3u : 1u)) return fail(QAFF_E_ALIGN, "weight must be aligned to its type");
+  return QAFF_OK;
+}
+
+static qaff::NormArgs norm_args(const void* x, const void* resid, const void* weight, double eps, void* h_out,
+                                int64_t M, int64_t K, int64_t ldx, int64_t ldr, int64_t ldh, int act_dt, int w_dt) {
+  qaff::NormArgs a;
+  a.x = x;
+  a.resid = resid;
+  a.w = weight;
+  a.h_out = h_out;
+  a.y = nullptr;
+  a.x_q = nullptr;
+  a.s_x = nullptr;
+  a.M = M;
+  a.K = K;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldh = ldh;
+  a.eps = eps;
+  a.act_dt = act_dt;
+  a.w_dt = w_dt;
+  return a;
+}
+
+int rmsnorm(const void* x, const void* resid, const void* weight, double eps, void* h_out, void* y, int64_t M,
+            int64_t K, int64_t x_stride, int64_t resid_stride, int64_t h_stride, int32_t act_dtype, int32_t w_dtype,
+            void* stream) {
+  int rc = check_rmsnorm(x, resid, weight, eps, h_out, M, K, x_stride, resid_stride, h_stride, act_dtype, w_dtype);
+  if (rc != QAFF_OK) return rc;
+  if (M == 0) return ok();
+  if (!y) return fail(QAFF_E_INVAL, "null tensor pointer (y)");
+  if (reinterpret_cast<uintptr_t>(y) & 1u) return fail(QAFF_E_ALIGN, "y must be 2-byte aligned");
+  qaff::NormArgs a = norm_args(x, resid, weight, eps, h_out, M, K, x_stride, resid_stride, h_stride, act_dtype, w_dtype);
+  a.y = y;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_rmsnorm(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "rmsnorm launch");
+  return ok();
+}
+
+int rmsnorm_w4a8(const void* x, const void* resid, const void* weight, double eps, void* h_out, int8_t* x_q,
+                 float* s_x, int64_t M, int64_t K, int64_t x_stride, int64_t resid_stride, int64_t h_stride,
+                 int32_t act_dtype, int32_t w_dtype, void* stream) {
+  int rc = check_rmsnorm(x, resid, weight, eps, h_out, M, K, x_stride, resid_stride, h_stride, act_dtype, w_dtype);
+  if (rc != QAFF_OK) return rc;
+  if (M == 0) return ok();
+  if (!x_q || !s_x) return fail(QAFF_E_INVAL, "null tensor pointer (x_q, s_x)");
+  if (reinterpret_cast<uintptr_t>(s_x) & 3u) return fail(QAFF_E_ALIGN, "s_x must be 4-byte aligned");
+  qaff::NormArgs a = norm_args(x, resid, weight, eps, h_out, M, K, x_stride, resid_stride, h_stride, act_dtype, w_dtype);
+  a.x_q = x_q;
+  a.s_x = s_x;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_rmsnorm(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "rmsnorm launch");
+  return ok();
+}
+
+// checks the cache and fills `out`
+static int check_cache(const qaff_kv_cache* c, qaff::KvCache* out) {
+  if (!c) return fail(QAFF_E_INVAL, "null cache");
+  if (!(c->bits == 2 || c->bits == 4 || c->bits == 8)) return fail(QAFF_E_INVAL, "bits must be 2, 4 or 8 (got %d)", c->bits);
+  if (!group_ok(c->group_size)) return fail(QAFF_E_INVAL, "group_size must be 32, 64 or 128 (got %d)", c->group_size);
+  if (c->head_dim <= 0 || c->head_dim % c->group_size)
+    return fail(QAFF_E_INVAL, "head_dim=%d is not a positive multiple of group_size=%d", c->head_dim, c->group_size);
+  if (!act_dtype_ok(c->dtype)) return fail(QAFF_E_INVAL, "dtype must be QAFF_BF16 or QAFF_F16 (got %d)", c->dtype);
+  if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1)
+    return fail(QAFF_E_INVAL, "num_pages, page_size and kv_heads must be >= 1");
+  if (c->head_dim > 256) return fail(QAFF_E_UNSUPPORTED, "head_dim above 256 (got %d)", c->head_dim);
+  if (c->page_size % 16) return fail(QAFF_E_UNSUPPORTED, "page_size must be a multiple of 16 (got %d)", c->page_size);
+  if (c->kv_heads > (1 << 16)) return fail(QAFF_E_UNSUPPORTED, "kv_heads above 65536");
+  if (c->num_pages >= (int64_t(1) << 31) / c->page_size) return fail(QAFF_E_UNSUPPORTED, "2^31 slots or more");
+  const void* p[6] = {c->k_packed, c->k_scales, c->k_biases, c->v_packed, c->v_scales, c->v_biases};
+  for (const void* q : p) {
+    if (!q) return fail(QAFF_E_INVAL, "null tensor pointer in the cache");
+    if (!aligned16(q)) return fail(QAFF_E_ALIGN, "the cache's arrays must be 16-byte aligned");
+  }
+  out->k_packed = c->k_packed;
+  out->k_scales = static_cast<uint16_t*>(c->k_scales);
+  out->k_biases = static_cast<uint16_t*>(c->k_biases);
+  out->v_packed = c->v_packed;
+  out->v_scales = static_cast<uint16_t*>(c->v_scales);
+  out->v_biases = static_cast<uint16_t*>(c->v_biases);
+  out->num_pages = c->num_pages;
+  out->num_slots = c->num_pages * c->page_size;
+  out->page_size = c->page_size;
+  out->kv_heads = c->kv_heads;
+  out->head_dim = c->head_dim;
+  out->G = c->group_size;
+  out->bits = c->bits;
+  out->dt = c->dtype;
+  return QAFF_OK;
+}
+
+static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (int64_t(1) << 40); }
+
+int kv_cache_append_affine(const qaff_kv_cache* cache, const void* k, const void* v, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                           int64_t T, void* stream) {
+  qaff::KvCache c;
+  int rc = check_cache(cache, &c);
+  if (rc != QAFF_OK) return rc;
+  if (T < 0) return fail(QAFF_E_INVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > kMaxDim) return fail(QAFF_E_UNSUPPORTED, "T above 2^30");
+  if (T == 0) return ok();
+  if (!k || !v || !slots) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(k) || !aligned16(v)) return fail(QAFF_E_ALIGN, "k and v must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(QAFF_E_ALIGN, "slots must be 8-byte aligned");
+  if (!stride_ok(k_token_stride) || !stride_ok(k_head_stride) || !stride_ok(v_token_stride) || !stride_ok(v_head_stride))
+    return fail(QAFF_E_ALIGN, "strides must be non-negative multiples of 8 elements");
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_kv_append(
+      c, qaff::KvRows{k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride}, slots, T,
+      static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "too many rows for one call");
+  if (e != hipSuccess) return hip_fail(e, "cache append launch");
+  return ok();
+}
+
+int kv_cache_read_affine(const qaff_kv_cache* cache, const int64_t* slots, void* k_out, void* v_out, int64_t T,
+                         void* stream) {
+  qaff::KvCache c;
+  int rc = check_cache(cache, &c);
+  if (rc != QAFF_OK) return rc;
+  if (T < 0) return fail(QAFF_E_INVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > kMaxDim) return fail(QAFF_E_UNSUPPORTED, "T above 2^30");
+  if (T == 0) return ok();
+  if (!k_out || !v_out || !slots) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(QAFF_E_ALIGN, "k_out and v_out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(QAFF_E_ALIGN, "slots must be 8-byte aligned");
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_kv_read(c, slots, k_out, v_out, T, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "too many rows for one call");
+  if (e != hipSuccess) return hip_fail(e, "cache read launch");
+  return ok();
+}
+
+int paged_attention_affine(const qaff_kv_cache* cache, const void* q, int64_t q_seq_stride, int64_t q_head_stride,
+                           const int32_t* page_table, int64_t table_stride, int64_t max_pages, const int32_t* seq_lens,
+                           void* out, int64_t B, int32_t heads, double scale, int64_t window, void* stream) {
+  qaff::PagedAttnArgs a;
+  int rc = check_cache(cache, &a.c);
+  if (rc != QAFF_OK) return rc;
+  const int D = a.c.head_dim;
+  if (!(D == 64 || D == 96 || D == 128 || D == 192 || D == 256))
+    return fail(QAFF_E_UNSUPPORTED, "head_dim must be 64, 96, 128, 192 or 256 (got %d)", D);
+  if (B < 0 || max_pages < 0) return fail(QAFF_E_INVAL, "B and max_pages must be >= 0");
+  if (heads < 1 || heads % a.c.kv_heads)
+    return fail(QAFF_E_INVAL, "heads=%d is not a positive multiple of kv_heads=%d", heads, a.c.kv_heads);
+  if (B > 65535 || heads > (1 << 16)) return fail(QAFF_E_UNSUPPORTED, "B above 65535 or heads above 65536");
+  if (max_pages >= (int64_t(1) << 31) / a.c.page_size) return fail(QAFF_E_UNSUPPORTED, "max_pages * page_size of 2^31 or more");
+  if (!(scale > -1e30 && scale < 1e30)) return fail(QAFF_E_INVAL, "scale must be finite");
+  if (window < 0) return fail(QAFF_E_INVAL, "window must be >= 0 (got %lld)", (long long)window);
+  if (B == 0) return ok();
+  if (!q || !seq_lens || !out || (!page_table && max_pages > 0)) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(out)) return fail(QAFF_E_ALIGN, "q and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u)
+    return fail(QAFF_E_ALIGN, "page_table and seq_lens must be 4-byte aligned");
+  if (!stride_ok(q_seq_stride) || !stride_ok(q_head_stride))
+    return fail(QAFF_E_ALIGN, "strides must be non-negative multiples of 8 elements");
+  if (table_stride < 0 || table_stride > (int64_t(1) << 40)) return fail(QAFF_E_INVAL, "table_stride must lie in [0, 2^40]");
+  a.q = q;
+  a.table = page_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.qts = q_seq_stride;
+  a.qhs = q_head_stride;
+  a.table_stride = table_stride;
+  a.window = window;
+  a.B = B;
+  a.heads = heads;
+  a.max_pages = (int)max_pages;
+  a.scale = (float)scale;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_paged_attention(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "this shape has no kernel");
+  if (e != hipSuccess) return hip_fail(e, "paged attention launch");
   return ok();
 }
 

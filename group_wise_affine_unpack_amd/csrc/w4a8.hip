@@ -999,6 +999,10 @@ hipError_t launch_w4a8_product(const W4A8Args& a, hipStream_t s) {
   return launch_gemm_tile(a, false, auto_tile(M, N, K), s);
 }
 
+hipError_t launch_w4a8_codes(const W4A8Args& a, hipStream_t s) {
+  return shape_ok(a) ? launch_w4a8_product(a, s) : hipErrorNotSupported;
+}
+
 hipError_t launch_w4a8(const W4A8Args& a, hipStream_t s) {
   if (!shape_ok(a)) return hipErrorNotSupported;
   const int M = (int)a.M, N = (int)a.N, K = (int)a.K;

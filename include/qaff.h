@@ -363,6 +363,137 @@ int qgemm_w4a8_smooth(const void *x, const float *smooth, const uint32_t *w_q4, 
                       int8_t *x_q, float *s_x, int32_t *acc_out, int64_t M, int64_t N, int64_t K, void *stream);
 
 /*
+ * qgemm_w4a8_codes - qgemm_w4a8 from activations that are int8 codes
+ * already (rmsnorm_w4a8 writes them): acc and y exactly as qgemm_w4a8
+ * defines them from x_q and s_x, which are inputs here.  The quantize
+ * launch falls away.  x_q [M, K] int8, codes in [-127, 127]; s_x [M] f32;
+ * the other arguments and errors as for qgemm_w4a8.
+ */
+int qgemm_w4a8_codes(const int8_t *x_q, const float *s_x, const uint32_t *w_q4, const void *s_w, void *y,
+                     int32_t *acc_out, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * rmsnorm, rmsnorm_w4a8 - root-mean-square norm of each row, with the
+ * residual's addition ahead of it, in one launch:
+ *     h[m,k] = x[m,k] + resid[m,k], rounded once to act_dtype (x without resid)
+ *     n[m,k] = (h[m,k] * rstd[m]) * weight[k],
+ *              rstd = f32(1 / sqrt(mean_k h^2 + eps)), the mean in fp64
+ *   rmsnorm:       y[m,k]   = n[m,k] rounded once to act_dtype
+ *   rmsnorm_w4a8:  s_x[m]   = max_k |n[m,k]| / 127          (IEEE fp32 division)
+ *                  x_q[m,k] = clamp(rint(n[m,k] / s_x[m]), -127, 127), half to
+ *                             even; s_x = 0 and codes 0 for a row of zeros
+ *                  (the rule of qgemm_w4a8, taken on n before any rounding to
+ *                  16 bits; qgemm_w4a8_codes takes both)
+ *   x       [M, K] act_dtype (BF16 or F16), rows x_stride elements apart
+ *   resid   [M, K] act_dtype or NULL, rows resid_stride apart
+ *   weight  [K]    w_dtype (BF16, F16 or F32)
+ *   h_out   [M, K] act_dtype, rows h_stride apart: h, what the next residual
+ *           addition takes.  Required with resid (it may be resid or x
+ *           itself with that one's stride: the residual stream updated in
+ *           place), NULL without it.
+ *   y, x_q  [M, K] dense;  s_x [M] f32.  They must not overlap the inputs.
+ *   K >= 1; strides >= K; eps >= 0 and finite.  Any alignment of 2 bytes
+ *   (16-byte aligned rows with K % 8 == 0 run faster).  The products and
+ *   divisions are IEEE fp32 and the sum is fp64, so outputs do not depend on
+ *   the launch.  A NaN in h makes its row's dense values NaN; the codes of a
+ *   row that holds a NaN or an infinity are unspecified.
+ */
+int rmsnorm(const void *x, const void *resid, const void *weight, double eps, void *h_out, void *y, int64_t M,
+            int64_t K, int64_t x_stride, int64_t resid_stride, int64_t h_stride, int32_t act_dtype, int32_t w_dtype,
+            void *stream);
+int rmsnorm_w4a8(const void *x, const void *resid, const void *weight, double eps, void *h_out, int8_t *x_q,
+                 float *s_x, int64_t M, int64_t K, int64_t x_stride, int64_t resid_stride, int64_t h_stride,
+                 int32_t act_dtype, int32_t w_dtype, void *stream);
+
+/*
+ * A paged key-value cache in the affine layout.  A row is one token's key
+ * (or value) of one head: head_dim codes in uint32 words, lowest column in
+ * the low bits, and a scale and a bias per group of group_size columns, the
+ * layout of a qmm_affine weight row.  Rows lie page by page, in a page head
+ * by head; token `off` of page `p` is slot p * page_size + off.  The caller
+ * owns every array (device memory; the struct itself is read during the call
+ * only).
+ *   bits in {2, 4, 8}; group_size in {32, 64, 128}; head_dim a multiple of
+ *   group_size, at most 256; page_size a multiple of 16 (others:
+ *   QAFF_E_UNSUPPORTED); dtype BF16 or F16, the type of scales and biases
+ *   and of the queries, keys, values and outputs of the calls below;
+ *   num_pages * page_size < 2^31.  The arrays may pass 4 GiB.
+ */
+typedef struct qaff_kv_cache {
+    uint32_t *k_packed; /* [num_pages, kv_heads, page_size, head_dim*bits/32], 16-byte aligned */
+    void *k_scales;     /* [num_pages, kv_heads, page_size, head_dim/group_size] dtype, 16-byte aligned */
+    void *k_biases;     /* as k_scales */
+    uint32_t *v_packed; /* as k_packed, k_scales, k_biases, for the values */
+    void *v_scales;
+    void *v_biases;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t group_size;
+    int32_t bits;
+    int32_t dtype;
+} qaff_kv_cache;
+
+/*
+ * kv_cache_append_affine - quantize the keys and values of T tokens into
+ * their slots.  Each row gets the codes, scales and biases, bit for bit,
+ * that quantize_pack_affine gives that row (w_dtype = sb_dtype = dtype).
+ *   k, v   [T, kv_heads, head_dim] dtype, 16-byte aligned; token and head
+ *          strides in elements, multiples of 8 (0 is a broadcast): the
+ *          slices of a fused q/k/v product need no copy
+ *   slots  [T] int64: the slot of each token.  A slot outside
+ *          [0, num_pages * page_size) is skipped (-1 marks the padding of a
+ *          batch).  Slots in range must be distinct: two tokens of one slot
+ *          race, and the row then mixes both.
+ * Nothing but the named rows is written.  One launch.
+ */
+int kv_cache_append_affine(const qaff_kv_cache *cache, const void *k, const void *v, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                           const int64_t *slots, int64_t T, void *stream);
+
+/*
+ * kv_cache_read_affine - the dense keys and values of T slots:
+ *     value = code * scale + bias, in fp32 (the product exact, the sum
+ *     rounded), then rounded to dtype
+ *   slots  [T] int64, repeats allowed; a slot outside the cache reads as zeros
+ *   k_out, v_out  [T, kv_heads, head_dim] dtype, dense, 16-byte aligned
+ * One launch.
+ */
+int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void *k_out, void *v_out, int64_t T,
+                         void *stream);
+
+/*
+ * paged_attention_affine - attention of one new token of each of B sequences
+ * over the cached tokens of that sequence, the new one's own row among them
+ * (append it first):
+ *     z[t] = scale * sum_d q[b,h,d] * k[t,d],
+ *            t in [max(0, len - window), len), or [0, len) with window = 0
+ *     out[b,h,d] = sum_t softmax(z)[t] * v[t,d], rounded once to dtype
+ * Token t of sequence b lies at offset t % page_size of page
+ * page_table[b, t / page_size]; query head h reads key head
+ * h / (heads / kv_heads).
+ *   q           [B, heads, head_dim] dtype, 16-byte aligned; sequence and
+ *               head strides in elements, multiples of 8
+ *   page_table  [B, max_pages] int32, rows table_stride elements apart.
+ *               Entries past a sequence's length are not read.  The tokens of
+ *               an entry outside [0, num_pages) are left out, as if masked.
+ *   seq_lens    [B] int32: cached tokens.  0 or less gives a row of zeros, as
+ *               does a row with no token left; a length past max_pages *
+ *               page_size counts as that.
+ *   out         [B, heads, head_dim] dtype, dense, 16-byte aligned
+ *   heads a multiple of kv_heads; head_dim in {64, 96, 128, 192, 256};
+ *   window >= 0; scale finite.
+ * Lengths are read on the device only: a captured call follows the lengths
+ * of the replay.  What the cache holds in slots that no sequence sees has no
+ * influence, NaN included.
+ */
+int paged_attention_affine(const qaff_kv_cache *cache, const void *q, int64_t q_seq_stride, int64_t q_head_stride,
+                           const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                           const int32_t *seq_lens, void *out, int64_t B, int32_t heads, double scale, int64_t window,
+                           void *stream);
+
+/*
  * gptq_to_affine_repack - rewrite a GPTQ layer in the affine layout
  * (setup call; it MAY SYNCHRONIZE `stream`: it reads g_idx back to the host
  * to build the permutation and to check it).
