@@ -13,7 +13,6 @@ Functions mirror the C entry points:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 from typing import Optional
@@ -133,8 +132,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# the current stream's handle, without making a torch.cuda.Stream (1.7 us of a 6 us call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -150,16 +153,20 @@ def _u32(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+def _run(name: str, device, *args) -> None:
+    """Calls an entry point on the current stream of `device`, with `device` the current one (a launch goes there)."""
+    f = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _raw_stream(device.index))
+    if st != 0:
+        _check(st, name)
 
 
-def _on(device):
-    """The context in which `device` is the current one (a launch goes to the current device)."""
-    return _HERE_ALREADY if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _same(first: torch.Tensor, **others):
-    """Checks that (tensor, shape) pairs have their shapes and lie on the device of `first`."""
+def _check_shapes(first: torch.Tensor, **others):
+    """Raises for the first of (tensor, shape) pairs that lacks its shape or lies on another device than `first`."""
     for name, (t, shape) in others.items():
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -167,11 +174,12 @@ def _same(first: torch.Tensor, **others):
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
-def _out(out: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+def _out(out: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
+    """`out`, checked, or a new dense tensor of the shape and type of `like`."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.shape != shape or out.dtype != dtype or out.device != device:
-        raise ValueError(f"out must be a {tuple(shape)} tensor of {dtype} on {device}")
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError(f"out must be a {tuple(like.shape)} tensor of {like.dtype} on {like.device}")
     return out
 
 
@@ -179,14 +187,16 @@ def _row_ptr(t: torch.Tensor) -> int:
     """Address of a tensor whose last dimension is dense; the others go by their strides."""
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("the last dimension must be contiguous")
     return t.data_ptr()
 
 
-def _stride(t: torch.Tensor, dim: int) -> int:
-    """Stride of a dimension; 0 where it has one entry, whose stride means nothing."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _strides(t: torch.Tensor):
+    """Strides of the two leading dimensions; 0 where one has a single entry, whose stride means nothing."""
+    a, b = t.stride()[:2]
+    n, m = t.shape[:2]
+    return a if n > 1 else 0, b if m > 1 else 0
 
 
 def _affine(fn: str, x, w_packed, scales, biases, group_size, bits, k_perm, out):
@@ -424,54 +434,51 @@ def qgemm_w4a8_codes(x_q: torch.Tensor, s_x: torch.Tensor, w_q4: torch.Tensor, s
     dev = x_q.device
     if x_q.dtype != torch.int8 or s_x.dtype != torch.float32 or s_w.dtype != torch.float16:
         raise ValueError("x_q must be int8, s_x float32 and s_w float16")
-    _same(x_q, s_x=(s_x, (M,)), w_q4=(w_q4, (N, K // 8)), s_w=(s_w, (N,)))
-    y = _out(out, (M, N), torch.float16, dev)
+    _check_shapes(x_q, s_x=(s_x, (M,)), w_q4=(w_q4, (N, K // 8)), s_w=(s_w, (N,)))
+    y = torch.empty((M, N), dtype=torch.float16, device=dev)
+    if out is not None:
+        y = _out(out, y)
     acc = torch.empty((M, N), dtype=torch.int32, device=dev) if want_acc else None
-    with _on(dev):
-        st = lib().qgemm_w4a8_codes(_ptr(x_q), _ptr(s_x), _ptr(_u32(w_q4)), _ptr(s_w), _ptr(y), _ptr(acc), M, N, K,
-                                    _stream(dev))
-    _check(st, "qgemm_w4a8_codes")
+    _run("qgemm_w4a8_codes", dev, _ptr(x_q), _ptr(s_x), _ptr(_u32(w_q4)), _ptr(s_w), _ptr(y), _ptr(acc), M, N, K)
     return y, acc
 
 
-def _norm(fn: str, x, weight, eps, resid, resid_out, outputs):
+def _norm(fn: str, x, weight, eps, resid, resid_out, *outputs):
     M, K = x.shape
-    _same(x, weight=(weight, (K,)))
-
-    def stride(t):
-        return t.stride(0) if M > 1 else K
-
-    h, ld = x, [stride(x), K, K]
+    dev, dt = x.device, x.dtype
+    ldx, ldr, ldh = x.stride(0) if M > 1 else K, K, K
+    if weight.shape != (K,) or weight.device != dev:
+        _check_shapes(x, weight=(weight, (K,)))
+    h, hp, rp = x, None, None
     if resid is not None:
-        _same(x, resid=(resid, (M, K)))
-        h = torch.empty((M, K), dtype=x.dtype, device=x.device) if resid_out is None else resid_out
-        _same(x, resid_out=(h, (M, K)))
-        if resid.dtype != x.dtype or h.dtype != x.dtype:
-            raise ValueError("x, resid and resid_out must have one dtype")
-        ld = [stride(x), stride(resid), stride(h)]
+        h = torch.empty_like(x, memory_format=torch.contiguous_format) if resid_out is None else resid_out
+        for t in (resid, h):
+            if t.shape != x.shape or t.device != dev:
+                _check_shapes(x, resid=(resid, x.shape), resid_out=(h, x.shape))
+            if t.dtype != dt:
+                raise ValueError("x, resid and resid_out must have one dtype")
+        if M > 1:
+            ldr, ldh = resid.stride(0), h.stride(0)
+        hp, rp = _row_ptr(h), _row_ptr(resid)
     elif resid_out is not None:
         raise ValueError("resid_out without resid")
-    with _on(x.device):
-        st = getattr(lib(), fn)(_row_ptr(x), None if resid is None else _row_ptr(resid), _ptr(weight), eps,
-                                None if resid is None else _row_ptr(h), *[_ptr(t) for t in outputs], M, K, *ld, _dt(x),
-                                _dt(weight), _stream(x.device))
-    _check(st, fn)
+    _run(fn, dev, _row_ptr(x), rp, _ptr(weight), eps, hp, *outputs, M, K, ldx, ldr, ldh, _dt(x), _dt(weight))
     return h
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid: Optional[torch.Tensor] = None,
             resid_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """(y, h): h = x + resid (x without resid), y = h / rms(h) * weight; x, resid, resid_out [M, K] with dense rows."""
-    y = _out(out, x.shape, x.dtype, x.device)
-    return y, _norm("rmsnorm", x, weight, eps, resid, resid_out, (y,))
+    y = _out(out, x)
+    return y, _norm("rmsnorm", x, weight, eps, resid, resid_out, _ptr(y))
 
 
 def rmsnorm_w4a8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid: Optional[torch.Tensor] = None,
                  resid_out: Optional[torch.Tensor] = None):
     """(x_q int8 [M, K], s_x f32 [M], h): rmsnorm's value quantized per row, for qgemm_w4a8_codes."""
-    x_q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    s_x = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
-    return x_q, s_x, _norm("rmsnorm_w4a8", x, weight, eps, resid, resid_out, (x_q, s_x))
+    x_q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    s_x = x.new_empty(x.shape[0], dtype=torch.float32)
+    return x_q, s_x, _norm("rmsnorm_w4a8", x, weight, eps, resid, resid_out, x_q.data_ptr(), s_x.data_ptr())
 
 
 class AffineKVCache:
@@ -487,8 +494,8 @@ class AffineKVCache:
     def __init__(self, k, v, group_size: int, bits: int):
         self.k, self.v = tuple(k), tuple(v)
         packed, scales = self.k[:2]
-        if bits not in (2, 4, 8):
-            raise ValueError("bits must be 2, 4 or 8")
+        if bits not in (2, 4, 8) or group_size not in (32, 64, 128):
+            raise ValueError("bits must be 2, 4 or 8 and group_size 32, 64 or 128")
         pages, heads, size, words = packed.shape
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, words * 32 // bits
         self.group_size, self.bits, self.dtype, self.device = group_size, bits, scales.dtype, packed.device
@@ -496,9 +503,9 @@ class AffineKVCache:
             raise ValueError("scales must be bfloat16 or float16")
         rows = (pages, heads, size)
         for name, (p, s, b) in (("k", self.k), ("v", self.v)):
-            _same(packed, **{name + " packed": (_u32(p), (*rows, words)),
-                             name + " scales": (s, (*rows, self.head_dim // group_size)),
-                             name + " biases": (b, (*rows, self.head_dim // group_size))})
+            _check_shapes(packed, **{name + " packed": (_u32(p), (*rows, words)),
+                                     name + " scales": (s, (*rows, self.head_dim // group_size)),
+                                     name + " biases": (b, (*rows, self.head_dim // group_size))})
             if s.dtype != self.dtype or b.dtype != self.dtype:
                 raise ValueError("scales and biases must have one dtype")
         self.arrays = KVCacheArrays(*[_ptr(t) for t in self.k + self.v], pages, size, heads, self.head_dim, group_size,
@@ -518,28 +525,32 @@ class AffineKVCache:
 
 def kv_cache_append_affine(cache: AffineKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantize k, v [T, kv_heads, head_dim] (rows dense) into slots [T] int64 of the cache; a slot outside is skipped."""
-    T = slots.shape[0]
+    dev = cache.device
+    T, = slots.shape
     shape = (T, cache.kv_heads, cache.head_dim)
-    _same(cache.k[0], k=(k, shape), v=(v, shape), slots=(slots, (T,)))
+    if k.shape != shape or v.shape != shape or k.device != dev or v.device != dev or slots.device != dev:
+        _check_shapes(cache.k[0], k=(k, shape), v=(v, shape), slots=(slots, (T,)))
     if k.dtype != cache.dtype or v.dtype != cache.dtype or slots.dtype != torch.int64:
         raise ValueError(f"k and v must be {cache.dtype}, slots int64")
-    with _on(cache.device):
-        st = lib().kv_cache_append_affine(cache.ref, _row_ptr(k), _row_ptr(v), _stride(k, 0), _stride(k, 1),
-                                          _stride(v, 0), _stride(v, 1), _ptr(slots), T, _stream(cache.device))
-    _check(st, "kv_cache_append_affine")
+    _run("kv_cache_append_affine", dev, cache.ref, _row_ptr(k), _row_ptr(v), *_strides(k), *_strides(v), _ptr(slots), T)
 
 
 def kv_cache_read_affine(cache: AffineKVCache, slots: torch.Tensor, out=None):
     """(k, v) [T, kv_heads, head_dim] of slots [T] int64; a slot outside the cache reads as zeros."""
-    T = slots.shape[0]
-    shape = (T, cache.kv_heads, cache.head_dim)
-    _same(cache.k[0], slots=(slots, (T,)))
+    T, = slots.shape
     if slots.dtype != torch.int64:
         raise ValueError("slots must be int64")
-    k, v = (_out(o, shape, cache.dtype, cache.device) for o in (out or (None, None)))
-    with _on(cache.device):
-        st = lib().kv_cache_read_affine(cache.ref, _ptr(slots), _ptr(k), _ptr(v), T, _stream(cache.device))
-    _check(st, "kv_cache_read_affine")
+    if slots.device != cache.device:
+        _check_shapes(cache.k[0], slots=(slots, (T,)))
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if out is None:
+        k, v = cache.k[1].new_empty(shape), cache.k[1].new_empty(shape)
+    else:
+        k, v = out
+        for t in out:
+            if t.shape != shape or t.dtype != cache.dtype or t.device != cache.device:
+                raise ValueError(f"out must be two {shape} tensors of {cache.dtype} on {cache.device}")
+    _run("kv_cache_read_affine", cache.device, cache.ref, _ptr(slots), _ptr(k), _ptr(v), T)
     return k, v
 
 
@@ -551,17 +562,18 @@ def paged_attention_affine(q: torch.Tensor, cache: AffineKVCache, page_table: to
     page_table [B, max_pages] int32 (rows dense), seq_lens [B] int32; scale
     defaults to head_dim ** -0.5; window > 0 keeps the last `window` tokens.
     """
+    dev = cache.device
     B, heads, D = q.shape
-    _same(cache.k[0], q=(q, (B, heads, cache.head_dim)), page_table=(page_table, (B, page_table.shape[-1])),
-          seq_lens=(seq_lens, (B,)))
+    per = page_table.shape[-1]
+    if (D != cache.head_dim or page_table.shape != (B, per) or seq_lens.shape != (B,) or q.device != dev
+            or page_table.device != dev or seq_lens.device != dev):
+        _check_shapes(cache.k[0], q=(q, (B, heads, cache.head_dim)), page_table=(page_table, (B, per)), seq_lens=(seq_lens, (B,)))
     if q.dtype != cache.dtype or page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError(f"q must be {cache.dtype}, page_table and seq_lens int32")
-    o = _out(out, q.shape, q.dtype, q.device)
-    with _on(cache.device):
-        st = lib().paged_attention_affine(cache.ref, _row_ptr(q), _stride(q, 0), _stride(q, 1), _row_ptr(page_table),
-                                          _stride(page_table, 0), page_table.shape[1], _ptr(seq_lens), _ptr(o), B,
-                                          heads, D ** -0.5 if scale is None else scale, window, _stream(cache.device))
-    _check(st, "paged_attention_affine")
+    o = _out(out, q)
+    _run("paged_attention_affine", dev, cache.ref, _row_ptr(q), *_strides(q), _row_ptr(page_table),
+         page_table.stride(0) if B > 1 else per, per, _ptr(seq_lens), _ptr(o), B, heads,
+         D ** -0.5 if scale is None else scale, window)
     return o
 
 

@@ -15,20 +15,172 @@
 namespace qaff {
 namespace {
 
-// sum (fp64) or maximum (fp32) over the WPR waves of a row; every lane gets it
+// Sum (fp64) and maximum (fp32) over the 64 lanes, every lane gets them:
+// rotations inside each row of 16 lanes, then swaps of rows.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += dpp_f64<0x128>(v);
+  v += dpp_f64<0x124>(v);
+  v += dpp_f64<0x122>(v);
+  v += dpp_f64<0x121>(v);
+  uint64_t u = __builtin_bit_cast(uint64_t, v);
+  auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  u = __builtin_bit_cast(uint64_t, v);
+  lo = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
 }
 __device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  v = fmaxf(v, dpp_mov<0x128>(v));
+  v = fmaxf(v, dpp_mov<0x124>(v));
+  v = fmaxf(v, dpp_mov<0x122>(v));
+  v = fmaxf(v, dpp_mov<0x121>(v));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+template <bool F16_>
+__device__ __forceinline__ float half_of(uint32_t w, int h) {
+  if constexpr (F16_) return f16_bits_to_f32(h ? w >> 16 : w & 0xffffu);
+  else return __uint_as_float(h ? w & 0xffff0000u : w << 16);
+}
+
+// (mean square + eps)^-1/2 in fp64, rounded once
+__device__ __forceinline__ float rstd_of(double sum, const NormArgs& a) {
+  return (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
 }
 
 __device__ __forceinline__ float q8(float n, float s) {
   return s != 0.f ? fminf(fmaxf(rintf(__fdiv_rn(n, s)), -127.f), 127.f) : 0.f;
+}
+
+// A row per WPR waves (WAVES / WPR rows a workgroup), held in registers:
+// thread i of the row takes the 8-value chunks i, i + 64 WPR, ... (CPT of
+// them, K <= 512 WPR CPT).  16-byte aligned rows, K % 8 == 0.  Every load of
+// the row, residual and weight is in flight before the first sum.
+template <bool F16_, bool CODES, bool W32, int WAVES, int WPR, int CPT>
+__global__ __launch_bounds__(64 * WAVES) void rmsnorm_rows_kernel(NormArgs a) {
+  const int t = threadIdx.x, wave = t >> 6, sub = wave % WPR;
+  const long m = (long)blockIdx.x * (WAVES / WPR) + wave / WPR;
+  const int K8 = (int)(a.K >> 3), c0 = sub * 64 + (t & 63);
+  __shared__ double sums[WAVES];
+  __shared__ float maxs[WAVES];
+  const bool in_row = WPR == WAVES || m < a.M;  // (a wave past the last row runs along for the barriers)
+  const u32x4_t* x = (const u32x4_t*)((const uint16_t*)a.x + m * a.ldx);
+  const u32x4_t* r = (const u32x4_t*)((const uint16_t*)a.resid + m * a.ldr);
+  u32x4_t h[CPT], rr[CPT], w[CPT][W32 ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = c0 + 64 * WPR * i;
+    h[i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (in_row && c < K8) {
+      h[i] = x[c];
+      if (a.resid) rr[i] = r[c];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = c0 + 64 * WPR * i;
+    if (in_row && c < K8) {
+      if constexpr (W32) {
+        w[i][0] = ((const u32x4_t*)a.w)[2 * c];
+        w[i][1] = ((const u32x4_t*)a.w)[2 * c + 1];
+      } else {
+        w[i][0] = ((const u32x4_t*)a.w)[c];
+      }
+    }
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = c0 + 64 * WPR * i;
+    if (in_row && c < K8 && a.resid) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = __fadd_rn(half_of<F16_>(h[i][j], 0), half_of<F16_>(rr[i][j], 0));
+        const float hi = __fadd_rn(half_of<F16_>(h[i][j], 1), half_of<F16_>(rr[i][j], 1));
+        h[i][j] = (uint32_t)f32_to_act_bits(lo, F16_) | (uint32_t)f32_to_act_bits(hi, F16_) << 16;
+      }
+      ((u32x4_t*)((uint16_t*)a.h_out + m * a.ldh))[c] = h[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double v = (double)half_of<F16_>(h[i][j / 2], j & 1);
+      sum = fma(v, v, sum);
+    }
+  }
+  sum = wave_sum_f64(sum);
+  if constexpr (WPR > 1) {
+    if ((t & 63) == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) sum += sums[wave - sub + k];
+  }
+  const float rstd = rstd_of(sum, a);
+  auto n_of = [&](int i, int j) {
+    float wv;
+    if constexpr (W32)
+      wv = __uint_as_float(w[i][j / 4][j & 3]);
+    else
+      wv = a.w_dt == F16 ? half_of<true>(w[i][0][j / 2], j & 1) : half_of<false>(w[i][0][j / 2], j & 1);
+    return __fmul_rn(__fmul_rn(half_of<F16_>(h[i][j / 2], j & 1), rstd), wv);
+  };
+  if constexpr (!CODES) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = c0 + 64 * WPR * i;
+      if (in_row && c < K8) {
+        u32x4_t o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = (uint32_t)f32_to_act_bits(n_of(i, 2 * j), F16_) | (uint32_t)f32_to_act_bits(n_of(i, 2 * j + 1), F16_) << 16;
+        ((u32x4_t*)((uint16_t*)a.y + m * a.K))[c] = o;
+      }
+    }
+  } else {
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+      if (in_row && c0 + 64 * WPR * i < K8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(n_of(i, j)));
+    mx = wave_max_f32(mx);
+    if constexpr (WPR > 1) {
+      if ((t & 63) == 0) maxs[wave] = mx;
+      __syncthreads();
+      mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) mx = fmaxf(mx, maxs[wave - sub + k]);
+    }
+    const float s = __fdiv_rn(mx, 127.f);
+    if (in_row && c0 == 0) a.s_x[m] = s;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = c0 + 64 * WPR * i;
+      if (in_row && c < K8) {
+        u32x2_t o;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) word |= ((uint32_t)(int)q8(n_of(i, 4 * j + e), s) & 0xffu) << (8 * e);
+          o[j] = word;
+        }
+        ((u32x2_t*)(a.x_q + m * a.K))[c] = o;
+      }
+    }
+  }
 }
 
 // One workgroup of 256 threads per row, any K and any row start.
@@ -56,7 +208,7 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
   if ((t & 63) == 0) sums[t >> 6] = sum;
   __syncthreads();
   sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-  const float rstd = (float)(1.0 / sqrt(sum / (double)K + a.eps));
+  const float rstd = rstd_of(sum, a);
   const uint16_t* hs = r ? ho : x;  // each thread reads back what it wrote
   auto n_of = [&](int k) { return __fmul_rn(__fmul_rn(load_as_f32(hs, k, DT), rstd), load_as_f32(a.w, k, a.w_dt)); };
   if constexpr (!CODES) {
@@ -77,17 +229,54 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
 
 }  // namespace
 
+namespace {
+
+template <bool F16_, bool CODES, bool W32>
+void launch_rows(const NormArgs& a, hipStream_t s) {
+  const int64_t C = a.K / 8;  // 8-value chunks
+  auto go = [&](auto kernel, int waves, int wpr) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.M + waves / wpr - 1) / (waves / wpr))), dim3(64 * waves), 0, s, a);
+  };
+  if (C <= 64)
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 1, 1>, 4, 1);
+  else if (C <= 128)
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 2, 1>, 4, 2);
+  else if (C <= 256)
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 4, 1>, 4, 4);
+  else if (C <= 512)
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 4, 2>, 4, 4);
+  else if (C <= 1024)
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 8, 8, 2>, 8, 8);
+  else
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 16, 16, 2>, 16, 16);
+}
+
+template <bool F16_, bool CODES>
+void launch_dt(const NormArgs& a, hipStream_t s) {
+  auto at16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; };
+  const bool rows = a.K % 8 == 0 && a.K <= 16384 && at16(a.x, a.ldx) && at16(a.w, 0) &&
+                    (!a.resid || (at16(a.resid, a.ldr) && at16(a.h_out, a.ldh))) &&
+                    (CODES ? (reinterpret_cast<uintptr_t>(a.x_q) & 7) == 0 : at16(a.y, 0));
+  if (!rows)
+    hipLaunchKernelGGL((rmsnorm_any_kernel<F16_, CODES>), dim3((unsigned)a.M), dim3(256), 0, s, a);
+  else if (a.w_dt == F32)
+    launch_rows<F16_, CODES, true>(a, s);
+  else
+    launch_rows<F16_, CODES, false>(a, s);
+}
+
+}  // namespace
+
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.M), block(256);
   const bool f16 = a.act_dt == F16, codes = a.x_q != nullptr;
   if (f16 && codes)
-    hipLaunchKernelGGL((rmsnorm_any_kernel<true, true>), grid, block, 0, s, a);
+    launch_dt<true, true>(a, s);
   else if (f16)
-    hipLaunchKernelGGL((rmsnorm_any_kernel<true, false>), grid, block, 0, s, a);
+    launch_dt<true, false>(a, s);
   else if (codes)
-    hipLaunchKernelGGL((rmsnorm_any_kernel<false, true>), grid, block, 0, s, a);
+    launch_dt<false, true>(a, s);
   else
-    hipLaunchKernelGGL((rmsnorm_any_kernel<false, false>), grid, block, 0, s, a);
+    launch_dt<false, false>(a, s);
   return hipGetLastError();
 }
 
