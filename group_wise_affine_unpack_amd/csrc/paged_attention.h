@@ -18,6 +18,8 @@
 // bits 0-9 of each 16-bit half (4-bit: bits 0-3 and, times 16, bits 4-7) is
 // the whole conversion: one AND for two codes.  The factors 2^24 and 16 go to
 // q (exact powers of two, per column) and to the outputs.
+// The key biases' part of z is one product more, kb[t,g] by Q_g[h] cut into
+// 16-bit pieces, in the parameters' own type.
 // Registers: C_g has the tokens of a lane's quarter (lane / 16) as rows and
 // the head (lane % 16) as column, which is where the value product takes its
 // second operand from, so p never leaves the lane.  Value codes arrive as
@@ -33,37 +35,57 @@
 // limits (a wave-uniform branch) sets a new mu.  A's smallest step is 2^-24,
 // 2^-30 of the largest term.
 //
-// Work: the tokens of all sequences are cut into chunks of about equal size
-// (the lengths are on the device, so each workgroup finds its chunk from
-// them: a sum and a scan over the batch); four waves share a chunk, joined
-// through LDS.  A sequence of one chunk is written out at once; the others
-// leave fp32 partial sums with their mu, joined by a second kernel.
+// Memory: each wave copies the 32 tokens after the ones at work straight
+// into LDS (16 bytes a lane, no register between, non-temporal: with the
+// streaming hint 131072 tokens took 39.5 us where they took 44.5), and reads
+// its operands from there in whatever layout they want.  What a lane reads
+// of memory is thereby one code row's 16-byte piece instead of 28 loads of 2
+// to 16 bytes a step.
+// What bounds it: at 8 bits memory (64 sequences of 4096 tokens, D = 128:
+// 571 MB in 95 us, 6.0 TB/s), at 4 bits the vector instructions, about 270 a
+// step of 4.6 KB (302 MB in 60 to 64 us, 4.8 TB/s; vector pipes busy 68% of
+// the time), for few tokens the chain lengths -> page table -> rows -> join.
+// Measured and not kept: operands loaded from memory into registers with one
+// step of look-ahead (70 us for those 302 MB), three or four stages of
+// look-ahead (the same), four workgroups a CU (71 us), chunks of equal size
+// instead of equal shares (a ragged 8-bit batch 119 against 101 us).
+//
+// Work: equal shares of all tiles of 128 tokens (paged_attn_kernel), four
+// waves to a tile, joined through LDS; sequences cut by a share's end leave
+// fp32 partial sums with their mu for a second kernel.  Short tables take a
+// workgroup per sequence and unit instead (paged_attn_short_kernel).
 // Instantiated per code width in paged_attention_b{2,4,8}.hip.
 #pragma once
+
+#include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
 namespace qaff {
 namespace {
 
-constexpr int WAVES = 4;
 constexpr float PBIAS = 5.f;    // log2 of p at the reference
 constexpr float MROOM = 4.f;    // how far a logit may pass the reference (log2)
-constexpr float VROOM = 64.f;   // how far a value scale may pass it
+constexpr int VROOM = 6;        // how far a value scale may pass its power of two (log2)
+
+struct AttnMeta {
+  int64_t start;  // a sequence's start on the line of one unit
+  int tiles;
+};
 
 struct AttnWork {
   PagedAttnArgs a;
   FastDiv page;         // tokens a page
   int share, htiles;    // query heads a key head; tiles of 16 of them
-  int target, min_chunk;
-  float* part_o;        // [slot][gm][D]
-  float* part_ml;       // [slot][gm][2]
-  int2* meta;           // [B]: chunks, first slot
+  float* part_o;        // [2 workgroups][gm][D]
+  float* part_ml;       // [2 workgroups][gm][2]
+  AttnMeta* meta;       // [B + 1]; the last one's `tiles` is a workgroup's share
 };
 
-template <int D_, int G_, int BITS_, bool F16_>
+template <int D_, int G_, int BITS_, bool F16_, int WAVES_>
 struct Cfg {
-  static constexpr int D = D_, G = G_, BITS = BITS_, NG = D / G;
+  static constexpr int D = D_, G = G_, BITS = BITS_, NG = D / G, WAVES = WAVES_;
   static constexpr bool ACT16 = F16_;
   static constexpr int KS = G / 32;                      // product steps a group (keys)
   static constexpr int KB = G / 4 * BITS / 8;            // key code bytes a lane and group
@@ -72,13 +94,23 @@ struct Cfg {
   static constexpr int VBITS = VC * BITS;                // value code bits a lane, token and group
   static constexpr int VW = VBITS <= 32 ? 1 : 2;
   static constexpr int SW = 2 * NG;                      // words of four tokens' scales
+  static constexpr int BW = (NG + 1) / 2;                // words of one token's
   static constexpr int ROWB = D * BITS / 8;
-};
-
-template <class C>
-struct Raw {  // what a step reads, as it lies in memory
-  uint32_t kc[2][C::NG][C::KW], ks[2][C::SW], kb[2][C::SW];
-  uint32_t vc[2][4][C::NG][C::VW], vs[2][C::SW], vb[2][C::SW];
+  // A stage in LDS: 32 tokens' key codes, value codes, then per half the
+  // key scales, key biases, value scales and value biases, each as in memory
+  static constexpr int CODES = 16 * ROWB, PARAMS = 32 * NG;  // bytes of 16 tokens' codes, of one kind of parameter
+  static constexpr int STAGE = 4 * CODES + 8 * PARAMS;
+  // Two stages a wave, one ahead of the one at work.  (Three stages and two
+  // workgroups a CU instead of three: 131072 tokens the same, a ragged 4-bit
+  // batch of 64 sequences up to 8192 tokens 75 against 67 us.)
+  static constexpr int STAGES = 2, LDS = WAVES * STAGES * STAGE;
+  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 ? 3 : LDS * 2 <= 155 * 1024 ? 2 : 1;  // workgroups of four waves
+  static constexpr int COPIES = (CODES + 1023) / 1024, PCOPIES = (8 * PARAMS + 1023) / 1024;
+  // rows of 2^n 16-byte pieces keep piece c of row r at c ^ swizzle(r), so that a piece of many rows is spread over the banks
+  static constexpr int PIECES = ROWB % 16 == 0 && ((ROWB / 16) & (ROWB / 16 - 1)) == 0 ? ROWB / 16 : 0;
+  __device__ static constexpr int swizzle(int row) { return PIECES ? (row >> 2) & (PIECES - 1) & 3 : 0; }
+  // where byte `b` of row `row` of 16 lies
+  __device__ static constexpr int at(int row, int b) { return row * ROWB + ((b >> 4 ^ swizzle(row)) << 4) + (b & 15); }
 };
 
 template <int BYTES>
@@ -94,6 +126,12 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* out) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) out[4 * i + j] = v[j];
     }
+  } else if constexpr (BYTES == 6) {
+    out[0] = *reinterpret_cast<const uint16_t*>(p) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2) << 16;
+    out[1] = *reinterpret_cast<const uint16_t*>(p + 4);
+  } else if constexpr (BYTES == 12) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) out[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   } else if constexpr (BYTES % 8 == 0) {
 #pragma unroll
     for (int i = 0; i < BYTES / 8; ++i) {
@@ -185,111 +223,250 @@ template <class C>
 struct Wave {
   // constant over the loop
   f16x8_t q[C::NG][C::KS];
-  float qsum[C::NG];
-  float zscale;           // logits to base 2, with q's power of two and the codes' taken back
+  u32x4_t qsum;           // the key biases' operand: Q_g of this lane's head, a 16-bit piece of it by the lane's quarter
+  float zscale;           // logits to base 2, with q's power of two and the codes' taken back; >= 0
   // running
   f32x4_t o[C::NG][C::VC];
   float l, bias[C::NG];   // sums over this lane's tokens
-  float mref, mu, mlim, vexp, vlim;
+  float mref, mu, mlim, vexp;
+  uint32_t vlim;          // bits of the 16-bit value scale that may not be passed
 };
 
-template <class C>
-__device__ __forceinline__ void load_raw(Raw<C>& r, int u, const KvCache& c, size_t row, uint32_t kvo, uint32_t vvo,
-                                         uint32_t svo) {
-  const uint8_t* kc = (const uint8_t*)c.k_packed + row * C::ROWB;
-  const uint8_t* vc = (const uint8_t*)c.v_packed + row * C::ROWB;
-  const size_t so = row * (2 * C::NG);
-#pragma unroll
-  for (int g = 0; g < C::NG; ++g) load_bytes<C::KB>(kc + kvo + g * (C::G * C::BITS / 8), r.kc[u][g]);
-  load_bytes<8 * C::NG>((const uint8_t*)c.k_scales + so + svo, r.ks[u]);
-  load_bytes<8 * C::NG>((const uint8_t*)c.k_biases + so + svo, r.kb[u]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int g = 0; g < C::NG; ++g)
-      load_bytes<(C::VBITS < 8 ? 1 : C::VBITS / 8)>(vc + vvo + i * C::ROWB + g * (C::G * C::BITS / 8), r.vc[u][i][g]);
-  load_bytes<8 * C::NG>((const uint8_t*)c.v_scales + so + svo, r.vs[u]);
-  load_bytes<8 * C::NG>((const uint8_t*)c.v_biases + so + svo, r.vb[u]);
+// 16 bytes a lane from memory into LDS, without a register between: lane l's
+// land at `lds` + 16 l.  The compiler does not see these loads: the wait for
+// them is wait_copies below, and every LDS read of theirs comes after it.
+// The first LANES lanes copy.  (Their mask is set here and not by a branch: one
+// divergent branch in the loop makes the compiler treat its uniform ones as
+// such, and copy every accumulator around them.)
+template <int LANES>
+__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
+  if constexpr (LANES >= 64) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(lds) : "memory");
+  } else {
+    uint64_t all;
+    asm volatile(
+        "s_mov_b64 %0, exec\n\ts_mov_b32 m0, %3\n\ts_mov_b64 exec, %4\n\t"
+        "global_load_lds_dwordx4 %1, %2 nt\n\ts_mov_b64 exec, %0"
+        : "=&s"(all)
+        : "v"(off), "s"(base), "s"(lds), "s"((uint64_t(1) << LANES) - 1)
+        : "memory");
+  }
+}
+template <int LANES>
+__device__ __forceinline__ void copy_to_lds(const uint8_t* p, uint32_t lds) {
+  uint64_t all;
+  asm volatile(
+      "s_mov_b64 %0, exec\n\ts_mov_b32 m0, %2\n\ts_mov_b64 exec, %3\n\t"
+      "global_load_lds_dwordx4 %1, off nt\n\ts_mov_b64 exec, %0"
+      : "=&s"(all)
+      : "v"(p), "s"(lds), "s"(LANES >= 64 ? ~uint64_t(0) : (uint64_t(1) << (LANES & 63)) - 1)
+      : "memory");
+}
+// f(which of the copies, its lanes) for each of the copies of N 16-byte pieces
+template <int N, int M = 0, class F>
+__device__ __forceinline__ void copies(F&& f) {
+  f(std::integral_constant<int, M>{}, std::integral_constant<int, (N - 64 * M < 64 ? N - 64 * M : 64)>{});
+  if constexpr (N > 64 * (M + 1)) copies<N, M + 1>(f);
+}
+// until this wave's copies are in LDS
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// 16x16x32 product of 16-bit parameters and pieces of Q_g, in their own type
+template <bool F16_>
+__device__ __forceinline__ f32x4_t mfma_act(u32x4_t a, u32x4_t b, f32x4_t c) {
+  if constexpr (F16_)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// 32 tokens; bit 4 u + i of `live`: token 16 u + 4 (lane / 16) + i counts
-// (all of the wave's do unless `edge`)
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// q as the products take it, from this lane's columns of each group: raw
+// [NG][G/4] 16-bit values of its head, zeros for a column that has none.
 template <class C>
-__device__ __forceinline__ void step(Wave<C>& w, const Raw<C>& r, bool edge, uint32_t live, int lane) {
-  float z[2][4], p[2][4];
+__device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C::G / 8], bool have, int kq, float scale) {
+  float qv[C::NG][C::G / 4], mx = 0.f;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int g = 0; g < C::NG; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[u][i] = 0.f;
-#pragma unroll
-    for (int g = 0; g < C::NG; ++g) {
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < C::KS; ++s)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_codes<C>(r.kc[u][g], s), w.q[g][s], acc, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[u][i] = fmaf(half_at<C::ACT16>(r.ks[u], i * C::NG + g), acc[i], z[u][i]);
-        z[u][i] = fmaf(half_at<C::ACT16>(r.kb[u], i * C::NG + g), w.qsum[g], z[u][i]);
-      }
+    for (int k = 0; k < C::G / 4; ++k) {
+      qv[g][k] = have ? half_at<C::ACT16>(raw[g], k) : 0.f;
+      mx = fmaxf(mx, fabsf(qv[g][k]));
     }
+  mx = quads_max(mx);
+  // the largest entry to [2^14, 2^15), with the sign of the scale
+  int e = 0;
+  if (mx > 0.f && mx < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(mx) + 1;
+  const float sign = scale < 0.f ? -1.f : 1.f;
+  w.qsum = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[u][i] *= w.zscale;
+  for (int g = 0; g < C::NG; ++g) {
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      uint32_t reg[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float lo = sign * __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 0)], e);
+        const float hi = sign * __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 1)], e);
+        const float f = 1.f / (float)(1 << key_shift<C>(r));
+        reg[r] = (uint32_t)f32_to_f16_bits(lo * f) | (uint32_t)f32_to_f16_bits(hi * f) << 16;
+        sum += lo + hi;
+      }
+      w.q[g][s] = as_f16x8(reg[0], reg[1], reg[2], reg[3]);
+    }
+    // Q_g in the units of the products of codes, cut into 16-bit pieces: quarter 0 holds the leading one
+    float left = quads_sum(sum) * 0x1p-24f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint16_t piece = f32_to_act_bits(left, C::ACT16);
+      if (kq == k) w.qsum[g / 2] |= (uint32_t)piece << (16 * (g & 1));
+      left -= C::ACT16 ? f16_bits_to_f32(piece) : bf16_bits_to_f32(piece);
+    }
   }
-  if (edge) {  // uniform
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!(live >> (4 * u + i) & 1u)) z[u][i] = -__builtin_inff();
-  }
-  float vs[2][4][C::NG], vmax = 0.f;
+  w.zscale = __builtin_amdgcn_ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e);
+}
+
+// New references for the heads of this wave, and everything summed so far
+// brought to them.
+template <class C>
+__device__ __forceinline__ void rescale(Wave<C>& w, const uint32_t (&vs)[2][C::SW], float zmax) {
+  float vm = 0.f;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::SW; ++i) {
+      // (opaque: shared with the unpacking after the branch, these would put a second side to it)
+      uint32_t word = vs[u][i];
+      asm("" : "+v"(word));
 #pragma unroll
-      for (int g = 0; g < C::NG; ++g) {
-        float v = half_at<C::ACT16>(r.vs[u], i * C::NG + g);
-        if (edge && !(live >> (4 * u + i) & 1u)) v = 0.f;
-        vs[u][i][g] = v;
-        vmax = fmaxf(vmax, fabsf(v));
+      for (int k = 0; k < 2; ++k) {
+        const float v = fabsf(half_at<C::ACT16>(&word, k));
+        vm = fmaxf(vm, v < __builtin_inff() ? v : 0.f);  // (one that is not finite makes its own columns so)
       }
-  float zmax = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
-                     fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
-  if (__builtin_amdgcn_ballot_w64(zmax > w.mlim || vmax > w.vlim)) {  // uniform: new references
-    const float m = fmaxf(w.mref, quads_max(zmax));
-    // the exponent of the largest scale, kept where 2^(5 - mu) and its sums stay finite
-    const float vm = quads_max(vmax);
-    const float e = fmaxf(w.vexp, fminf(fmaxf((float)((int)(__float_as_uint(vm) >> 23) - 127), -90.f), 110.f));
-    const float mu = (m == -__builtin_inff() ? 0.f : m) + e;
-    const float alpha = w.mref == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(w.mu - mu);
-    w.mref = m;
-    w.mu = mu;
-    w.mlim = m + MROOM;
-    w.vexp = e;
-    w.vlim = __builtin_amdgcn_ldexpf(VROOM, (int)e);
-    w.l *= alpha;
+    }
+  vm = quads_max(vm);
+  const float m = fmaxf(w.mref, quads_max(zmax));
+  // the exponent of the largest scale, kept where 2^(5 - mu) and its sums stay finite
+  const float e = fmaxf(w.vexp, fminf(fmaxf((float)((int)(__float_as_uint(vm) >> 23) - 127), -90.f), 110.f));
+  const float mu = (m == -__builtin_inff() ? 0.f : m) + e;
+  const float alpha = w.mref == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(w.mu - mu);
+  w.mref = m;
+  w.mu = mu;
+  w.mlim = m + MROOM;
+  w.vexp = e;
+  const float lim = __builtin_amdgcn_ldexpf(1.f, (int)e + VROOM);
+  w.vlim = C::ACT16 ? (lim < 65504.f ? f32_to_f16_bits(lim) : 0x7bffu) : __float_as_uint(lim) >> 16;
+  w.l *= alpha;
+#pragma unroll
+  for (int g = 0; g < C::NG; ++g) {
+    w.bias[g] *= alpha;
+#pragma unroll
+    for (int c = 0; c < C::VC; ++c) w.o[g][c] *= alpha;
+  }
+}
+
+// Lane offsets into a stage: codes by group, parameters.
+template <class C>
+struct Lanes {
+  uint32_t k[C::NG][C::KB > 16 ? 2 : 1], v[C::NG], par, kb;
+};
+
+// 32 tokens from a stage in LDS.  tok: each half's first token; -1: no such
+// tile, or its page lies outside the cache.  edge (uniform): some of the 32
+// do not count.
+template <class C>
+__device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<C>& ln, const int (&tok)[2], bool edge,
+                                     int first, int end, int lane) {
+  // every read of the stage first
+  uint32_t kc[2][C::NG][C::KW], kbw[2][C::BW], ks[2][C::SW], vs[2][C::SW], vb[2][C::SW], vc[2][4][C::NG][C::VW];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* par = st + 4 * C::CODES + u * 4 * C::PARAMS;
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
-      w.bias[g] *= alpha;
+      load_bytes<(C::KB > 16 ? 16 : C::KB)>(st + u * C::CODES + ln.k[g][0], kc[u][g]);
+      if constexpr (C::KB > 16) load_bytes<16>(st + u * C::CODES + ln.k[g][1], kc[u][g] + 4);
+    }
+    load_bytes<2 * C::NG>(par + C::PARAMS + ln.kb, kbw[u]);
+    load_bytes<8 * C::NG>(par + ln.par, ks[u]);
+  }
 #pragma unroll
-      for (int c = 0; c < C::VC; ++c) w.o[g][c] *= alpha;
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* par = st + 4 * C::CODES + (u * 4 + 2) * C::PARAMS + ln.par;
+    load_bytes<8 * C::NG>(par, vs[u]);
+    load_bytes<8 * C::NG>(par + C::PARAMS, vb[u]);
+#pragma unroll
+    for (int g = 0; g < C::NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_bytes<(C::VBITS < 8 ? 1 : C::VBITS / 8)>(st + (2 + u) * C::CODES + i * C::ROWB + ln.v[g], vc[u][i][g]);
+  }
+  float z[2][4], p[2][4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    u32x4_t kb = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < C::BW; ++i) kb[i] = kbw[u][i];
+    const f32x4_t zb = mfma_act<C::ACT16>(kb, w.qsum, f32x4_t{0.f, 0.f, 0.f, 0.f});
+    f32x4_t acc[C::NG];
+#pragma unroll
+    for (int g = 0; g < C::NG; ++g) {
+      acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s)
+        acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_codes<C>(kc[u][g], s), w.q[g][s], acc[g], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[u][i] = zb[i];
+#pragma unroll
+      for (int g = 0; g < C::NG; ++g) z[u][i] = fmaf(half_at<C::ACT16>(ks[u], i * C::NG + g), acc[g][i], z[u][i]);
     }
   }
+  if (edge) {  // tokens that do not count get p = 0 and finite parameters
+    int kq = lane >> 4;
+    asm volatile("" : "+v"(kq));  // (keeps the comparisons below inside the branch)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = tok[u] + 4 * kq + i;
+        if (tok[u] < 0 || t < first || t >= end) {
+          z[u][i] = -__builtin_inff();
+#pragma unroll
+          for (int g = 0; g < C::NG; ++g) {
+            const int k = i * C::NG + g;
+            vs[u][k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
+            vb[u][k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
+          }
+        }
+      }
+  }
+  const float zmax = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
+                           fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3]))) * w.zscale;
+  uint32_t vmax = vs[0][0];
+#pragma unroll
+  for (int i = 1; i < 2 * C::SW; ++i) vmax = pk_max_u16(vmax, vs[i / C::SW][i % C::SW]);
+  vmax = max(vmax >> 16, vmax & 0xffffu);  // (a scale below zero has its top bit set and passes every limit)
+  const uint64_t pass = __builtin_amdgcn_ballot_w64(zmax > w.mlim || vmax > w.vlim);
+  uint32_t any = (uint32_t)pass | (uint32_t)(pass >> 32);
+  asm volatile("" : "+s"(any));
+  if (any) rescale<C>(w, vs, zmax);
   const float off = PBIAS - w.mu;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[u][i] = __builtin_amdgcn_exp2f(z[u][i] + off);
+      p[u][i] = __builtin_amdgcn_exp2f(fmaf(z[u][i], w.zscale, off));
       w.l += p[u][i];
 #pragma unroll
-      for (int g = 0; g < C::NG; ++g) {
-        float b = half_at<C::ACT16>(r.vb[u], i * C::NG + g);
-        if (edge && !(live >> (4 * u + i) & 1u)) b = 0.f;
-        w.bias[g] = fmaf(p[u][i], b, w.bias[g]);
-      }
+      for (int g = 0; g < C::NG; ++g)
+        w.bias[g] = fmaf(p[u][i], half_at<C::ACT16>(vb[u], i * C::NG + g), w.bias[g]);
     }
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
@@ -297,8 +474,8 @@ __device__ __forceinline__ void step(Wave<C>& w, const Raw<C>& r, bool edge, uin
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int u = k >> 1, i = 2 * (k & 1);
-      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-      const h2 h = {(_Float16)(p[u][i] * vs[u][i][g]), (_Float16)(p[u][i + 1] * vs[u][i + 1][g])};
+      const f16x2_t h = {(_Float16)(p[u][i] * half_at<C::ACT16>(vs[u], i * C::NG + g)),
+                         (_Float16)(p[u][i + 1] * half_at<C::ACT16>(vs[u], (i + 1) * C::NG + g))};
       aw[k] = __builtin_bit_cast(uint32_t, h);
     }
     const f16x8_t A = as_f16x8(aw[0], aw[1], aw[2], aw[3]);
@@ -307,16 +484,11 @@ __device__ __forceinline__ void step(Wave<C>& w, const Raw<C>& r, bool edge, uin
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int u = k >> 1, i = 2 * (k & 1);
-      const uint32_t* x = r.vc[u][i][g];
-      const uint32_t* y = r.vc[u][i + 1][g];
+      const uint32_t* x = vc[u][i][g];
+      const uint32_t* y = vc[u][i + 1][g];
 #pragma unroll
-      for (int b = 0; b < PIECES; ++b) {
-        if constexpr (C::VBITS <= 16)
-          pr[b][k] = x[0] | y[0] << 16;
-        else
-          pr[b][k] = (b & 1) ? __builtin_amdgcn_perm(y[b / 2], x[b / 2], 0x07060302u)
-                             : __builtin_amdgcn_perm(y[b / 2], x[b / 2], 0x05040100u);
-      }
+      for (int b = 0; b < PIECES; ++b)
+        pr[b][k] = __builtin_amdgcn_perm(y[b / 2], x[b / 2], (b & 1) ? 0x07060302u : 0x05040100u);
       // two lanes share a byte of 2-bit codes where a group gives a lane two columns
       if constexpr (C::VBITS == 4) pr[0][k] >>= 4 * (lane & 1);
     }
@@ -331,154 +503,121 @@ __device__ __forceinline__ void step(Wave<C>& w, const Raw<C>& r, bool edge, uin
   }
 }
 
-__device__ __forceinline__ int span_of(const PagedAttnArgs& a, int b, int& first, int& len) {
+// What starting a unit costs a workgroup, in tiles (without it, a workgroup
+// that a ragged batch gives many short units is the last: 64 sequences up to
+// 8192 tokens, 4-bit, 90 us at 0, 75 at 2, 70 at 3; equal lengths the same).
+constexpr int START = 2;
+
+// Tokens [first, len) of sequence b; returns its tiles of 128 tokens from the
+// 16-token tile of `first` on, at least one.
+__device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, int b, int& first, int& len) {
   len = (int)max(0l, min((long)a.seq_lens[b], (long)a.max_pages * a.c.page_size));
   first = a.window > 0 ? (int)max(0l, (long)len - a.window) : 0;
-  return len - (first & ~15);
+  return max(1, (int)(((long)len - (first & ~15) + 127) >> 7));
+}
+
+__device__ __forceinline__ uint32_t quotient(uint64_t n, uint32_t d) {
+  return (n >> 32) == 0 ? (uint32_t)n / d : (uint32_t)(n / d);
 }
 
 // inclusive sum over the 64 lanes
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int t = __shfl_up(v, o);
-    if (lane >= o) v += t;
-  }
-  return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int scan_step(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = scan_step<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
+  v = scan_step<0x112, 0xf>(v);
+  v = scan_step<0x114, 0xf>(v);
+  v = scan_step<0x118, 0xf>(v);
+  v = scan_step<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
+  return scan_step<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
 }
 
-struct Place {  // a workgroup's chunk
-  int b, c, n, slot0;
+// The work of all (sequence, unit of heads), in that order, on one line: each
+// unit's START and then its tiles.  Where point x of it lies.
+struct Place {
+  int b, unit, at;
+  int tiles, first, len;  // of the sequence
+  int64_t start;          // its start on the line of one unit
 };
 
-// Finds chunk `x` of the batch: sequence b is cut into n_b chunks of
-// max(1, ceil(span / chunk)), chunk sized so that about `target` units cover
-// everything.  False when there is no such chunk.
-__device__ __forceinline__ bool find_chunk(const AttnWork& w, int x, int units_per_chunk, Place* out, int* sh) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, B = (int)w.a.B;
-  int first, len, span0 = 0;
-  long total = 0;
-  for (int b0 = 0; b0 < B; b0 += 256) {
-    const int s = b0 + t < B ? span_of(w.a, b0 + t, first, len) : 0;
-    if (b0 == 0) span0 = s;
-    total += s;
-  }
-  long* lsh = reinterpret_cast<long*>(sh);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
-  if (lane == 0) lsh[wave] = total;
-  __syncthreads();
-  total = (lsh[0] + lsh[1]) + (lsh[2] + lsh[3]);
-  __syncthreads();
-  const long want = (total * units_per_chunk + w.target - 1) / w.target;
-  const int chunk = (int)min(max((want + 127) & ~127l, (long)w.min_chunk), (long)(1 << 30));
-  int base = 0, sbase = 0;
-  if (t == 0) sh[12] = 0;
-  for (int b0 = 0; b0 < B; b0 += 256) {
-    const bool in = b0 + t < B;
-    const int s = b0 == 0 ? span0 : (in ? span_of(w.a, b0 + t, first, len) : 0);
-    const int n = in ? max(1, (int)(((long)s + chunk - 1) / chunk)) : 0, m = n > 1 ? n : 0;
-    const int in_n = wave_scan(n, lane), in_m = wave_scan(m, lane);
-    __syncthreads();
-    if (lane == 63) {
-      sh[wave] = in_n;
-      sh[4 + wave] = in_m;
-    }
-    __syncthreads();
-    int pn = base, pm = sbase;
-    for (int k = 0; k < wave; ++k) {
-      pn += sh[k];
-      pm += sh[4 + k];
-    }
-    base += (sh[0] + sh[1]) + (sh[2] + sh[3]);
-    sbase += (sh[4] + sh[5]) + (sh[6] + sh[7]);
-    const int at = x - (pn + in_n - n);
-    if (in && at >= 0 && at < n) {
-      sh[8] = b0 + t;
-      sh[9] = at;
-      sh[10] = n;
-      sh[11] = pm + in_m - m;
-      sh[12] = 1;
-    }
-    if (base > x) break;
-  }
-  __syncthreads();
-  out->b = sh[8];
-  out->c = sh[9];
-  out->n = sh[10];
-  out->slot0 = sh[11];
-  return sh[12] != 0;
+// The batch as every wave sees it, a lane a sequence of the 64 at hand.
+struct Batch {
+  int b0, tiles, first, len;  // tiles with START, 0 past the batch
+  int64_t start;              // of sequence b0 on the line of one unit
+};
+
+__device__ __forceinline__ void batch_at(const AttnWork& w, int b0, Batch& s) {
+  const int b = b0 + (int)(threadIdx.x & 63);
+  s.b0 = b0;
+  s.tiles = s.first = s.len = 0;
+  if (b < w.a.B) s.tiles = START + tiles_of(w.a, b, s.first, s.len);
 }
 
+// the line's length for one unit, with the first 64 sequences left at hand: no barrier, and at 64 sequences or fewer, one load
+__device__ __forceinline__ int64_t batch_tiles(const AttnWork& w, Batch& s) {
+  double total = 0.0;
+  for (int b0 = 64; b0 < w.a.B; b0 += 64) {
+    batch_at(w, b0, s);
+    total += s.tiles;
+  }
+  batch_at(w, 0, s);
+  s.start = 0;
+  const uint64_t n = (uint64_t)wave_sum_f64(total + s.tiles);  // (the same in every lane)
+  return (int64_t)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(n >> 32)) << 32 |
+                   __builtin_amdgcn_readfirstlane((uint32_t)n));
+}
+
+// Finds point x, at or past the sequences at hand.
+__device__ __forceinline__ Place find_tile(const AttnWork& w, Batch& s, int64_t x, int units) {
+  Place p;
+  for (;;) {
+    const int upto = wave_scan(s.tiles);
+    const int64_t rel = x - s.start * units;  // (the first lane whose sequences up to it pass it)
+    const uint64_t hit = __builtin_amdgcn_ballot_w64((int64_t)upto * units > rel);
+    if (hit != 0 || s.b0 + 64 >= w.a.B) {
+      const int l = __builtin_ctzll(hit | (uint64_t(1) << 63));
+      p.b = s.b0 + l;
+      const int line = __builtin_amdgcn_readlane(s.tiles, l);
+      p.tiles = line - START;
+      p.first = __builtin_amdgcn_readlane(s.first, l);
+      p.len = __builtin_amdgcn_readlane(s.len, l);
+      p.start = s.start + __builtin_amdgcn_readlane(upto, l) - line;
+      const uint64_t in = (uint64_t)(x - p.start * units);
+      p.unit = (int)quotient(in, (uint32_t)line);
+      p.at = (int)(in - (uint64_t)p.unit * (uint32_t)line);
+      return p;
+    }
+    s.start += __builtin_amdgcn_readlane(upto, 63);
+    batch_at(w, s.b0 + 64, s);
+  }
+}
+
+// Attention of one unit of heads (key head, tile of 16 query heads) of
+// sequence b to its tokens [begin, end) from `first` on, by all waves of the
+// workgroup: written out if that is `whole`, else left as a part in `slot`.
 template <class C>
-__global__ __launch_bounds__(256) void paged_attn_kernel(AttnWork wk) {
+__device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float (&msh)[C::WAVES][16],
+                                       float (&lsh)[C::WAVES][16], int b, int unit, int first, int begin, int end,
+                                       bool whole, size_t slot) {
+  constexpr int WAVES = C::WAVES, TILE = 32 * WAVES;
   const PagedAttnArgs& a = wk.a;
   const KvCache& c = a.c;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int n16 = lane & 15, kq = lane >> 4;
-  extern __shared__ float lds[];  // [WAVES][gm][D + 4]
-  __shared__ __align__(8) int sh[16];
-  __shared__ float msh[WAVES][16], lsh[WAVES][16];
-  const int units_per_chunk = c.kv_heads * wk.htiles;
-  const int x = (int)blockIdx.x / units_per_chunk, rest = (int)blockIdx.x - x * units_per_chunk;
-  const int j = rest / wk.htiles, ht = rest - j * wk.htiles;
-  Place pl;
-  if (!find_chunk(wk, x, units_per_chunk, &pl, sh)) return;
-  const int b = __builtin_amdgcn_readfirstlane(pl.b), ci = __builtin_amdgcn_readfirstlane(pl.c),
-            nchunks = __builtin_amdgcn_readfirstlane(pl.n);
-  if (wk.meta && ci == 0 && rest == 0 && t == 0) wk.meta[b] = make_int2(nchunks, pl.slot0);
-  int first, len;
-  const int span = span_of(a, b, first, len);
-  first = __builtin_amdgcn_readfirstlane(first);
-  len = __builtin_amdgcn_readfirstlane(len);
-  const int csize = (((span + nchunks - 1) / nchunks) + 127) & ~127;
-  const int begin = __builtin_amdgcn_readfirstlane((first & ~15) + ci * csize);
-  const int end = __builtin_amdgcn_readfirstlane(min(begin + csize, len));
-  const int h0 = j * wk.share + 16 * ht, gm = min(16, wk.share - 16 * ht);  // this tile's heads
+  float* lds = reinterpret_cast<float*>(smem);
+  const int j = unit / wk.htiles, ht = unit - j * wk.htiles;
+  const int h0 = j * wk.share + 16 * ht, gm = min(16, wk.share - 16 * ht);  // this unit's heads
 
-  Wave<C> w;
   // q: lane (head n16, quarter kq) holds columns [kq G/4, (kq+1) G/4) of each group
+  uint32_t qraw[C::NG][C::G / 8];
   {
-    float qv[C::NG][C::G / 4], mx = 0.f;
-    const uint16_t* q = (const uint16_t*)a.q + (long)b * a.qts + (long)(h0 + n16) * a.qhs;
-    const bool have = n16 < gm;
+    const uint16_t* q = (const uint16_t*)a.q + (long)b * a.qts + (long)(h0 + min(n16, gm - 1)) * a.qhs;
 #pragma unroll
-    for (int g = 0; g < C::NG; ++g)
-#pragma unroll
-      for (int e = 0; e < C::G / 32; ++e) {
-        uint32_t raw[4] = {0u, 0u, 0u, 0u};
-        if (have) load_bytes<16>((const uint8_t*)(q + g * C::G + kq * (C::G / 4) + 8 * e), raw);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float v = half_at<C::ACT16>(raw, k);
-          qv[g][8 * e + k] = v;
-          mx = fmaxf(mx, fabsf(v));
-        }
-      }
-    mx = quads_max(mx);
-    // the largest entry to [2^14, 2^15)
-    int e = 0;
-    if (mx > 0.f && mx < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(mx) + 1;
-#pragma unroll
-    for (int g = 0; g < C::NG; ++g) {
-      float sum = 0.f;
-#pragma unroll
-      for (int s = 0; s < C::KS; ++s) {
-        uint32_t reg[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float lo = __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 0)], e);
-          const float hi = __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 1)], e);
-          const float f = 1.f / (float)(1 << key_shift<C>(r));
-          reg[r] = (uint32_t)f32_to_f16_bits(lo * f) | (uint32_t)f32_to_f16_bits(hi * f) << 16;
-          sum += lo + hi;
-        }
-        w.q[g][s] = as_f16x8(reg[0], reg[1], reg[2], reg[3]);
-      }
-      w.qsum[g] = quads_sum(sum) * 0x1p-24f;
-    }
-    w.zscale = __builtin_amdgcn_ldexpf(a.scale * 1.4426950408889634f, 24 - e);
+    for (int g = 0; g < C::NG; ++g) load_bytes<C::G / 2>((const uint8_t*)(q + g * C::G + kq * (C::G / 4)), qraw[g]);
   }
+  Wave<C> w;
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
     w.bias[g] = 0.f;
@@ -489,56 +628,104 @@ __global__ __launch_bounds__(256) void paged_attn_kernel(AttnWork wk) {
   w.mref = w.mlim = -__builtin_inff();
   w.mu = 0.f;
   w.vexp = -90.f;
-  w.vlim = 0.f;
+  w.vlim = 0u;
 
-  // this wave's steps: tokens begin + 32 (wave + 4 i)
+  // this wave's steps: tokens begin + 32 (wave + WAVES i)
   const int t0 = begin + 32 * wave;
-  const int steps = t0 < end ? (end - t0 + 127) >> 7 : 0;
+  const int steps = t0 < end ? (end - t0 + TILE - 1) / TILE : 0;
   if (steps > 0) {
-    const uint32_t kvo = (uint32_t)(n16 * C::ROWB + kq * C::KB);
-    const uint32_t vvo = (uint32_t)(4 * kq * C::ROWB + n16 * C::VBITS / 8);
-    const uint32_t svo = (uint32_t)(4 * kq * 2 * C::NG);
     const int32_t* table = a.table + (long)b * a.table_stride;
-    int ids = -1, ids_from = -32;  // lane k: the page of 16-token tile k of 32 steps; -1: none
-    auto load = [&](Raw<C>& r, int i, uint32_t& live) {
-      if (i >= ids_from + 32) {  // uniform
-        ids_from = i;
-        const int tok = t0 + 128 * (i + (lane >> 1)) + 16 * (lane & 1);
-        ids = -1;
-        if (tok < end) {
-          ids = table[wk.page.div((uint32_t)tok)];
-          if ((uint32_t)ids >= (uint32_t)c.num_pages) ids = -1;
-        }
+    // lane k: where 16-token tile k of 32 steps lies, in tiles of the cache's rows; -1: no such tile, or its page is outside
+    int at = -1, at_from = -32;
+    Lanes<C> ln;
+#pragma unroll
+    for (int g = 0; g < C::NG; ++g) {
+      const int col = g * (C::G * C::BITS / 8);
+      ln.k[g][0] = (uint32_t)C::at(n16, col + kq * C::KB);
+      if constexpr (C::KB > 16) ln.k[g][1] = (uint32_t)C::at(n16, col + kq * C::KB + 16);
+      ln.v[g] = (uint32_t)C::at(4 * kq, col + n16 * C::VBITS / 8);
+    }
+    ln.par = (uint32_t)(4 * kq * 2 * C::NG);
+    ln.kb = (uint32_t)(n16 * 2 * C::NG);
+    // what this lane copies: 16-byte piece 64 m + lane of 16 tokens' codes, and of a stage's parameters
+    uint32_t src[C::COPIES];
+#pragma unroll
+    for (int m = 0; m < C::COPIES; ++m) {
+      const int q = 64 * m + lane;
+      if constexpr (C::PIECES > 0) {
+        const int row = q / C::PIECES;
+        src[m] = (uint32_t)(row * C::ROWB + ((q % C::PIECES ^ C::swizzle(row)) << 4));
+      } else {
+        src[m] = (uint32_t)(16 * q);
       }
-      live = 0;
+    }
+    const uint8_t* psrc[C::PCOPIES];
+    bool phalf[C::PCOPIES];
+#pragma unroll
+    for (int m = 0; m < C::PCOPIES; ++m) {
+      const int q = 64 * m + lane, part = q / (2 * C::NG);  // part = 4 half + kind
+      const void* const kind[4] = {c.k_scales, c.k_biases, c.v_scales, c.v_biases};
+      psrc[m] = (const uint8_t*)((part & 2) ? ((part & 1) ? kind[3] : kind[2]) : ((part & 1) ? kind[1] : kind[0])) +
+                16 * (q % (2 * C::NG));
+      phalf[m] = part >= 4;
+    }
+    const uint32_t ring = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem + wave * C::STAGES * C::STAGE);
+    auto copy = [&](int i, uint32_t dst) {  // stage i of this wave (page 0 in the place of one outside the cache)
+      if (i >= at_from + 32) {  // uniform
+        at_from = i;
+        const int tok = t0 + TILE * (i + (lane >> 1)) + 16 * (lane & 1);
+        const uint32_t tk = (uint32_t)min(tok, end - 1) & ~15u, pg = wk.page.div(tk);
+        const int id = table[pg];
+        const uint32_t tiles = (uint32_t)c.page_size >> 4;  // (fewer than 2^31 in any memory)
+        at = tok < end && (uint32_t)id < (uint32_t)c.num_pages
+                 ? (int)(((uint32_t)id * (uint32_t)c.kv_heads + (uint32_t)j) * tiles + ((tk - pg * wk.page.d) >> 4))
+                 : -1;
+      }
+      uint32_t row[2];  // in tiles
+#pragma unroll
+      for (int u = 0; u < 2; ++u) row[u] = (uint32_t)max(__builtin_amdgcn_readlane(at, 2 * (i - at_from) + u), 0);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint8_t* base = (const uint8_t*)(p < 2 ? c.k_packed : c.v_packed) + (size_t)row[p & 1] * C::CODES;
+        copies<C::CODES / 16>([&](auto m, auto lanes) {
+          copy_to_lds<decltype(lanes)::value>(base, src[decltype(m)::value], dst + p * C::CODES + 1024 * decltype(m)::value);
+        });
+      }
+      copies<8 * C::PARAMS / 16>([&](auto m, auto lanes) {
+        constexpr int M = decltype(m)::value;
+        copy_to_lds<decltype(lanes)::value>(psrc[M] + (size_t)(phalf[M] ? row[1] : row[0]) * C::PARAMS,
+                                            dst + 4 * C::CODES + 1024 * M);
+      });
+    };
+    copy(0, ring);
+    set_q<C>(w, qraw, n16 < gm, kq, a.scale);
+    // the tiles of the stage being computed: the copies run ahead and may have gone on to the next 32 steps'
+    int at_now = at, at_now_from = 0;
+    uint32_t buf = 0;
+    for (int i = 0; i < steps; ++i) {
+      wait_copies();  // stage i is in LDS
+      if (i == at_now_from + 32) {
+        at_now = at;
+        at_now_from = at_from;
+      }
+      // the reads of stage i - 1, whose place the next copies take, are done
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (i + 1 < steps) copy(i + 1, ring + (buf ^ C::STAGE));
+      int tok[2];
+      bool edge = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int tok = t0 + 128 * i + 16 * u;
-        const int id = __builtin_amdgcn_readlane(ids, 2 * (i - ids_from) + u);
-        const uint32_t off = id < 0 ? 0u : (uint32_t)tok - wk.page.div((uint32_t)tok) * wk.page.d;
-        const size_t row = ((size_t)(id < 0 ? 0 : id) * c.kv_heads + j) * c.page_size + off;
-        load_raw<C>(r, u, c, row, kvo, vvo, svo);
-        if (id >= 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int tk = tok + 4 * kq + k;
-            if (tk >= first && tk < end) live |= 1u << (4 * u + k);
-          }
-        }
+        const int t = t0 + TILE * i + 16 * u;
+        const bool there = __builtin_amdgcn_readlane(at_now, 2 * (i - at_now_from) + u) >= 0;
+        tok[u] = there ? t : -1;
+        edge |= !there || t < first || t + 16 > end;
       }
-    };
-    Raw<C> r0, r1;
-    uint32_t live0, live1;
-    load(r0, 0, live0);
-    for (int i = 0;;) {
-      load(r1, i + 1, live1);
-      step<C>(w, r0, __builtin_amdgcn_ballot_w64(live0 != 0xffu) != 0, live0, lane);
-      if (++i == steps) break;
-      load(r0, i + 1, live0);
-      step<C>(w, r1, __builtin_amdgcn_ballot_w64(live1 != 0xffu) != 0, live1, lane);
-      if (++i == steps) break;
+      step<C>(w, smem + wave * C::STAGES * C::STAGE + buf, ln, tok, edge, first, end, lane);
+      buf ^= C::STAGE;
     }
   }
+  __syncthreads();
   // join the waves
   w.l = quads_sum(w.l);
   const float m_own = (w.mref == -__builtin_inff() && w.l == w.l) ? -__builtin_inff() : w.mu;
@@ -560,10 +747,8 @@ __global__ __launch_bounds__(256) void paged_attn_kernel(AttnWork wk) {
     }
   }
   __syncthreads();
-  const bool whole = nchunks == 1;
-  const size_t slot = ((size_t)(pl.slot0 + ci) * c.kv_heads + j) * wk.htiles + ht;
   const int gstore = min(16, wk.share);
-  for (int i = t; i < gm * (C::D / 4); i += 256) {
+  for (int i = t; i < gm * (C::D / 4); i += 64 * WAVES) {
     const int h = i / (C::D / 4), d4 = i - h * (C::D / 4);
     float m = msh[0][h];
 #pragma unroll
@@ -596,91 +781,170 @@ __global__ __launch_bounds__(256) void paged_attn_kernel(AttnWork wk) {
   }
 }
 
+// Every workgroup takes an equal stretch of the line of all units' work: whole
+// units, and at its ends parts of units that it shares with its neighbours.
+// The lengths are on the device, so each finds its own from them.
+template <class C>
+__global__ __launch_bounds__(256, C::PER_CU) void paged_attn_kernel(AttnWork wk) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ float msh[C::WAVES][16], lsh[C::WAVES][16];
+  const PagedAttnArgs& a = wk.a;
+  const int units = a.c.kv_heads * wk.htiles;
+  Batch batch;
+  const int64_t all = batch_tiles(wk, batch) * units;
+  const int64_t share = (all + gridDim.x - 1) / gridDim.x;
+  const int64_t xend = min(share * (blockIdx.x + 1), all);
+  if (blockIdx.x == 0 && threadIdx.x == 0) wk.meta[a.B].tiles = (int)min(share, (int64_t)(1 << 30));
+  for (int64_t x = share * blockIdx.x; x < xend;) {
+    const Place p = find_tile(wk, batch, x, units);
+    const int take = (int)min((int64_t)(START + p.tiles - p.at), xend - x);
+    if (p.unit == 0 && p.at == 0 && threadIdx.x == 0) wk.meta[p.b] = AttnMeta{p.start, p.tiles};
+    const int tile = max(p.at - START, 0), tend = p.at + take - START;
+    if (tend > tile) {  // uniform
+      const int begin = (p.first & ~15) + 128 * tile;
+      // a part that is not its unit's first is its workgroup's first
+      attend<C>(wk, smem, msh, lsh, p.b, p.unit, p.first, begin, min((p.first & ~15) + 128 * tend, p.len),
+                tend - tile == p.tiles, 2 * (size_t)blockIdx.x + (tile == 0));
+    }
+    x += take;
+    if (x < xend) __syncthreads();
+  }
+}
+
+// One workgroup per sequence and unit: short tables, no parts, one launch.
+template <class C>
+__global__ __launch_bounds__(64 * C::WAVES, C::WAVES == 4 ? C::PER_CU : 1) void paged_attn_short_kernel(AttnWork wk) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ float msh[C::WAVES][16], lsh[C::WAVES][16];
+  const int units = wk.a.c.kv_heads * wk.htiles;
+  const int b = (int)blockIdx.x / units;
+  int first, len;
+  tiles_of(wk.a, b, first, len);
+  first = __builtin_amdgcn_readfirstlane(first);
+  len = __builtin_amdgcn_readfirstlane(len);
+  attend<C>(wk, smem, msh, lsh, b, (int)blockIdx.x - b * units, first, first & ~15, len, true, 0);
+}
+
 // Joins the chunks of one sequence and head: 32 lanes by eight groups of chunks.
 template <bool F16_>
 __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   const PagedAttnArgs& a = wk.a;
   const int b = blockIdx.y, head = blockIdx.x, t = threadIdx.x, D = a.c.head_dim;
-  const int2 mt = wk.meta[b];
-  if (mt.x <= 1) return;
+  const AttnMeta mt = wk.meta[b];
+  const uint32_t share = (uint32_t)wk.meta[a.B].tiles;
   const int j = head / wk.share, ht = (head - j * wk.share) / 16, h = head - j * wk.share - 16 * ht;
   const int gstore = min(16, wk.share);
-  __shared__ float msh[4], osh[8][256 + 4], lsh[8];
-  auto at = [&](int k) { return ((((size_t)(mt.y + k) * a.c.kv_heads + j) * wk.htiles + ht) * gstore + h); };
-  float m = -__builtin_inff();
-  for (int k = t; k < mt.x; k += 256) m = fmaxf(m, wk.part_ml[2 * at(k)]);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((t & 63) == 0) msh[t >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(msh[0], msh[1]), fmaxf(msh[2], msh[3]));
+  __shared__ float msh[8], osh[8][256 + 4], lsh[8];
+  // the workgroups of this unit's first and last tile
+  const uint64_t x0 = (uint64_t)mt.start * (a.c.kv_heads * wk.htiles) +
+                      (uint64_t)(j * wk.htiles + ht) * (START + mt.tiles) + START;
+  const uint32_t w0 = quotient(x0, share), w1 = quotient(x0 + mt.tiles - 1, share);
+  if (w0 == w1) return;
+  const int n = (int)(w1 - w0) + 1;
+  auto at = [&](int k) { return (2 * (size_t)(w0 + k) + (k == 0)) * gstore + h; };
   const int grp = t >> 5, ln = t & 31;
   f32x4_t o[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-  float l = 0.f;
-  for (int k = grp; k < mt.x; k += 8) {
-    const size_t s = at(k);
-    const float mk = wk.part_ml[2 * s];
-    const float f = mk == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(mk - m);
-    l = fmaf(f, wk.part_ml[2 * s + 1], l);
+  float m = -__builtin_inff(), l = 0.f;
+  for (int k0 = grp; k0 < n; k0 += 8 * 4) {  // four parts' loads in flight
+    f32x2_t ml[4];
+    f32x4_t v[4][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (4 * ln + 128 * e < D) {
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(wk.part_o + s * D + 4 * ln + 128 * e);
+    for (int i = 0; i < 4; ++i) {
+      const size_t s = at(min(k0 + 8 * i, n - 1));
+      ml[i] = *reinterpret_cast<const f32x2_t*>(wk.part_ml + 2 * s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[e][i] = fmaf(f, v[i], o[e][i]);
-      }
+      for (int e = 0; e < 2; ++e)
+        if (4 * ln + 128 * e < D) v[i][e] = *reinterpret_cast<const f32x4_t*>(wk.part_o + s * D + 4 * ln + 128 * e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + 8 * i >= n || ml[i][0] == -__builtin_inff()) continue;  // (a part that saw nothing)
+      const float mn = fmaxf(m, ml[i][0]);
+      const float fo = __builtin_amdgcn_exp2f(m - mn), fn = __builtin_amdgcn_exp2f(ml[i][0] - mn);
+      m = mn;
+      l = l * fo + ml[i][1] * fn;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (4 * ln + 128 * e < D)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[e][c] = o[e][c] * fo + v[i][e][c] * fn;
+    }
   }
 #pragma unroll
   for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4_t*>(&osh[grp][4 * ln + 128 * e]) = o[e];
-  if (ln == 0) lsh[grp] = l;
+  if (ln == 0) {
+    msh[grp] = m;
+    lsh[grp] = l;
+  }
   __syncthreads();
   if (t < D) {
+    m = msh[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) m = fmaxf(m, msh[k]);
     float s = 0.f, ls = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      s += osh[k][t];
-      ls += lsh[k];
+      const float f = msh[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(msh[k] - m);
+      s = fmaf(f, osh[k][t], s);
+      ls = fmaf(f, lsh[k], ls);
     }
     ((uint16_t*)a.out)[((size_t)b * a.heads + head) * D + t] = f32_to_act_bits(ls == 0.f ? 0.f : s / ls, F16_);
   }
 }
 
+// LDS of a launch: the ring, and after the loop [WAVES][heads][D + 4] floats
 template <class C>
+size_t attn_lds(int heads) {
+  return std::max<size_t>(C::LDS, (size_t)C::WAVES * heads * (C::D + 4) * 4);
+}
+
+template <int D, int G, int BITS, bool F16_>
 hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
+  using C = Cfg<D, G, BITS, F16_, 4>;
+  // eight waves where their stages fit
+  using S = Cfg<D, G, BITS, F16_, (Cfg<D, G, BITS, F16_, 8>::LDS <= 155 * 1024 ? 8 : 4)>;
   const PagedAttnArgs& a = w.a;
-  const void* fn = reinterpret_cast<const void*>(&paged_attn_kernel<C>);
   const int gm = w.share < 16 ? w.share : 16;
-  const size_t lds = (size_t)WAVES * gm * (C::D + 4) * 4;
-  int64_t resident = 0;
-  hipError_t e = resident_workgroups(fn, 256, lds, 8, &resident);
-  if (e != hipSuccess) return e;
   const int64_t units = (int64_t)a.c.kv_heads * w.htiles;
-  w.target = (int)resident;
-  w.min_chunk = 128;
-  const int64_t grid = w.target + units * a.B;
-  if (grid >= (int64_t(1) << 31)) return hipErrorNotSupported;
-  const bool split = (int64_t)a.max_pages * a.c.page_size > w.min_chunk;
+  // the most tokens a sequence can see, with the rest of the window's first 16-token tile
+  const int64_t table = (int64_t)a.max_pages * a.c.page_size;
+  const int64_t tokens = a.window > 0 ? std::min(table, a.window + 15) : table;
   w.part_o = w.part_ml = nullptr;
   w.meta = nullptr;
-  if (split) {
-    // a sequence of more than one chunk has at most 2 span / chunk of them
-    const size_t slots = 2 * (size_t)w.target + 2 * units;
-    const size_t meta = ((size_t)a.B * sizeof(int2) + 255) & ~size_t(255);
-    const size_t ml = (slots * gm * 2 * sizeof(float) + 255) & ~size_t(255);
-    void* p = nullptr;
-    e = stream_workspace(s, meta + ml + slots * gm * C::D * sizeof(float), &p);
-    if (e != hipSuccess) return e;
-    w.meta = static_cast<int2*>(p);
-    w.part_ml = reinterpret_cast<float*>(static_cast<char*>(p) + meta);
-    w.part_o = reinterpret_cast<float*>(static_cast<char*>(p) + meta + ml);
+  // Short sequences: a workgroup each, no parts, no second kernel.  Up to
+  // 1024 tokens (one sequence of 1024, 4-bit, D = 128: 10.8 against 9.9 us;
+  // 32 of them: 13 against 19), up to 2048 when there is a workgroup for half
+  // the CUs (16 sequences by 8 key heads: 17.9 against 18.5; 32: 21 against
+  // 25).  Eight waves share one, four when there are more than the CUs
+  // (128 sequences of 512 tokens: 24.5 against 32 us).
+  const int64_t wgs = units * a.B;
+  if (tokens <= 1024 || (tokens <= 2048 && wgs >= 128)) {
+    if (wgs >= (int64_t(1) << 31)) return hipErrorNotSupported;
+    if (wgs > 256)
+      hipLaunchKernelGGL(paged_attn_short_kernel<C>, dim3((unsigned)wgs), dim3(256), attn_lds<C>(gm), s, w);
+    else
+      hipLaunchKernelGGL(paged_attn_short_kernel<S>, dim3((unsigned)wgs), dim3(64 * S::WAVES), attn_lds<S>(gm), s, w);
+    return hipGetLastError();
   }
+  const size_t lds = attn_lds<C>(gm);
+  int64_t resident = 0;
+  hipError_t e = resident_workgroups(reinterpret_cast<const void*>(&paged_attn_kernel<C>), 256, lds, 8, &resident);
+  if (e != hipSuccess) return e;
+  const int64_t grid = std::min(resident, units * a.B * ((tokens + 127) / 128));  // (a workgroup a tile at most)
+  const size_t slots = 2 * (size_t)grid;
+  const size_t meta = ((a.B + 1) * sizeof(AttnMeta) + 255) & ~size_t(255);
+  const size_t ml = (slots * gm * 2 * sizeof(float) + 255) & ~size_t(255);
+  void* p = nullptr;
+  e = stream_workspace(s, meta + ml + slots * gm * D * sizeof(float), &p);
+  if (e != hipSuccess) return e;
+  w.meta = static_cast<AttnMeta*>(p);
+  w.part_ml = reinterpret_cast<float*>(static_cast<char*>(p) + meta);
+  w.part_o = reinterpret_cast<float*>(static_cast<char*>(p) + meta + ml);
   hipLaunchKernelGGL(paged_attn_kernel<C>, dim3((unsigned)grid), dim3(256), lds, s, w);
   e = hipGetLastError();
-  if (e == hipSuccess && split) {
-    hipLaunchKernelGGL(paged_attn_join_kernel<C::ACT16>, dim3((unsigned)a.heads, (unsigned)a.B), dim3(256), 0, s, w);
-    e = hipGetLastError();
-  }
-  return e;
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(paged_attn_join_kernel<F16_>, dim3((unsigned)a.heads, (unsigned)a.B), dim3(256), 0, s, w);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -692,7 +956,7 @@ hipError_t launch_paged_attention_bits(const PagedAttnArgs& a, hipStream_t s) {
   w.htiles = (w.share + 15) / 16;
 #define QAFF_ATTN(D, G)                                                            \
   case D * 1000 + G:                                                               \
-    return a.c.dt == F16 ? launch_cfg<Cfg<D, G, BITS, true>>(w, s) : launch_cfg<Cfg<D, G, BITS, false>>(w, s);
+    return a.c.dt == F16 ? launch_cfg<D, G, BITS, true>(w, s) : launch_cfg<D, G, BITS, false>(w, s);
   switch (a.c.head_dim * 1000 + a.c.G) {
     QAFF_ATTN(64, 32)
     QAFF_ATTN(64, 64)

@@ -87,7 +87,7 @@ def paged_attention(q, k, v, dtype: str, G: int, bits: int, table, lens, scale: 
                 out[b, h] = p @ vv
                 delta = abs(scale) * (4 * np.sqrt(D) * u * ((1024 + kc) * np.abs(ks)) @ np.abs(qf[b, h])
                                       + u * np.abs(qf[b, h]).max() * np.abs(kv_).sum(1)).max()
-                bound[b, h] = (2.0**-11 * (p @ (vs * vc)) + 4 * min(delta, 1.0) * (p @ np.abs(vv))
-                               + 4 * np.sqrt(len(at)) * u * (p @ (vs * (1024 + vc)))
-                               + 2.0**-30 * vs.max() * vc.sum(0))
+                bound[b, h] = (2.0**-11 * (p @ (np.abs(vs) * vc)) + 4 * min(delta, 1.0) * (p @ np.abs(vv))
+                               + 4 * np.sqrt(len(at)) * u * (p @ (np.abs(vs) * (1024 + vc)))
+                               + 2.0**-30 * np.abs(vs).max() * vc.sum(0))
     return out, bound

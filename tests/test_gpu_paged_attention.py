@@ -81,6 +81,38 @@ def test_head_sizes_groups_widths_types(D, G, bits, act):
     _run([70, 5, 161], 6, 2, D, G, bits, 16, act=act, seed=2)
 
 
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 64), (96, 32), (128, 32), (128, 64), (128, 128), (192, 32), (192, 64),
+                                 (256, 32), (256, 64), (256, 128)])
+@pytest.mark.parametrize("bits", [2, 4, 8])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_head_sizes_groups_widths_types_in_parts(D, G, bits, act):
+    # a table of 2560 tokens: sequences cut into parts and joined
+    _run([700, 0, 33, 260], 3, 1, D, G, bits, 16, act=act, seed=30, max_pages=160)
+
+
+@pytest.mark.parametrize("n", [1, 16, 31, 127, 128, 129, 255, 256, 257, 1000, 2559, 2560])
+def test_lengths_in_parts(n):
+    _run([n], 4, 2, 128, 64, 4, 16, seed=31, max_pages=160)
+
+
+@pytest.mark.parametrize("window", [1, 17, 130, 2100, 2400])
+def test_windows_in_parts(window):
+    _run([1, 20, 130, 901, 2500], 4, 2, 64, 32, 8, 16, act="f16", seed=32, window=window, max_pages=160)
+
+
+@pytest.mark.parametrize("heads,kvh", [(17, 1), (40, 1), (33, 11)])
+def test_head_sharing_in_parts(heads, kvh):
+    _run([700, 129], heads, kvh, 64, 64, 4, 32, seed=33, max_pages=80)
+
+
+@pytest.mark.parametrize("B,n", [(70, 200), (300, 90), (20, 1200), (40, 300)])
+def test_batches_at_every_kernel(B, n):
+    # more units than CUs, more sequences than lanes, tables of 1024 tokens, of 2048 and past that
+    lens = np.random.default_rng(34).integers(0, n, B)
+    for pages in (64, 128, 132):
+        _run(list(np.minimum(lens, pages * 16)), 2, 2, 64, 64, 4, 16, seed=34, max_pages=pages)
+
+
 @pytest.mark.parametrize("heads,kvh", [(1, 1), (3, 3), (2, 1), (7, 1), (16, 1), (17, 1), (40, 1), (71, 1), (32, 8), (33, 11)])
 def test_head_sharing(heads, kvh):
     _run([37, 90], heads, kvh, 64, 64, 4, 32, seed=3)
@@ -146,6 +178,18 @@ def test_value_scales_over_many_decades():
     _run([400, 57], 4, 1, 128, 64, 8, 16, seed=14, scale_spread=4.0)
 
 
+def test_scales_below_zero_and_of_zero():
+    # a caller's own cache: flipped groups, constant ones
+    c = Case([200, 31], 4, 1, 128, 64, 4, 16, seed=36)
+    rng = np.random.default_rng(36)
+    for t in (c.k, c.v):
+        t[1][rng.random(t[1].shape) < 0.3] ^= 0x8000
+        t[1][rng.random(t[1].shape) < 0.1] = 0
+    c.check(qa.paged_attention_affine(*c.args()))
+    c.v[1][:] = 0
+    c.check(qa.paged_attention_affine(*c.args()))
+
+
 @pytest.mark.parametrize("pos", ["first", "last"])
 @pytest.mark.parametrize("n", [1, 16, 31, 64, 129, 700])
 def test_the_outermost_tokens_count(pos, n):
@@ -165,9 +209,10 @@ def test_the_outermost_tokens_count(pos, n):
 
 
 @pytest.mark.parametrize("poison", [float("nan"), float("inf"), -3e38])
-def test_slots_that_no_sequence_sees_have_no_influence(poison):
+@pytest.mark.parametrize("pages", [6, 160])
+def test_slots_that_no_sequence_sees_have_no_influence(poison, pages):
     # past the length in the last page, ahead of the window, in other pages
-    c = Case([37, 0, 90], 4, 2, 64, 32, 4, 16, seed=16)
+    c = Case([37, 0, 90], 4, 2, 64, 32, 4, 16, seed=16, max_pages=pages)
     q, cache, table, lens = c.args()
     for window in (0, 20):
         clean = qa.paged_attention_affine(q, cache, table, lens, window=window)
@@ -182,8 +227,9 @@ def test_slots_that_no_sequence_sees_have_no_influence(poison):
         assert torch.equal(qa.paged_attention_affine(q, other, table, lens, window=window), clean)
 
 
-def test_table_entries_outside_the_cache_are_left_out():
-    c = Case([100, 64, 40], 4, 2, 64, 64, 4, 16, seed=17)
+@pytest.mark.parametrize("pages", [7, 160])
+def test_table_entries_outside_the_cache_are_left_out(pages):
+    c = Case([100, 64, 40], 4, 2, 64, 64, 4, 16, seed=17, max_pages=pages)
     c.table[0, 2], c.table[0, 6] = -1, c.pages
     c.table[1, :4] = [2**31 - 1, -2**31, c.pages + 5, -7]   # nothing left: zeros
     c.table[2, 0] = -3
@@ -235,8 +281,9 @@ def test_queries_at_the_ends_of_their_range(act):
         assert (err <= bound[0] * 1.01 + HALF_STEP[act] * np.abs(ref[0]) + F16_GRAIN).all(), (i, err.max())
 
 
-def test_nan_in_a_seen_row_stays_with_its_sequence():
-    c = Case([40, 40], 2, 1, 64, 64, 4, 16, seed=21)
+@pytest.mark.parametrize("pages", [3, 160])
+def test_nan_in_a_seen_row_stays_with_its_sequence(pages):
+    c = Case([40, 40], 2, 1, 64, 64, 4, 16, seed=21, max_pages=pages)
     q, cache, table, lens = c.args()
     clean = qa.paged_attention_affine(q, cache, table, lens)
     cache.k[1][c.table[0, 1], 0, 3] = float("nan")
@@ -244,16 +291,29 @@ def test_nan_in_a_seen_row_stays_with_its_sequence():
     assert torch.isnan(out[0]).all() and torch.equal(out[1], clean[1])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", [1, 2])
+def test_a_value_group_that_is_not_finite_stays_with_its_columns(bad, what):
+    c = Case([40, 40], 2, 1, 128, 64, 4, 16, seed=35)
+    q, cache, table, lens = c.args()
+    clean = qa.paged_attention_affine(q, cache, table, lens)
+    cache.v[what][c.table[0, 1], 0, 3, 1] = bad
+    out = qa.paged_attention_affine(q, cache, table, lens)
+    assert torch.equal(out[0, :, :64], clean[0, :, :64]) and torch.equal(out[1], clean[1])
+    assert not torch.isfinite(out[0, :, 64:]).any() if what == 2 else not torch.isfinite(out[0, :, 64:]).all()
+
+
 def test_same_call_same_bits_and_the_batch_does_not_matter():
-    c = Case([3000, 17, 900], 8, 2, 128, 64, 4, 16, seed=22)
+    c = Case([3000, 17, 900], 8, 2, 128, 64, 4, 16, seed=22)  # in parts
     args = c.args()
     a = qa.paged_attention_affine(*args)
     for _ in range(3):
         assert torch.equal(qa.paged_attention_affine(*args), a)
 
 
-def test_graph_replays_follow_new_lengths():
-    c = Case([900, 40, 0], 8, 2, 128, 64, 4, 16, seed=23)
+@pytest.mark.parametrize("pages", [57, 160])  # one launch; parts and their join
+def test_graph_replays_follow_new_lengths(pages):
+    c = Case([900, 40, 0], 8, 2, 128, 64, 4, 16, seed=23, max_pages=pages)
     q, cache, table, lens = c.args()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
