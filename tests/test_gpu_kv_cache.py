@@ -174,3 +174,28 @@ def test_python_refusals():
         qa.kv_cache_append_affine(cache, torch.zeros((3, 2, 72), dtype=torch.bfloat16, device=dev)[..., 4:68], x, s)
     with pytest.raises(ValueError):
         qa.kv_cache_read_affine(cache, s, out=(x.half(), x))
+
+
+@pytest.mark.parametrize("bits", [2, 4, 8])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_codes_are_the_ieee_quotients(bits, act):
+    # two million values a case in groups of every magnitude (the reciprocal's ends included), short significands that
+    # give exact ties, and groups of one value apart from the rest
+    dev = require_gpu()
+    rng = np.random.default_rng((77, bits))
+    T, H, D, G = 4096, 4, 128, 32
+    x = rng.standard_normal((T, H, D // G, G))
+    x[: T // 4] = np.round(x[: T // 4] * 4) / 4
+    x[T // 4: T // 2] *= rng.integers(1, 64, (T // 4, H, D // G, 1))
+    x[T // 2: T // 2 + 256, :, :, 0] *= 1000
+    lim = 30 if act == "bf16" else 4
+    scale = np.exp2(rng.uniform(-lim, lim, (T, H, D // G, 1)))
+    if act == "bf16":
+        scale[-512:] = np.exp2(rng.uniform(-130, 124, (512, H, D // G, 1)))
+    x = si.store((x * scale).reshape(T, H, D).astype(np.float32), act)
+    cache = qa.AffineKVCache.empty(T // 16, 16, H, D, G, bits, TORCH_DT[act], dev)
+    xd = dev16(x, act, dev)
+    qa.kv_cache_append_affine(cache, xd, xd, torch.arange(T, device=dev))
+    for t, ref in zip(cache.k, od.quantize_rows(x, act, G, bits)):
+        got = _host(t).transpose(0, 2, 1, 3).reshape(T, H, -1)
+        assert (got == ref).all()
