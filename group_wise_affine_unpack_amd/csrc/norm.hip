@@ -26,8 +26,26 @@ __device__ __forceinline__ float rstd_of(double sum, const NormArgs& a) {
   return (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
 }
 
-__device__ __forceinline__ float q8(float n, float s) {
+// x_q = clamp(rint(n / s), -127, 127), 0 when s == 0, the division IEEE
+__device__ __forceinline__ float code_of(float n, float s) {
   return s != 0.f ? fminf(fmaxf(rintf(__fdiv_rn(n, s)), -127.f), 127.f) : 0.f;
+}
+// The same for eight values, r = 1/s: n r corrected by its residual is within
+// a few units of the last place (2^-17) of the quotient, so its whole number
+// is the quotient's unless it lies next to a half, and then all eight take
+// the division (2048 x 4096: 17.5 -> 16.2 us).
+__device__ __forceinline__ void codes_of(const float (&n)[8], float s, float r, float (&q)[8]) {
+  float next = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float q0 = __fmul_rn(n[j], r), q1 = __fmaf_rn(__fmaf_rn(-s, q0, n[j]), r, q0);
+    q[j] = rintf(q1);
+    next = fmaxf(next, fabsf(q1 - q[j]));
+  }
+  if (!(next < 0.4999f && s >= 0x1p-90f && s <= 0x1p90f)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = code_of(n[j], s);
+  }
 }
 
 // A row per WPR waves (WAVES / WPR rows a workgroup), held in registers:
@@ -131,17 +149,22 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_rows_kernel(NormArgs a) {
     }
     const float s = __fdiv_rn(mx, 127.f);
     if (in_row && c0 == 0) a.s_x[m] = s;
+    const float r = __fdiv_rn(1.f, s);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = c0 + 64 * WPR * i;
       if (in_row && c < K8) {
+        float n[8], q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[j] = n_of(i, j);
+        codes_of(n, s, r, q);
         u32x2_t o;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t word = 0;
+          uint32_t word = 0;  // (each byte holds the code plus 128: no clamp is needed, |n| <= 127 s up to rounding)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) word |= ((uint32_t)(int)q8(n_of(i, 4 * j + e), s) & 0xffu) << (8 * e);
-          o[j] = word;
+          for (int e = 0; e < 4; ++e) word = __builtin_amdgcn_cvt_pk_u8_f32(q[4 * j + e] + 128.f, e, word);
+          o[j] = word ^ 0x80808080u;
         }
         ((u32x2_t*)(a.x_q + m * a.K))[c] = o;
       }
@@ -189,7 +212,7 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
     mx = fmaxf(fmaxf(maxs[0], maxs[1]), fmaxf(maxs[2], maxs[3]));
     const float s = __fdiv_rn(mx, 127.f);
     if (t == 0) a.s_x[m] = s;
-    for (int k = t; k < K; k += 256) a.x_q[m * K + k] = (int8_t)q8(n_of(k), s);
+    for (int k = t; k < K; k += 256) a.x_q[m * K + k] = (int8_t)code_of(n_of(k), s);
   }
 }
 
@@ -210,7 +233,7 @@ void launch_rows(const NormArgs& a, hipStream_t s) {
   else if (C <= 256)
     go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 4, 1>, 4, 4);
   else if (C <= 512)
-    go(rmsnorm_rows_kernel<F16_, CODES, W32, 4, 4, 2>, 4, 4);
+    go(rmsnorm_rows_kernel<F16_, CODES, W32, 8, 8, 1>, 8, 8);
   else if (C <= 1024)
     go(rmsnorm_rows_kernel<F16_, CODES, W32, 8, 8, 2>, 8, 8);
   else
