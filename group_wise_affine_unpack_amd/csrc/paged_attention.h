@@ -104,7 +104,17 @@ struct Cfg {
   // workgroups a CU instead of three: 131072 tokens the same, a ragged 4-bit
   // batch of 64 sequences up to 8192 tokens 75 against 67 us.)
   static constexpr int STAGES = 2, LDS = WAVES * STAGES * STAGE;
-  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 ? 3 : LDS * 2 <= 155 * 1024 ? 2 : 1;  // workgroups of four waves
+  // Registers of a step: accumulators, q, what it reads of a stage, and about
+  // 64 more.  Past 256, values are read after the softmax (LATE).
+  static constexpr int KEYS = 2 * NG * KW + 2 * BW + 2 * SW, VALS = 4 * SW + 8 * NG * VW;
+  static constexpr bool LATE = D / 4 + D / 8 + KEYS + VALS + 64 > 256;
+  static constexpr int REGS =
+      D / 4 + D / 8 + 64 + (LATE ? (KEYS > 4 * SW + 8 * VW ? KEYS : 4 * SW + 8 * VW) : KEYS + VALS);
+  // workgroups of four waves a CU, by LDS and registers (one more than the registers hold spills: D = 128, G = 32,
+  // 4-bit, 3 instead of 2: five times the time)
+  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 && REGS <= 168   ? 3
+                                : LDS * 2 <= 155 * 1024 && REGS <= 256 ? 2
+                                                                       : 1;
   static constexpr int COPIES = (CODES + 1023) / 1024, PCOPIES = (8 * PARAMS + 1023) / 1024;
   // rows of 2^n 16-byte pieces keep piece c of row r at c ^ swizzle(r), so that a piece of many rows is spread over the banks
   static constexpr int PIECES = ROWB % 16 == 0 && ((ROWB / 16) & (ROWB / 16 - 1)) == 0 ? ROWB / 16 : 0;
@@ -382,8 +392,13 @@ struct Lanes {
 template <class C>
 __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<C>& ln, const int (&tok)[2], bool edge,
                                      int first, int end, int lane) {
-  // every read of the stage first
+  // every read of the stage first (LATE: of the keys)
   uint32_t kc[2][C::NG][C::KW], kbw[2][C::BW], ks[2][C::SW], vs[2][C::SW], vb[2][C::SW], vc[2][4][C::NG][C::VW];
+  auto read_values = [&](int u, int g) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_bytes<(C::VBITS < 8 ? 1 : C::VBITS / 8)>(st + (2 + u) * C::CODES + i * C::ROWB + ln.v[g], vc[u][i][g]);
+  };
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint8_t* par = st + 4 * C::CODES + u * 4 * C::PARAMS;
@@ -399,12 +414,11 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
   for (int u = 0; u < 2; ++u) {
     const uint8_t* par = st + 4 * C::CODES + (u * 4 + 2) * C::PARAMS + ln.par;
     load_bytes<8 * C::NG>(par, vs[u]);
-    load_bytes<8 * C::NG>(par + C::PARAMS, vb[u]);
+    if constexpr (!C::LATE) {
+      load_bytes<8 * C::NG>(par + C::PARAMS, vb[u]);
 #pragma unroll
-    for (int g = 0; g < C::NG; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        load_bytes<(C::VBITS < 8 ? 1 : C::VBITS / 8)>(st + (2 + u) * C::CODES + i * C::ROWB + ln.v[g], vc[u][i][g]);
+      for (int g = 0; g < C::NG; ++g) read_values(u, g);
+    }
   }
   float z[2][4], p[2][4];
 #pragma unroll
@@ -428,24 +442,27 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
       for (int g = 0; g < C::NG; ++g) z[u][i] = fmaf(half_at<C::ACT16>(ks[u], i * C::NG + g), acc[g][i], z[u][i]);
     }
   }
-  if (edge) {  // tokens that do not count get p = 0 and finite parameters
+  // tokens that do not count get p = 0 and finite parameters
+  auto counts = [&](int u, int i, int kq) {
+    const int t = tok[u] + 4 * kq + i;
+    return tok[u] >= 0 && t >= first && t < end;
+  };
+  auto hide = [&](uint32_t* x, int i) {
+#pragma unroll
+    for (int k = i * C::NG; k < (i + 1) * C::NG; ++k) x[k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
+  };
+  if (edge) {
     int kq = lane >> 4;
     asm volatile("" : "+v"(kq));  // (keeps the comparisons below inside the branch)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = tok[u] + 4 * kq + i;
-        if (tok[u] < 0 || t < first || t >= end) {
+      for (int i = 0; i < 4; ++i)
+        if (!counts(u, i, kq)) {
           z[u][i] = -__builtin_inff();
-#pragma unroll
-          for (int g = 0; g < C::NG; ++g) {
-            const int k = i * C::NG + g;
-            vs[u][k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
-            vb[u][k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
-          }
+          hide(vs[u], i);
+          if constexpr (!C::LATE) hide(vb[u], i);
         }
-      }
   }
   const float zmax = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
                            fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3]))) * w.zscale;
@@ -457,6 +474,19 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
   uint32_t any = (uint32_t)pass | (uint32_t)(pass >> 32);
   asm volatile("" : "+s"(any));
   if (any) rescale<C>(w, vs, zmax);
+  if constexpr (C::LATE) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_bytes<8 * C::NG>(st + 4 * C::CODES + (u * 4 + 3) * C::PARAMS + ln.par, vb[u]);
+    if (edge) {
+      int kq = lane >> 4;
+      asm volatile("" : "+v"(kq));
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!counts(u, i, kq)) hide(vb[u], i);
+    }
+  }
   const float off = PBIAS - w.mu;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
@@ -480,6 +510,10 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
     }
     const f16x8_t A = as_f16x8(aw[0], aw[1], aw[2], aw[3]);
     constexpr int PIECES = C::VBITS <= 16 ? 1 : C::VBITS / 16;
+    if constexpr (C::LATE) {
+      read_values(0, g);
+      read_values(1, g);
+    }
     uint32_t pr[PIECES][4];  // [piece][pair of tokens]
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
