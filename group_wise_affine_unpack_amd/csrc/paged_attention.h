@@ -80,7 +80,7 @@ struct AttnWork {
   int share, htiles;    // query heads a key head; tiles of 16 of them
   float* part_o;        // [2 workgroups][gm][D]
   float* part_ml;       // [2 workgroups][gm][2]
-  AttnMeta* meta;       // [B + 1]; the last one's `tiles` is a workgroup's share
+  AttnMeta* meta;       // [B + 1]; the last one: a unit's start, a workgroup's share
 };
 
 template <int D_, int G_, int BITS_, bool F16_, int WAVES_>
@@ -537,10 +537,11 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
   }
 }
 
-// What starting a unit costs a workgroup, in tiles (without it, a workgroup
-// that a ragged batch gives many short units is the last: 64 sequences up to
-// 8192 tokens, 4-bit, 90 us at 0, 75 at 2, 70 at 3; equal lengths the same).
-constexpr int START = 2;
+// What starting a unit costs a workgroup, in tiles; nothing where each takes
+// one tile.  (Without it, a workgroup that a ragged batch gives many short
+// units is the last: 64 sequences up to 8192 tokens, 4-bit, 90 us at 0, 67 at
+// 2 and at 3; equal lengths the same.)
+__device__ __forceinline__ int start_cost(int64_t tiles, int64_t workgroups) { return tiles <= workgroups ? 0 : 2; }
 
 // Tokens [first, len) of sequence b; returns its tiles of 128 tokens from the
 // 16-token tile of `first` on, at least one.
@@ -569,7 +570,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // The work of all (sequence, unit of heads), in that order, on one line: each
-// unit's START and then its tiles.  Where point x of it lies.
+// unit's start (start_cost) and then its tiles.  Where point x of it lies.
 struct Place {
   int b, unit, at;
   int tiles, first, len;  // of the sequence
@@ -578,7 +579,8 @@ struct Place {
 
 // The batch as every wave sees it, a lane a sequence of the 64 at hand.
 struct Batch {
-  int b0, tiles, first, len;  // tiles with START, 0 past the batch
+  int b0, tiles, first, len;  // tiles with the start, 0 past the batch
+  int lead;                   // a unit's start
   int64_t start;              // of sequence b0 on the line of one unit
 };
 
@@ -586,12 +588,14 @@ __device__ __forceinline__ void batch_at(const AttnWork& w, int b0, Batch& s) {
   const int b = b0 + (int)(threadIdx.x & 63);
   s.b0 = b0;
   s.tiles = s.first = s.len = 0;
-  if (b < w.a.B) s.tiles = START + tiles_of(w.a, b, s.first, s.len);
+  if (b < w.a.B) s.tiles = s.lead + tiles_of(w.a, b, s.first, s.len);
 }
 
-// the line's length for one unit, with the first 64 sequences left at hand: no barrier, and at 64 sequences or fewer, one load
-__device__ __forceinline__ int64_t batch_tiles(const AttnWork& w, Batch& s) {
+// The line's length for one unit, with the first 64 sequences left at hand:
+// no barrier, and at 64 sequences or fewer, one load.
+__device__ __forceinline__ int64_t line_of(const AttnWork& w, int units, Batch& s) {
   double total = 0.0;
+  s.lead = 0;
   for (int b0 = 64; b0 < w.a.B; b0 += 64) {
     batch_at(w, b0, s);
     total += s.tiles;
@@ -599,8 +603,11 @@ __device__ __forceinline__ int64_t batch_tiles(const AttnWork& w, Batch& s) {
   batch_at(w, 0, s);
   s.start = 0;
   const uint64_t n = (uint64_t)wave_sum_f64(total + s.tiles);  // (the same in every lane)
-  return (int64_t)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(n >> 32)) << 32 |
-                   __builtin_amdgcn_readfirstlane((uint32_t)n));
+  const int64_t tiles = (int64_t)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(n >> 32)) << 32 |
+                                  __builtin_amdgcn_readfirstlane((uint32_t)n));
+  s.lead = start_cost(tiles * units, gridDim.x);
+  if (s.tiles > 0) s.tiles += s.lead;
+  return tiles + (int64_t)s.lead * w.a.B;
 }
 
 // Finds point x, at or past the sequences at hand.
@@ -614,7 +621,7 @@ __device__ __forceinline__ Place find_tile(const AttnWork& w, Batch& s, int64_t 
       const int l = __builtin_ctzll(hit | (uint64_t(1) << 63));
       p.b = s.b0 + l;
       const int line = __builtin_amdgcn_readlane(s.tiles, l);
-      p.tiles = line - START;
+      p.tiles = line - s.lead;
       p.first = __builtin_amdgcn_readlane(s.first, l);
       p.len = __builtin_amdgcn_readlane(s.len, l);
       p.start = s.start + __builtin_amdgcn_readlane(upto, l) - line;
@@ -825,15 +832,15 @@ __global__ __launch_bounds__(256, C::PER_CU) void paged_attn_kernel(AttnWork wk)
   const PagedAttnArgs& a = wk.a;
   const int units = a.c.kv_heads * wk.htiles;
   Batch batch;
-  const int64_t all = batch_tiles(wk, batch) * units;
+  const int64_t all = line_of(wk, units, batch) * units;
   const int64_t share = (all + gridDim.x - 1) / gridDim.x;
   const int64_t xend = min(share * (blockIdx.x + 1), all);
-  if (blockIdx.x == 0 && threadIdx.x == 0) wk.meta[a.B].tiles = (int)min(share, (int64_t)(1 << 30));
+  if (blockIdx.x == 0 && threadIdx.x == 0) wk.meta[a.B] = AttnMeta{batch.lead, (int)min(share, (int64_t)(1 << 30))};
   for (int64_t x = share * blockIdx.x; x < xend;) {
     const Place p = find_tile(wk, batch, x, units);
-    const int take = (int)min((int64_t)(START + p.tiles - p.at), xend - x);
+    const int take = (int)min((int64_t)(batch.lead + p.tiles - p.at), xend - x);
     if (p.unit == 0 && p.at == 0 && threadIdx.x == 0) wk.meta[p.b] = AttnMeta{p.start, p.tiles};
-    const int tile = max(p.at - START, 0), tend = p.at + take - START;
+    const int tile = max(p.at - batch.lead, 0), tend = p.at + take - batch.lead;
     if (tend > tile) {  // uniform
       const int begin = (p.first & ~15) + 128 * tile;
       // a part that is not its unit's first is its workgroup's first
@@ -865,13 +872,13 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   const PagedAttnArgs& a = wk.a;
   const int b = blockIdx.y, head = blockIdx.x, t = threadIdx.x, D = a.c.head_dim;
   const AttnMeta mt = wk.meta[b];
-  const uint32_t share = (uint32_t)wk.meta[a.B].tiles;
+  const uint32_t share = (uint32_t)wk.meta[a.B].tiles, lead = (uint32_t)wk.meta[a.B].start;
   const int j = head / wk.share, ht = (head - j * wk.share) / 16, h = head - j * wk.share - 16 * ht;
   const int gstore = min(16, wk.share);
   __shared__ float msh[8], osh[8][256 + 4], lsh[8];
   // the workgroups of this unit's first and last tile
   const uint64_t x0 = (uint64_t)mt.start * (a.c.kv_heads * wk.htiles) +
-                      (uint64_t)(j * wk.htiles + ht) * (START + mt.tiles) + START;
+                      (uint64_t)(j * wk.htiles + ht) * (lead + mt.tiles) + lead;
   const uint32_t w0 = quotient(x0, share), w1 = quotient(x0 + mt.tiles - 1, share);
   if (w0 == w1) return;
   const int n = (int)(w1 - w0) + 1;
