@@ -308,10 +308,11 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
       mx = fmaxf(mx, fabsf(qv[g][k]));
     }
   mx = quads_max(mx);
-  // the largest entry to [2^14, 2^15), with the sign of the scale
+  // the largest entry to [2^14, 2^15) (one below 2^-113 to less), with the sign of the scale
   int e = 0;
-  if (mx > 0.f && mx < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(mx) + 1;
-  const float sign = scale < 0.f ? -1.f : 1.f;
+  if (mx > 0.f && mx < __builtin_inff()) e = min(14 - __builtin_amdgcn_frexp_expf(mx) + 1, 127);
+  const float to = __builtin_amdgcn_ldexpf(scale < 0.f ? -1.f : 1.f, e);
+  const f16x2_t ones = {(_Float16)1.f, (_Float16)1.f};
   w.qsum = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
@@ -321,11 +322,10 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
       uint32_t reg[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float lo = sign * __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 0)], e);
-        const float hi = sign * __builtin_amdgcn_ldexpf(qv[g][key_dim<C>(s, r, 1)], e);
-        const float f = 1.f / (float)(1 << key_shift<C>(r));
-        reg[r] = (uint32_t)f32_to_f16_bits(lo * f) | (uint32_t)f32_to_f16_bits(hi * f) << 16;
-        sum += lo + hi;
+        const f16x2_t h = {(_Float16)(qv[g][key_dim<C>(s, r, 0)] * to), (_Float16)(qv[g][key_dim<C>(s, r, 1)] * to)};
+        sum = __builtin_amdgcn_fdot2(h, ones, sum, false);
+        const _Float16 f = (_Float16)(1.f / (float)(1 << key_shift<C>(r)));
+        reg[r] = __builtin_bit_cast(uint32_t, h * f16x2_t{f, f});
       }
       w.q[g][s] = as_f16x8(reg[0], reg[1], reg[2], reg[3]);
     }
@@ -740,6 +740,11 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
       });
     };
     copy(0, ring);
+    // (q's conversion stays behind the last of these copies: it waits for q, and with it for them)
+#pragma unroll
+    for (int g = 0; g < C::NG; ++g)
+#pragma unroll
+      for (int k = 0; k < C::G / 8; ++k) asm volatile("" : "+v"(qraw[g][k]));
     set_q<C>(w, qraw, n16 < gm, kq, a.scale);
     // the tiles of the stage being computed: the copies run ahead and may have gone on to the next 32 steps'
     int at_now = at, at_now_from = 0;
