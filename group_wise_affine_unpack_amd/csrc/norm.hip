@@ -10,6 +10,8 @@
 // overflows) and rstd is rounded once to fp32: the sum's order then leaves rstd's
 // bits, and so the codes, unchanged.  Every other step is one IEEE fp32
 // operation.
+#include <algorithm>
+
 #include "common.h"
 
 namespace qaff {
@@ -256,17 +258,36 @@ void launch_dt(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
-  const bool f16 = a.act_dt == F16, codes = a.x_q != nullptr;
-  if (f16 && codes)
-    launch_dt<true, true>(a, s);
-  else if (f16)
-    launch_dt<true, false>(a, s);
-  else if (codes)
-    launch_dt<false, true>(a, s);
-  else
-    launch_dt<false, false>(a, s);
-  return hipGetLastError();
+hipError_t launch_rmsnorm(const NormArgs& all, hipStream_t s) {
+  // 2^21 rows a launch: one has fewer than 2^32 threads, and a row up to 1024 of them
+  constexpr int64_t ROWS = int64_t(1) << 21;
+  const bool f16 = all.act_dt == F16, codes = all.x_q != nullptr;
+  for (int64_t m = 0; m < all.M; m += ROWS) {
+    NormArgs a = all;
+    a.M = std::min(all.M - m, ROWS);
+    a.x = (const uint16_t*)all.x + m * all.ldx;
+    if (all.resid) {
+      a.resid = (const uint16_t*)all.resid + m * all.ldr;
+      a.h_out = (uint16_t*)all.h_out + m * all.ldh;
+    }
+    if (codes) {
+      a.x_q = all.x_q + m * all.K;
+      a.s_x = all.s_x + m;
+    } else {
+      a.y = (uint16_t*)all.y + m * all.K;
+    }
+    if (f16 && codes)
+      launch_dt<true, true>(a, s);
+    else if (f16)
+      launch_dt<true, false>(a, s);
+    else if (codes)
+      launch_dt<false, true>(a, s);
+    else
+      launch_dt<false, false>(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace qaff

@@ -178,6 +178,23 @@ def test_product_from_codes_equals_the_product_from_activations(M, N, K):
     assert rep["ok"], rep
 
 
+@pytest.mark.parametrize("K", [8, 6])
+def test_more_rows_than_one_launch_takes(K):
+    # 2^21 rows a launch: the rows around the cut as a call of their own has them
+    dev = require_gpu()
+    M, n = (1 << 21) + 5, 1 << 21
+    x = torch.randn((M, K), device=dev).bfloat16()
+    w = torch.randn(K, device=dev)
+    y, h = qa.rmsnorm(x, w, resid=x)
+    x_q, s_x, h2 = qa.rmsnorm_w4a8(x, w, resid=x)
+    part = slice(n - 3, M)
+    xp = x[part].contiguous()
+    yp, hp = qa.rmsnorm(xp, w, resid=xp)
+    qp, sp, _ = qa.rmsnorm_w4a8(xp, w, resid=xp)
+    assert torch.equal(y[part], yp) and torch.equal(h[part], hp) and torch.equal(h, h2)
+    assert torch.equal(x_q[part], qp) and torch.equal(s_x[part], sp)
+
+
 def test_norm_refusals():
     dev = require_gpu()
     x = torch.zeros((2, 64), dtype=torch.bfloat16, device=dev)
