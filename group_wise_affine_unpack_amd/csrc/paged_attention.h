@@ -71,7 +71,7 @@ constexpr int VROOM = 6;        // how far a value scale may pass its power of t
 
 struct AttnMeta {
   int64_t start;  // a sequence's start on the line of one unit
-  int tiles;
+  int tiles;      // its tiles
 };
 
 struct AttnWork {
@@ -80,7 +80,7 @@ struct AttnWork {
   int share, htiles;    // query heads a key head; tiles of 16 of them
   float* part_o;        // [2 workgroups][gm][D]
   float* part_ml;       // [2 workgroups][gm][2]
-  AttnMeta* meta;       // [B + 1]; the last one: a unit's start, a workgroup's share
+  AttnMeta* meta;       // [B + 1]; the last one: a workgroup's share of the line, a unit's start on it
 };
 
 template <int D_, int G_, int BITS_, bool F16_, int WAVES_>
@@ -234,7 +234,7 @@ struct Wave {
   // constant over the loop
   f16x8_t q[C::NG][C::KS];
   u32x4_t qsum;           // the key biases' operand: Q_g of this lane's head, a 16-bit piece of it by the lane's quarter
-  float zscale;           // logits to base 2, with q's power of two and the codes' taken back; >= 0
+  float zscale;           // logits to base 2, with q's power of two and the codes' taken back; > 0
   // running
   f32x4_t o[C::NG][C::VC];
   float l, bias[C::NG];   // sums over this lane's tokens
@@ -308,10 +308,13 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
       mx = fmaxf(mx, fabsf(qv[g][k]));
     }
   mx = quads_max(mx);
-  // the largest entry to [2^14, 2^15) (one below 2^-113 to less), with the sign of the scale
+  // the largest entry to [2^14, 2^15) (one below 2^-113 to less), with the sign of the scale; to less also
+  // where zscale would pass below 2^-126, since z = -inf of a hidden token times a zscale of 0 is not hidden
+  const float base2 = fabsf(scale) * 1.4426950408889634f;
   int e = 0;
-  if (mx > 0.f && mx < __builtin_inff()) e = min(14 - __builtin_amdgcn_frexp_expf(mx) + 1, 127);
-  const float to = __builtin_amdgcn_ldexpf(scale < 0.f ? -1.f : 1.f, e);
+  if (mx > 0.f && mx < __builtin_inff())
+    e = min(min(14 - __builtin_amdgcn_frexp_expf(mx) + 1, 127), 149 + __builtin_amdgcn_frexp_expf(base2));
+  const float to = scale == 0.f ? 0.f : __builtin_amdgcn_ldexpf(scale < 0.f ? -1.f : 1.f, e);
   const f16x2_t ones = {(_Float16)1.f, (_Float16)1.f};
   w.qsum = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
@@ -338,7 +341,7 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
       left -= C::ACT16 ? f16_bits_to_f32(piece) : bf16_bits_to_f32(piece);
     }
   }
-  w.zscale = __builtin_amdgcn_ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e);
+  w.zscale = scale == 0.f ? 1.f : __builtin_amdgcn_ldexpf(base2, 24 - e);
 }
 
 // New references for the heads of this wave, and everything summed so far
@@ -551,8 +554,8 @@ __device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, int b, int& firs
   return max(1, (int)(((long)len - (first & ~15) + 127) >> 7));
 }
 
-__device__ __forceinline__ uint32_t quotient(uint64_t n, uint32_t d) {
-  return (n >> 32) == 0 ? (uint32_t)n / d : (uint32_t)(n / d);
+__device__ __forceinline__ uint32_t quotient(uint64_t n, uint64_t d) {
+  return ((n | d) >> 32) == 0 ? (uint32_t)n / (uint32_t)d : (uint32_t)(n / d);
 }
 
 // inclusive sum over the 64 lanes
@@ -840,7 +843,7 @@ __global__ __launch_bounds__(256, C::PER_CU) void paged_attn_kernel(AttnWork wk)
   const int64_t all = line_of(wk, units, batch) * units;
   const int64_t share = (all + gridDim.x - 1) / gridDim.x;
   const int64_t xend = min(share * (blockIdx.x + 1), all);
-  if (blockIdx.x == 0 && threadIdx.x == 0) wk.meta[a.B] = AttnMeta{batch.lead, (int)min(share, (int64_t)(1 << 30))};
+  if (blockIdx.x == 0 && threadIdx.x == 0) wk.meta[a.B] = AttnMeta{share, batch.lead};
   for (int64_t x = share * blockIdx.x; x < xend;) {
     const Place p = find_tile(wk, batch, x, units);
     const int take = (int)min((int64_t)(batch.lead + p.tiles - p.at), xend - x);
@@ -877,7 +880,8 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   const PagedAttnArgs& a = wk.a;
   const int b = blockIdx.y, head = blockIdx.x, t = threadIdx.x, D = a.c.head_dim;
   const AttnMeta mt = wk.meta[b];
-  const uint32_t share = (uint32_t)wk.meta[a.B].tiles, lead = (uint32_t)wk.meta[a.B].start;
+  const uint64_t share = (uint64_t)wk.meta[a.B].start;
+  const uint32_t lead = (uint32_t)wk.meta[a.B].tiles;
   const int j = head / wk.share, ht = (head - j * wk.share) / 16, h = head - j * wk.share - 16 * ht;
   const int gstore = min(16, wk.share);
   __shared__ float msh[8], osh[8][256 + 4], lsh[8];
@@ -954,7 +958,7 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   const int64_t units = (int64_t)a.c.kv_heads * w.htiles;
   // the most tokens a sequence can see, with the rest of the window's first 16-token tile
   const int64_t table = (int64_t)a.max_pages * a.c.page_size;
-  const int64_t tokens = a.window > 0 ? std::min(table, a.window + 15) : table;
+  const int64_t tokens = a.window > 0 && a.window < table ? std::min(table, a.window + 15) : table;
   w.part_o = w.part_ml = nullptr;
   w.meta = nullptr;
   // Short sequences: a workgroup each, no parts, no second kernel.  Up to
@@ -964,8 +968,7 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   // 25).  Eight waves share one, four when there are more than the CUs
   // (128 sequences of 512 tokens: 24.5 against 32 us).
   const int64_t wgs = units * a.B;
-  if (tokens <= 1024 || (tokens <= 2048 && wgs >= 128)) {
-    if (wgs >= (int64_t(1) << 31)) return hipErrorNotSupported;
+  if ((tokens <= 1024 || (tokens <= 2048 && wgs >= 128)) && wgs < (1 << 24)) {  // (2^32 threads at most in a launch)
     if (wgs > 256)
       hipLaunchKernelGGL(paged_attn_short_kernel<C>, dim3((unsigned)wgs), dim3(256), attn_lds<C>(gm), s, w);
     else

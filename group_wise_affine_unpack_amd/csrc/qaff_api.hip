@@ -94,7 +94,7 @@ int qaff_stream_read(const void* src, uint64_t bytes, uint32_t* sink, int32_t bl
   return ok();
 }
 
-int qaff_version(void) { return 200; }
+int qaff_version(void) { return 210; }
 
 int qaff_release_workspaces(uint64_t* freed_bytes) {
   size_t freed = 0;
@@ -609,7 +609,10 @@ int paged_attention_affine(const qaff_kv_cache* cache, const void* q, int64_t q_
   if (heads < 1 || heads % a.c.kv_heads)
     return fail(QAFF_E_INVAL, "heads=%d is not a positive multiple of kv_heads=%d", heads, a.c.kv_heads);
   if (B > 65535 || heads > (1 << 16)) return fail(QAFF_E_UNSUPPORTED, "B above 65535 or heads above 65536");
-  if (max_pages >= (int64_t(1) << 31) / a.c.page_size) return fail(QAFF_E_UNSUPPORTED, "max_pages * page_size of 2^31 or more");
+  if (max_pages > ((int64_t(1) << 31) - (1 << 16)) / a.c.page_size)
+    return fail(QAFF_E_UNSUPPORTED, "max_pages * page_size above 2^31 - 2^16");
+  if (a.c.num_pages >= (int64_t(1) << 31) / a.c.kv_heads / (a.c.page_size / 16))
+    return fail(QAFF_E_UNSUPPORTED, "2^31 tiles of 16 rows or more");
   if (!(scale > -1e30 && scale < 1e30)) return fail(QAFF_E_INVAL, "scale must be finite");
   if (window < 0) return fail(QAFF_E_INVAL, "window must be >= 0 (got %lld)", (long long)window);
   if (B == 0) return ok();

@@ -23,7 +23,7 @@
  *   - The caller owns every buffer; the library keeps no pointer to them
  *     after the call returns.  Internal scratch (GEMM pre-pass buffers and
  *     split-K partials, GPTQ partials and tables, permuted activations for
- *     k_perm) comes from a buffer the library keeps per (device, stream):
+ *     k_perm, the parts of split sequences in paged_attention_affine) comes from a buffer the library keeps per (device, stream):
  *     calls on one stream reuse it in stream order, and once it is large
  *     enough no call allocates.  It only grows, and growing is refused
  *     (QAFF_E_HIP) while `stream` is being captured into a graph: capture a
@@ -446,7 +446,8 @@ typedef struct qaff_kv_cache {
  *          [0, num_pages * page_size) is skipped (-1 marks the padding of a
  *          batch).  Slots in range must be distinct: two tokens of one slot
  *          race, and the row then mixes both.
- * Nothing but the named rows is written.  One launch.
+ * Nothing but the named rows is written.  One launch.  T * kv_heads *
+ * head_dim must stay below 2^33 (QAFF_E_UNSUPPORTED).
  */
 int kv_cache_append_affine(const qaff_kv_cache *cache, const void *k, const void *v, int64_t k_token_stride,
                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
@@ -458,7 +459,8 @@ int kv_cache_append_affine(const qaff_kv_cache *cache, const void *k, const void
  *     rounded), then rounded to dtype
  *   slots  [T] int64, repeats allowed; a slot outside the cache reads as zeros
  *   k_out, v_out  [T, kv_heads, head_dim] dtype, dense, 16-byte aligned
- * One launch.
+ * One launch.  T * kv_heads * head_dim must stay below 2^34
+ * (QAFF_E_UNSUPPORTED).
  */
 int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void *k_out, void *v_out, int64_t T,
                          void *stream);
@@ -483,10 +485,22 @@ int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void 
  *               page_size counts as that.
  *   out         [B, heads, head_dim] dtype, dense, 16-byte aligned
  *   heads a multiple of kv_heads; head_dim in {64, 96, 128, 192, 256};
- *   window >= 0; scale finite.
+ *   window >= 0; scale finite, |scale| * max |q| below 2^115;
+ *   max_pages * page_size at most 2^31 - 2^16, B at most 65535, heads at most
+ *   65536, num_pages * kv_heads * page_size / 16 below 2^31
+ *   (QAFF_E_UNSUPPORTED).
  * Lengths are read on the device only: a captured call follows the lengths
  * of the replay.  What the cache holds in slots that no sequence sees has no
- * influence, NaN included.
+ * influence, NaN included.  A NaN or an infinity that a sequence sees stays
+ * with that sequence (in a value's group, with that group's columns).
+ * Accuracy: logits, softmax and sums in fp32; each softmax weight times the
+ * value's scale is rounded to 11 bits before the products with the integer
+ * codes.  Value scales must stay below 2^110.
+ * One launch when the table (with a window, that plus 15) has at most 1024
+ * tokens, or at most 2048 and B * kv_heads >= 128 (query heads of a key head
+ * past 16 count as another key head); otherwise two, with
+ * scratch (2 workgroups' parts a CU, a few MiB): capture such a call after
+ * an eager one of the same shapes.  The same call gives the same bits.
  */
 int paged_attention_affine(const qaff_kv_cache *cache, const void *q, int64_t q_seq_stride, int64_t q_head_stride,
                            const int32_t *page_table, int64_t table_stride, int64_t max_pages,

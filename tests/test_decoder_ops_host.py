@@ -81,6 +81,16 @@ def test_attention_arguments(kw, code):
     assert _attn(**kw) == code and _msg() != ""
 
 
+def test_attention_tables_past_31_bits():
+    assert _attn(_cache(), pages=(1 << 27)) == UNSUP
+    assert _attn(_cache(), pages=(1 << 27) - (1 << 12) + 1) == UNSUP  # (pages of 16: past 2^31 - 2^16 tokens)
+
+
+def test_attention_rows_past_31_bits():
+    # 2^26 pages of 16 tokens by 64 heads: 2^32 tiles
+    assert _attn(_cache(num_pages=1 << 26, kv_heads=64), heads=64) == UNSUP
+
+
 @pytest.mark.parametrize("D,G", [(32, 32), (160, 32), (224, 32)])
 def test_attention_head_sizes(D, G):
     assert _attn(_cache(head_dim=D, group_size=G)) == UNSUP

@@ -131,6 +131,14 @@ def test_every_row_empty():
     c, _ = _run([0, 0, 0], 4, 2, 64, 64, 4, 16, seed=6)
 
 
+def test_a_table_without_pages():
+    c = Case([0, 0], 2, 1, 64, 64, 4, 16, seed=37)
+    q, cache, table, _ = c.args()
+    lens = torch.tensor([5, 0], dtype=torch.int32, device=c.dev)  # more than the table has
+    assert (qa.paged_attention_affine(q, cache, table[:, :0], lens) == 0).all()
+    assert qa.paged_attention_affine(q[:0], cache, table[:0], lens[:0]).shape == (0, 2, 64)
+
+
 def test_negative_and_overlong_lengths():
     # less than nothing is nothing; past the table is the whole table
     c = Case([40, 40, 48], 2, 1, 64, 64, 4, 16, seed=7, max_pages=3)
@@ -140,7 +148,7 @@ def test_negative_and_overlong_lengths():
     c.check(out)
 
 
-@pytest.mark.parametrize("window", [1, 2, 16, 31, 100, 128, 500, 10**12])
+@pytest.mark.parametrize("window", [1, 2, 16, 31, 100, 128, 500, 10**12, 2**63 - 1])
 def test_windows(window):
     _run([1, 20, 130, 500, 901], 4, 2, 128, 64, 4, 16, seed=8, window=window)
 
@@ -168,9 +176,35 @@ def test_peaked_softmax(q_std, act):
     _run([300, 65], 4, 2, 128, 64, 8, 16, act=act, seed=12, q_std=q_std)
 
 
-@pytest.mark.parametrize("scale", [1e-3, 1.0, -0.125])
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 1.0, -0.125])
 def test_scales(scale):
     _run([100], 2, 1, 64, 64, 4, 16, seed=13, scale=scale)
+
+
+def test_logits_that_vanish():
+    # queries and a scale whose product is below every fp32: all tokens alike, those of a tile's rest still hidden
+    c = Case([37, 64], 2, 1, 64, 64, 4, 16, seed=38)
+    c.q = si.store((1e-38 * np.random.default_rng(38).standard_normal((2, 2, 64))).astype(np.float32), "bf16")
+    c.check(qa.paged_attention_affine(*c.args(), scale=1e-29), 1e-29)
+
+
+@pytest.mark.parametrize("pages", [8, 160])
+def test_rows_past_4_gib(pages):
+    # the same rows in a cache whose code and parameter arrays have them past byte 2^32 (one launch, and parts)
+    c = Case([120, 33], 4, 2, 128, 32, 2, 16, seed=39, max_pages=pages)
+    q, small, table, lens = c.args()
+    base = (1 << 32) // (2 * 16 * 8)  # scales: 2 heads of 16 rows of 4 groups, 2 bytes each
+    dev = q.device
+    triples = []
+    for t in (small.k, small.v):
+        new = [torch.empty((base + c.pages, *a.shape[1:]), dtype=a.dtype, device=dev) for a in t]
+        for n, a in zip(new, t):
+            n[base:] = a
+        triples.append(new)
+    big = qa.AffineKVCache(*triples, 32, 2)
+    out = qa.paged_attention_affine(q, big, table + base, lens)
+    assert torch.equal(out, qa.paged_attention_affine(q, small, table, lens))
+    c.check(out)
 
 
 def test_value_scales_over_many_decades():
