@@ -22,9 +22,14 @@
 // 16-bit pieces, in the parameters' own type.
 // Registers: C_g has the tokens of a lane's quarter (lane / 16) as rows and
 // the head (lane % 16) as column, which is where the value product takes its
-// second operand from, so p never leaves the lane.  Value codes arrive as
-// rows of tokens and are wanted as pairs of tokens: two tokens' codes of the
-// same columns are put into the halves of one register first.
+// second operand from, so p never leaves the lane.  Where a key head has few
+// query heads, each takes FOLD of the 16 columns: column (sub, head) keeps the
+// softmax of the tokens TOK sub + i of each quarter's four only, its other
+// weights are zero, and the columns of a head are added at the end.  That
+// takes the softmax's and the parameters' work of unused columns away.
+// Value codes arrive as rows of tokens and are wanted as pairs of tokens: two
+// tokens' codes of the same columns are put into the halves of one register
+// first.
 // q is scaled by a power of two per head so that its largest entry lies in
 // [2^14, 2^15): exact for f16 queries and, below 2^-29 of the largest, off by
 // at most 2^-39 of it for bf16 ones.
@@ -42,13 +47,15 @@
 // of memory is thereby one code row's 16-byte piece instead of 28 loads of 2
 // to 16 bytes a step.
 // What bounds it: at 8 bits memory (64 sequences of 4096 tokens, D = 128:
-// 571 MB in 95 us, 6.0 TB/s), at 4 bits the vector instructions, about 270 a
-// step of 4.6 KB (302 MB in 60 to 64 us, 4.8 TB/s; vector pipes busy 68% of
-// the time), for few tokens the chain lengths -> page table -> rows -> join.
+// 571 MB in 95 us, 6.0 TB/s), at 4 bits the waits of 12 waves a CU on their
+// copies and on each other's vector instructions, 237 a step of 4.6 KB with
+// four heads a key head (302 MB in 59 to 62 us, 5.0 TB/s; vector pipes busy
+// 58% of the time), for few tokens the chain lengths -> page table -> rows ->
+// join.
 // Measured and not kept: operands loaded from memory into registers with one
-// step of look-ahead (70 us for those 302 MB), three or four stages of
-// look-ahead (the same), four workgroups a CU (71 us), chunks of equal size
-// instead of equal shares (a ragged 8-bit batch 119 against 101 us).
+// step of look-ahead (70 us for those 302 MB where the copies took 64), three
+// or four stages of look-ahead (64), four workgroups a CU (71), chunks of
+// equal size instead of equal shares (a ragged 8-bit batch 119 against 101).
 //
 // Work: equal shares of all tiles of 128 tokens (paged_attn_kernel), four
 // waves to a tile, joined through LDS; sequences cut by a share's end leave
@@ -83,17 +90,18 @@ struct AttnWork {
   AttnMeta* meta;       // [B + 1]; the last one: a workgroup's share of the line, a unit's start on it
 };
 
-template <int D_, int G_, int BITS_, bool F16_, int WAVES_>
+template <int D_, int G_, int BITS_, bool F16_, int FOLD_, int WAVES_>
 struct Cfg {
   static constexpr int D = D_, G = G_, BITS = BITS_, NG = D / G, WAVES = WAVES_;
   static constexpr bool ACT16 = F16_;
+  static constexpr int FOLD = FOLD_, HEADS = 16 / FOLD, TOK = 4 / FOLD;  // columns a head, heads, tokens a lane of a quarter's four
   static constexpr int KS = G / 32;                      // product steps a group (keys)
   static constexpr int KB = G / 4 * BITS / 8;            // key code bytes a lane and group
   static constexpr int KW = KB < 4 ? 1 : KB / 4;
   static constexpr int VC = G / 16;                      // value columns a lane and group
   static constexpr int VBITS = VC * BITS;                // value code bits a lane, token and group
   static constexpr int VW = VBITS <= 32 ? 1 : 2;
-  static constexpr int SW = 2 * NG;                      // words of four tokens' scales
+  static constexpr int SW = (TOK * NG + 1) / 2;          // words of the scales of a lane's tokens of 16
   static constexpr int BW = (NG + 1) / 2;                // words of one token's
   static constexpr int ROWB = D * BITS / 8;
   // A stage in LDS: 32 tokens' key codes, value codes, then per half the
@@ -105,15 +113,16 @@ struct Cfg {
   // batch of 64 sequences up to 8192 tokens 75 against 67 us.)
   static constexpr int STAGES = 2, LDS = WAVES * STAGES * STAGE;
   // Registers of a step: accumulators, q, what it reads of a stage, and about
-  // 64 more.  Past 256, values are read after the softmax (LATE).
+  // 64 more (the compiler takes up to 25 on top).  Past 240, values are read after the softmax (LATE).
   static constexpr int KEYS = 2 * NG * KW + 2 * BW + 2 * SW, VALS = 4 * SW + 8 * NG * VW;
-  static constexpr bool LATE = D / 4 + D / 8 + KEYS + VALS + 64 > 256;
+  static constexpr bool LATE = D / 4 + D / 8 + KEYS + VALS + 64 > 240;
   static constexpr int REGS =
       D / 4 + D / 8 + 64 + (LATE ? (KEYS > 4 * SW + 8 * VW ? KEYS : 4 * SW + 8 * VW) : KEYS + VALS);
   // workgroups of four waves a CU, by LDS and registers (one more than the registers hold spills: D = 128, G = 32,
-  // 4-bit, 3 instead of 2: five times the time)
-  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 && REGS <= 168   ? 3
-                                : LDS * 2 <= 155 * 1024 && REGS <= 256 ? 2
+  // 4-bit, 16 heads, 3 instead of 2: five times the time; D = 256, G = 32, 2-bit, 2 instead of 1: 288 against 191 us.
+  // Four where REGS <= 116, D = 64: the same time)
+  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 && REGS <= 165   ? 3
+                                : LDS * 2 <= 155 * 1024 && REGS <= 228 ? 2
                                                                        : 1;
   static constexpr int COPIES = (CODES + 1023) / 1024, PCOPIES = (8 * PARAMS + 1023) / 1024;
   // rows of 2^n 16-byte pieces keep piece c of row r at c ^ swizzle(r), so that a piece of many rows is spread over the banks
@@ -344,6 +353,34 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
   w.zscale = scale == 0.f ? 1.f : __builtin_amdgcn_ldexpf(base2, 24 - e);
 }
 
+// which of a head's FOLD columns a lane has, and with them the tokens TOK sub + i of its quarter
+template <class C>
+__device__ __forceinline__ int sub_of(int lane) {
+  return C::FOLD == 1 ? 0 : (lane & 15) / C::HEADS;
+}
+template <class C>
+__device__ __forceinline__ float own(const f32x4_t& v, int i, int sub) {
+  if constexpr (C::FOLD == 1) return v[i];
+  else if constexpr (C::FOLD == 2) return sub ? v[2 + i] : v[i];
+  else {
+    const float lo = (sub & 1) ? v[1] : v[0], hi = (sub & 1) ? v[3] : v[2];
+    return (sub & 2) ? hi : lo;
+  }
+}
+// sum and maximum over the columns of a head
+template <class C>
+__device__ __forceinline__ float fold_sum(float v) {
+  if constexpr (C::FOLD >= 2) v += dpp_mov<0x128>(v);  // row_ror:8
+  if constexpr (C::FOLD >= 4) v += dpp_mov<0x124>(v);  // row_ror:4
+  return v;
+}
+template <class C>
+__device__ __forceinline__ float fold_max(float v) {
+  if constexpr (C::FOLD >= 2) v = fmaxf(v, dpp_mov<0x128>(v));
+  if constexpr (C::FOLD >= 4) v = fmaxf(v, dpp_mov<0x124>(v));
+  return v;
+}
+
 // New references for the heads of this wave, and everything summed so far
 // brought to them.
 template <class C>
@@ -362,8 +399,8 @@ __device__ __forceinline__ void rescale(Wave<C>& w, const uint32_t (&vs)[2][C::S
         vm = fmaxf(vm, v < __builtin_inff() ? v : 0.f);  // (one that is not finite makes its own columns so)
       }
     }
-  vm = quads_max(vm);
-  const float m = fmaxf(w.mref, quads_max(zmax));
+  vm = fold_max<C>(quads_max(vm));
+  const float m = fmaxf(w.mref, fold_max<C>(quads_max(zmax)));
   // the exponent of the largest scale, kept where 2^(5 - mu) and its sums stay finite
   const float e = fmaxf(w.vexp, fminf(fmaxf((float)((int)(__float_as_uint(vm) >> 23) - 127), -90.f), 110.f));
   const float mu = (m == -__builtin_inff() ? 0.f : m) + e;
@@ -387,6 +424,7 @@ __device__ __forceinline__ void rescale(Wave<C>& w, const uint32_t (&vs)[2][C::S
 template <class C>
 struct Lanes {
   uint32_t k[C::NG][C::KB > 16 ? 2 : 1], v[C::NG], par, kb;
+  uint32_t keep[2];  // of the pairs of a quarter's tokens, the halves that are this lane's
 };
 
 // 32 tokens from a stage in LDS.  tok: each half's first token; -1: no such
@@ -411,19 +449,20 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
       if constexpr (C::KB > 16) load_bytes<16>(st + u * C::CODES + ln.k[g][1], kc[u][g] + 4);
     }
     load_bytes<2 * C::NG>(par + C::PARAMS + ln.kb, kbw[u]);
-    load_bytes<8 * C::NG>(par + ln.par, ks[u]);
+    load_bytes<2 * C::TOK * C::NG>(par + ln.par, ks[u]);
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint8_t* par = st + 4 * C::CODES + (u * 4 + 2) * C::PARAMS + ln.par;
-    load_bytes<8 * C::NG>(par, vs[u]);
+    load_bytes<2 * C::TOK * C::NG>(par, vs[u]);
     if constexpr (!C::LATE) {
-      load_bytes<8 * C::NG>(par + C::PARAMS, vb[u]);
+      load_bytes<2 * C::TOK * C::NG>(par + C::PARAMS, vb[u]);
 #pragma unroll
       for (int g = 0; g < C::NG; ++g) read_values(u, g);
     }
   }
-  float z[2][4], p[2][4];
+  float z[2][C::TOK], p[2][C::TOK];
+  const int sub = sub_of<C>(lane);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     u32x4_t kb = {0u, 0u, 0u, 0u};
@@ -439,15 +478,15 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
         acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_codes<C>(kc[u][g], s), w.q[g][s], acc[g], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[u][i] = zb[i];
+    for (int i = 0; i < C::TOK; ++i) {
+      z[u][i] = own<C>(zb, i, sub);
 #pragma unroll
-      for (int g = 0; g < C::NG; ++g) z[u][i] = fmaf(half_at<C::ACT16>(ks[u], i * C::NG + g), acc[g][i], z[u][i]);
+      for (int g = 0; g < C::NG; ++g) z[u][i] = fmaf(half_at<C::ACT16>(ks[u], i * C::NG + g), own<C>(acc[g], i, sub), z[u][i]);
     }
   }
   // tokens that do not count get p = 0 and finite parameters
-  auto counts = [&](int u, int i, int kq) {
-    const int t = tok[u] + 4 * kq + i;
+  auto counts = [&](int u, int i, int at) {
+    const int t = tok[u] + at + i;
     return tok[u] >= 0 && t >= first && t < end;
   };
   auto hide = [&](uint32_t* x, int i) {
@@ -455,20 +494,22 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
     for (int k = i * C::NG; k < (i + 1) * C::NG; ++k) x[k / 2] &= (k & 1) ? 0xffffu : 0xffff0000u;
   };
   if (edge) {
-    int kq = lane >> 4;
-    asm volatile("" : "+v"(kq));  // (keeps the comparisons below inside the branch)
+    int at = 4 * (lane >> 4) + C::TOK * sub;
+    asm volatile("" : "+v"(at));  // (keeps the comparisons below inside the branch)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!counts(u, i, kq)) {
+      for (int i = 0; i < C::TOK; ++i)
+        if (!counts(u, i, at)) {
           z[u][i] = -__builtin_inff();
           hide(vs[u], i);
           if constexpr (!C::LATE) hide(vb[u], i);
         }
   }
-  const float zmax = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
-                           fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3]))) * w.zscale;
+  float zmax = fmaxf(z[0][0], z[1][0]);
+#pragma unroll
+  for (int i = 1; i < C::TOK; ++i) zmax = fmaxf(zmax, fmaxf(z[0][i], z[1][i]));
+  zmax *= w.zscale;
   uint32_t vmax = vs[0][0];
 #pragma unroll
   for (int i = 1; i < 2 * C::SW; ++i) vmax = pk_max_u16(vmax, vs[i / C::SW][i % C::SW]);
@@ -479,22 +520,22 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
   if (any) rescale<C>(w, vs, zmax);
   if constexpr (C::LATE) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_bytes<8 * C::NG>(st + 4 * C::CODES + (u * 4 + 3) * C::PARAMS + ln.par, vb[u]);
+    for (int u = 0; u < 2; ++u) load_bytes<2 * C::TOK * C::NG>(st + 4 * C::CODES + (u * 4 + 3) * C::PARAMS + ln.par, vb[u]);
     if (edge) {
-      int kq = lane >> 4;
-      asm volatile("" : "+v"(kq));
+      int at = 4 * (lane >> 4) + C::TOK * sub;
+      asm volatile("" : "+v"(at));
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!counts(u, i, kq)) hide(vb[u], i);
+        for (int i = 0; i < C::TOK; ++i)
+          if (!counts(u, i, at)) hide(vb[u], i);
     }
   }
   const float off = PBIAS - w.mu;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C::TOK; ++i) {
       p[u][i] = __builtin_amdgcn_exp2f(fmaf(z[u][i], w.zscale, off));
       w.l += p[u][i];
 #pragma unroll
@@ -503,13 +544,17 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
     }
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
-    uint32_t aw[4];
+    uint32_t aw[4];  // pairs of the quarter's tokens; zeros for those that are not this lane's
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = k >> 1, i = 2 * (k & 1);
-      const f16x2_t h = {(_Float16)(p[u][i] * half_at<C::ACT16>(vs[u], i * C::NG + g)),
-                         (_Float16)(p[u][i + 1] * half_at<C::ACT16>(vs[u], (i + 1) * C::NG + g))};
-      aw[k] = __builtin_bit_cast(uint32_t, h);
+    for (int u = 0; u < 2; ++u) {
+      _Float16 a[C::TOK];
+#pragma unroll
+      for (int i = 0; i < C::TOK; ++i) a[i] = (_Float16)(p[u][i] * half_at<C::ACT16>(vs[u], i * C::NG + g));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t both = __builtin_bit_cast(uint32_t, f16x2_t{a[2 * k % C::TOK], a[(2 * k + 1) % C::TOK]});
+        aw[2 * u + k] = C::FOLD == 1 ? both : both & ln.keep[k];
+      }
     }
     const f16x8_t A = as_f16x8(aw[0], aw[1], aw[2], aw[3]);
     constexpr int PIECES = C::VBITS <= 16 ? 1 : C::VBITS / 16;
@@ -649,15 +694,15 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
   const PagedAttnArgs& a = wk.a;
   const KvCache& c = a.c;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int n16 = lane & 15, kq = lane >> 4;
+  const int n16 = lane & 15, kq = lane >> 4, sub = sub_of<C>(lane), head = n16 % C::HEADS;
   float* lds = reinterpret_cast<float*>(smem);
   const int j = unit / wk.htiles, ht = unit - j * wk.htiles;
-  const int h0 = j * wk.share + 16 * ht, gm = min(16, wk.share - 16 * ht);  // this unit's heads
+  const int h0 = j * wk.share + C::HEADS * ht, gm = min(C::HEADS, wk.share - C::HEADS * ht);  // this unit's heads
 
   // q: lane (head n16, quarter kq) holds columns [kq G/4, (kq+1) G/4) of each group
   uint32_t qraw[C::NG][C::G / 8];
   {
-    const uint16_t* q = (const uint16_t*)a.q + (long)b * a.qts + (long)(h0 + min(n16, gm - 1)) * a.qhs;
+    const uint16_t* q = (const uint16_t*)a.q + (long)b * a.qts + (long)(h0 + min(head, gm - 1)) * a.qhs;
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) load_bytes<C::G / 2>((const uint8_t*)(q + g * C::G + kq * (C::G / 4)), qraw[g]);
   }
@@ -689,7 +734,10 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
       if constexpr (C::KB > 16) ln.k[g][1] = (uint32_t)C::at(n16, col + kq * C::KB + 16);
       ln.v[g] = (uint32_t)C::at(4 * kq, col + n16 * C::VBITS / 8);
     }
-    ln.par = (uint32_t)(4 * kq * 2 * C::NG);
+    ln.par = (uint32_t)((4 * kq + C::TOK * sub) * 2 * C::NG);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      ln.keep[k] = (C::TOK * sub / 2 != k) ? 0u : C::FOLD == 4 ? 0xffffu << (16 * (sub & 1)) : ~0u;
     ln.kb = (uint32_t)(n16 * 2 * C::NG);
     // what this lane copies: 16-byte piece 64 m + lane of 16 tokens' codes, and of a stage's parameters
     uint32_t src[C::COPIES];
@@ -748,7 +796,7 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
     for (int g = 0; g < C::NG; ++g)
 #pragma unroll
       for (int k = 0; k < C::G / 8; ++k) asm volatile("" : "+v"(qraw[g][k]));
-    set_q<C>(w, qraw, n16 < gm, kq, a.scale);
+    set_q<C>(w, qraw, head < gm, kq, a.scale);
     // the tiles of the stage being computed: the copies run ahead and may have gone on to the next 32 steps'
     int at_now = at, at_now_from = 0;
     uint32_t buf = 0;
@@ -776,18 +824,22 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
   }
   __syncthreads();
   // join the waves
-  w.l = quads_sum(w.l);
+  w.l = fold_sum<C>(quads_sum(w.l));
   const float m_own = (w.mref == -__builtin_inff() && w.l == w.l) ? -__builtin_inff() : w.mu;
-  if (kq == 0) {
-    msh[wave][n16] = m_own;
-    lsh[wave][n16] = w.l;
+  if (kq == 0 && sub == 0) {
+    msh[wave][head] = m_own;
+    lsh[wave][head] = w.l;
   }
   const int stride = C::D + 4;
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
-    const float bs = quads_sum(w.bias[g]);
-    if (n16 < gm) {
-      float* dst = lds + (wave * gm + n16) * stride + g * C::G + 4 * kq * C::VC;
+    const float bs = fold_sum<C>(quads_sum(w.bias[g]));
+#pragma unroll
+    for (int v = 0; v < C::VC; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.o[g][v][i] = fold_sum<C>(w.o[g][v][i]);
+    if (sub == 0 && head < gm) {
+      float* dst = lds + (wave * gm + head) * stride + g * C::G + 4 * kq * C::VC;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -948,11 +1000,11 @@ size_t attn_lds(int heads) {
   return std::max<size_t>(C::LDS, (size_t)C::WAVES * heads * (C::D + 4) * 4);
 }
 
-template <int D, int G, int BITS, bool F16_>
+template <int D, int G, int BITS, bool F16_, int FOLD>
 hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
-  using C = Cfg<D, G, BITS, F16_, 4>;
+  using C = Cfg<D, G, BITS, F16_, FOLD, 4>;
   // eight waves where their stages fit
-  using S = Cfg<D, G, BITS, F16_, (Cfg<D, G, BITS, F16_, 8>::LDS <= 155 * 1024 ? 8 : 4)>;
+  using S = Cfg<D, G, BITS, F16_, FOLD, (Cfg<D, G, BITS, F16_, FOLD, 8>::LDS <= 155 * 1024 ? 8 : 4)>;
   const PagedAttnArgs& a = w.a;
   const int gm = w.share < 16 ? w.share : 16;
   const int64_t units = (int64_t)a.c.kv_heads * w.htiles;
@@ -996,6 +1048,15 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int D, int G, int BITS, bool F16_>
+hipError_t launch_heads(AttnWork& w, hipStream_t s) {
+  // a head takes as many columns as there are (64 sequences of 4096 tokens, D = 128, G = 64, 4-bit, four heads a key
+  // head: 60.8 us, with one column each 64.1; eight heads: 65.5 and 67.4, with G = 32 80 and 87)
+  return w.share <= 4   ? launch_cfg<D, G, BITS, F16_, 4>(w, s)
+         : w.share <= 8 ? launch_cfg<D, G, BITS, F16_, 2>(w, s)
+                        : launch_cfg<D, G, BITS, F16_, 1>(w, s);
+}
+
 }  // namespace
 
 template <int BITS>
@@ -1005,7 +1066,7 @@ hipError_t launch_paged_attention_bits(const PagedAttnArgs& a, hipStream_t s) {
   w.htiles = (w.share + 15) / 16;
 #define QAFF_ATTN(D, G)                                                            \
   case D * 1000 + G:                                                               \
-    return a.c.dt == F16 ? launch_cfg<D, G, BITS, true>(w, s) : launch_cfg<D, G, BITS, false>(w, s);
+    return a.c.dt == F16 ? launch_heads<D, G, BITS, true>(w, s) : launch_heads<D, G, BITS, false>(w, s);
   switch (a.c.head_dim * 1000 + a.c.G) {
     QAFF_ATTN(64, 32)
     QAFF_ATTN(64, 64)

@@ -90,6 +90,20 @@ def test_head_sizes_groups_widths_types_in_parts(D, G, bits, act):
     _run([700, 0, 33, 260], 3, 1, D, G, bits, 16, act=act, seed=30, max_pages=160)
 
 
+@pytest.mark.parametrize("share", [1, 5, 8, 12])
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 64), (96, 32), (128, 32), (128, 64), (128, 128), (192, 32), (192, 64),
+                                 (256, 32), (256, 64), (256, 128)])
+@pytest.mark.parametrize("bits", [2, 4, 8])
+def test_head_sizes_groups_widths_at_other_sharings(D, G, bits, share):
+    # one launch, and parts; pages outside the cache and windows that begin inside a tile among them
+    act = "f16" if (D // G + bits + share) % 2 else "bf16"
+    _run([70, 5, 161], 2 * share, 2, D, G, bits, 16, act=act, seed=40, window=50)
+    c = Case([700, 0, 33, 260], share, 1, D, G, bits, 16, act=act, seed=41, max_pages=160)
+    c.table[0, 3] = -1
+    c.table[3, 16] = c.pages
+    c.check(qa.paged_attention_affine(*c.args()))
+
+
 @pytest.mark.parametrize("n", [1, 16, 31, 127, 128, 129, 255, 256, 257, 1000, 2559, 2560])
 def test_lengths_in_parts(n):
     _run([n], 4, 2, 128, 64, 4, 16, seed=31, max_pages=160)
