@@ -926,9 +926,9 @@ __global__ __launch_bounds__(64 * C::WAVES, C::WAVES == 4 ? C::PER_CU : 1) void 
   attend<C>(wk, smem, msh, lsh, b, (int)blockIdx.x - b * units, first, first & ~15, len, true, 0);
 }
 
-// Joins the chunks of one sequence and head: 32 lanes by eight groups of chunks.
-template <bool F16_>
-__global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
+// Joins the parts of one sequence and head: 32 lanes by GROUPS groups of parts.
+template <bool F16_, int GROUPS>
+__global__ __launch_bounds__(32 * GROUPS) void paged_attn_join_kernel(AttnWork wk) {
   const PagedAttnArgs& a = wk.a;
   const int b = blockIdx.y, head = blockIdx.x, t = threadIdx.x, D = a.c.head_dim;
   const AttnMeta mt = wk.meta[b];
@@ -936,7 +936,7 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   const uint32_t lead = (uint32_t)wk.meta[a.B].tiles;
   const int j = head / wk.share, ht = (head - j * wk.share) / 16, h = head - j * wk.share - 16 * ht;
   const int gstore = min(16, wk.share);
-  __shared__ float msh[8], osh[8][256 + 4], lsh[8];
+  __shared__ float msh[GROUPS], osh[GROUPS][256 + 4], lsh[GROUPS];
   // the workgroups of this unit's first and last tile
   const uint64_t x0 = (uint64_t)mt.start * (a.c.kv_heads * wk.htiles) +
                       (uint64_t)(j * wk.htiles + ht) * (lead + mt.tiles) + lead;
@@ -947,12 +947,12 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   const int grp = t >> 5, ln = t & 31;
   f32x4_t o[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   float m = -__builtin_inff(), l = 0.f;
-  for (int k0 = grp; k0 < n; k0 += 8 * 4) {  // four parts' loads in flight
+  for (int k0 = grp; k0 < n; k0 += GROUPS * 4) {  // four parts' loads in flight
     f32x2_t ml[4];
     f32x4_t v[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const size_t s = at(min(k0 + 8 * i, n - 1));
+      const size_t s = at(min(k0 + GROUPS * i, n - 1));
       ml[i] = *reinterpret_cast<const f32x2_t*>(wk.part_ml + 2 * s);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -960,7 +960,7 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (k0 + 8 * i >= n || ml[i][0] == -__builtin_inff()) continue;  // (a part that saw nothing)
+      if (k0 + GROUPS * i >= n || ml[i][0] == -__builtin_inff()) continue;  // (a part that saw nothing)
       const float mn = fmaxf(m, ml[i][0]);
       const float fo = __builtin_amdgcn_exp2f(m - mn), fn = __builtin_amdgcn_exp2f(ml[i][0] - mn);
       m = mn;
@@ -982,10 +982,10 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnWork wk) {
   if (t < D) {
     m = msh[0];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) m = fmaxf(m, msh[k]);
+    for (int k = 1; k < GROUPS; ++k) m = fmaxf(m, msh[k]);
     float s = 0.f, ls = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < GROUPS; ++k) {
       const float f = msh[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(msh[k] - m);
       s = fmaf(f, osh[k][t], s);
       ls = fmaf(f, lsh[k], ls);
@@ -1013,14 +1013,17 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   const int64_t tokens = a.window > 0 && a.window < table ? std::min(table, a.window + 15) : table;
   w.part_o = w.part_ml = nullptr;
   w.meta = nullptr;
-  // Short sequences: a workgroup each, no parts, no second kernel.  Up to
-  // 1024 tokens (one sequence of 1024, 4-bit, D = 128: 10.8 against 9.9 us;
-  // 32 of them: 13 against 19), up to 2048 when there is a workgroup for half
-  // the CUs (16 sequences by 8 key heads: 17.9 against 18.5; 32: 21 against
-  // 25).  Eight waves share one, four when there are more than the CUs
-  // (128 sequences of 512 tokens: 24.5 against 32 us).
+  // Short sequences: a workgroup each, no parts, no second kernel.  A step
+  // costs in proportion to D, and the more workgroups, the less the other
+  // kernel gains by cutting sequences: up to 80K columns and tokens a unit, or
+  // 2304 a workgroup (D = 128, 4-bit, 8 units: 576 tokens 8.1 against 8.8 us,
+  // 1024 10.2 against 8.9; 64 units: 1024 10.7 against 11.5, 2048 15.2 against
+  // 14.4; D = 256, 8 units: 320 9.7 against 10.3, 1024 14.1 against 10.5; 256
+  // units: 2048 29 against 33).  Eight waves share a unit, four when there are
+  // more than the CUs (128 sequences of 512 tokens: 24.5 against 32 us).
   const int64_t wgs = units * a.B;
-  if ((tokens <= 1024 || (tokens <= 2048 && wgs >= 128)) && wgs < (1 << 24)) {  // (2^32 threads at most in a launch)
+  const int64_t cost = tokens * D * (8 / S::WAVES);
+  if (tokens <= 2048 && cost <= std::max<int64_t>(80 * 1024, 2304 * wgs) && wgs < (1 << 24)) {  // (2^32 threads at most in a launch)
     if (wgs > 256)
       hipLaunchKernelGGL(paged_attn_short_kernel<C>, dim3((unsigned)wgs), dim3(256), attn_lds<C>(gm), s, w);
     else
@@ -1044,7 +1047,12 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   hipLaunchKernelGGL(paged_attn_kernel<C>, dim3((unsigned)grid), dim3(256), lds, s, w);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(paged_attn_join_kernel<F16_>, dim3((unsigned)a.heads, (unsigned)a.B), dim3(256), 0, s, w);
+  const dim3 rows((unsigned)a.heads, (unsigned)a.B);
+  // more than 32 parts a unit: one round of loads instead of three or four (131072 tokens: 34.6 against 35.1 us)
+  if (grid > 32 * units * a.B)
+    hipLaunchKernelGGL((paged_attn_join_kernel<F16_, 32>), rows, dim3(1024), 0, s, w);
+  else
+    hipLaunchKernelGGL((paged_attn_join_kernel<F16_, 8>), rows, dim3(256), 0, s, w);
   return hipGetLastError();
 }
 

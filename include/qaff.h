@@ -496,11 +496,11 @@ int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void 
  * Accuracy: logits, softmax and sums in fp32; each softmax weight times the
  * value's scale is rounded to 11 bits before the products with the integer
  * codes.  Value scales must stay below 2^110.
- * One launch when the table (with a window, that plus 15) has at most 1024
- * tokens, or at most 2048 and B * kv_heads >= 128 (query heads of a key head
- * past 16 count as another key head); otherwise two, with
- * scratch (2 workgroups' parts a CU, a few MiB): capture such a call after
- * an eager one of the same shapes.  The same call gives the same bits.
+ * One launch, without scratch, for short tables (with a window, short
+ * windows): always up to 160 tokens, never past 2048, between them by
+ * head_dim and batch.  Otherwise two, with scratch (2 workgroups' parts a CU,
+ * a few MiB): capture a call after an eager one of the same shapes.  The same
+ * call gives the same bits.
  */
 int paged_attention_affine(const qaff_kv_cache *cache, const void *q, int64_t q_seq_stride, int64_t q_head_stride,
                            const int32_t *page_table, int64_t table_stride, int64_t max_pages,
