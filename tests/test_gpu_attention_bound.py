@@ -1,0 +1,102 @@
+"""paged_attention_affine against fp64 within the bound that its own roundings
+give (oracle.decoder.attention_bound), half a step of the output's type on top.
+
+Every case first shows on the CPU that its tolerance can tell: the outputs
+with the first or the last token left out, or with a scale 5% off, are past
+it.  For that the first and the last token of each sequence have keys that
+point along a query, so that they hold a good part of its weights."""
+import numpy as np
+import pytest
+import torch
+
+import group_wise_affine_unpack_amd as qa
+import oracle
+import oracle.decoder as od
+from test_gpu_paged_attention import F16_GRAIN, HALF_STEP, Case
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [(64, 32), (64, 64), (96, 32), (128, 32), (128, 64), (128, 128), (192, 32), (192, 64), (256, 32), (256, 64),
+           (256, 128)]
+SHARES = [1, 4, 5, 8, 12, 20]
+
+
+def _mark(c):
+    """First and last tokens' keys along the query of the first head of each key head, by about log(tokens)."""
+    q = oracle.to_f64(c.q, c.act)
+    for b, n in enumerate(c.lens):
+        for t in {0, int(n) - 1} if n > 0 else ():
+            for j in range(c.kvh):
+                row = q[b, j * (c.heads // c.kvh)]
+                cols = min(c.D, int((np.log(n) + 1.5) / 2.2 * np.sqrt(c.D)))
+                at = (c.table[b, t // c.size], j, t % c.size)
+                codes = od.codes(c.k[0][at], c.bits)
+                codes[:cols] = np.where(row[:cols] > 0, 2**c.bits - 1, 0)
+                words = codes.reshape(-1, 32 // c.bits) << (c.bits * np.arange(32 // c.bits))
+                c.k[0][at] = words.sum(-1).astype(np.uint32)
+
+
+def _ref(c, scale=None, window=0, **kw):
+    return od.attention_bound(c.q, c.k, c.v, c.act, c.G, c.bits, c.table, c.lens, c.D**-0.5 if scale is None else scale, window,
+                              **kw)
+
+
+def _check(c, out, scale=None, window=0, what="", planted=True):
+    ref, bound = _ref(c, scale, window)
+    tol = bound * (1 + HALF_STEP[c.act]) + HALF_STEP[c.act] * np.abs(ref) + (F16_GRAIN if c.act == "f16" else 0)
+    if planted:
+        s = c.D**-0.5 if scale is None else scale
+        for name, wrong in (("first", _ref(c, s, window, leave_out=(0,))), ("last", _ref(c, s, window, leave_out=(-1,))),
+                            ("scale", _ref(c, 1.05 * s, window))):
+            told = (np.abs(wrong[0] - ref) > tol).any(axis=2)  # [sequence, head]
+            for b, n in enumerate(c.lens):
+                if n > (1 if name == "scale" else 0):
+                    assert told[b].any(), f"{name} of sequence {b} would pass"
+    err = np.abs(oracle.to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16), c.act) - ref)
+    share = float((err / np.where(tol > 0, tol, 1)).max())
+    print(f"[parity] {what} err {err.max():.2e}, at most {share:.2f} of the tolerance", flush=True)
+    assert (err <= tol).all(), f"{what}: {share} of the tolerance"
+
+
+def _run(*a, window=0, scale=None, planted=True, **kw):
+    print(f"[case] attention bound {a} {kw} window={window}", flush=True)
+    c = Case(*a, **kw)
+    _mark(c)
+    out = qa.paged_attention_affine(*c.args(), scale=scale, window=window)
+    torch.cuda.synchronize()
+    _check(c, out, scale, window, str(a[1:7]), planted)
+
+
+def _cases(shift):
+    for i, (D, G) in enumerate(LAYOUTS):
+        for j, bits in enumerate((2, 4, 8)):
+            yield D, G, bits, SHARES[(i + 2 * j + shift) % 6], ("bf16", "f16")[(i + j + shift) % 2]
+
+
+@pytest.mark.parametrize("D,G,bits,share,act", list(_cases(0)) + list(_cases(3)))
+def test_one_launch(D, G, bits, share, act):
+    _run([70, 5, 161], 2 * share, 2, D, G, bits, 16, act=act, seed=50)
+
+
+@pytest.mark.parametrize("D,G,bits,share,act", list(_cases(1)) + list(_cases(4)))
+def test_parts(D, G, bits, share, act):
+    _run([700, 0, 33, 260], share, 1, D, G, bits, 16, act=act, seed=51, max_pages=160)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 64, 127, 128, 129, 255, 256, 257, 1000, 2559, 2560])
+@pytest.mark.parametrize("max_pages", [None, 160])
+def test_lengths(n, max_pages):
+    _run([n], 4, 2, 128, 64, 4, 16, seed=52, max_pages=max_pages)
+
+
+@pytest.mark.parametrize("heads,kvh,n,bits,act", [(8, 1, 20000, 4, "bf16"), (2, 2, 9001, 4, "f16"), (16, 2, 6000, 8, "bf16"),
+                                                  (5, 1, 7000, 2, "f16")])
+def test_long_sequences(heads, kvh, n, bits, act):
+    _run([n], heads, kvh, 128, 64, bits, 64, act=act, seed=53)
+
+
+@pytest.mark.parametrize("q_std", [8.0, 60.0])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_peaked_softmax(q_std, act):
+    # logits in the tens and hundreds: the few tokens that carry weight are not the marked ones
+    _run([300, 65], 4, 2, 128, 64, 8, 16, act=act, seed=54, q_std=q_std, planted=False)
