@@ -19,7 +19,9 @@
 // the whole conversion: one AND for two codes.  The factors 2^24 and 16 go to
 // q (exact powers of two, per column) and to the outputs.
 // The key biases' part of z is one product more, kb[t,g] by Q_g[h] cut into
-// 16-bit pieces, in the parameters' own type.
+// three 16-bit pieces, in the parameters' own type: 24 bits in bf16; in f16,
+// whose steps end at 2^-24, to 2^-32 of the head's largest query entry, Q_g
+// being taken 2^17 times larger (below 2^15) for that.
 // Registers: C_g has the tokens of a lane's quarter (lane / 16) as rows and
 // the head (lane % 16) as column, which is where the value product takes its
 // second operand from, so p never leaves the lane.  Where a key head has few
@@ -94,6 +96,7 @@ template <int D_, int G_, int BITS_, bool F16_, int FOLD_, int WAVES_>
 struct Cfg {
   static constexpr int D = D_, G = G_, BITS = BITS_, NG = D / G, WAVES = WAVES_;
   static constexpr bool ACT16 = F16_;
+  static constexpr float QSUM = F16_ ? 0x1p17f : 1.f;  // Q_g's factor over the products of codes
   static constexpr int FOLD = FOLD_, HEADS = 16 / FOLD, TOK = 4 / FOLD;  // columns a head, heads, tokens a lane of a quarter's four
   static constexpr int KS = G / 32;                      // product steps a group (keys)
   static constexpr int KB = G / 4 * BITS / 8;            // key code bytes a lane and group
@@ -242,7 +245,7 @@ template <class C>
 struct Wave {
   // constant over the loop
   f16x8_t q[C::NG][C::KS];
-  u32x4_t qsum;           // the key biases' operand: Q_g of this lane's head, a 16-bit piece of it by the lane's quarter
+  u32x4_t qsum;           // the key biases' operand: Q_g of this lane's head (times QSUM), a 16-bit piece of it by the lane's quarter
   float zscale;           // logits to base 2, with q's power of two and the codes' taken back; > 0
   // running
   f32x4_t o[C::NG][C::VC];
@@ -341,8 +344,8 @@ __device__ __forceinline__ void set_q(Wave<C>& w, const uint32_t (&raw)[C::NG][C
       }
       w.q[g][s] = as_f16x8(reg[0], reg[1], reg[2], reg[3]);
     }
-    // Q_g in the units of the products of codes, cut into 16-bit pieces: quarter 0 holds the leading one
-    float left = quads_sum(sum) * 0x1p-24f;
+    // Q_g in QSUM'ths of the products of codes, cut into 16-bit pieces: quarter 0 holds the leading one
+    float left = quads_sum(sum) * (0x1p-24f * C::QSUM);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const uint16_t piece = f32_to_act_bits(left, C::ACT16);
@@ -479,7 +482,7 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
     }
 #pragma unroll
     for (int i = 0; i < C::TOK; ++i) {
-      z[u][i] = own<C>(zb, i, sub);
+      z[u][i] = own<C>(zb, i, sub) * (1.f / C::QSUM);
 #pragma unroll
       for (int g = 0; g < C::NG; ++g) z[u][i] = fmaf(half_at<C::ACT16>(ks[u], i * C::NG + g), own<C>(acc[g], i, sub), z[u][i]);
     }

@@ -12,6 +12,7 @@ import torch
 import group_wise_affine_unpack_amd as qa
 import oracle
 import oracle.decoder as od
+import synth_inputs as si
 from test_gpu_paged_attention import F16_GRAIN, HALF_STEP, Case
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,23 @@ def test_long_sequences(heads, kvh, n, bits, act):
 def test_peaked_softmax(q_std, act):
     # logits in the tens and hundreds: the few tokens that carry weight are not the marked ones
     _run([300, 65], 4, 2, 128, 64, 8, 16, act=act, seed=54, q_std=q_std, planted=False)
+
+
+def _offset_keys(c, rng, wide, offset):
+    """Queries of a wide pair of channels in each group that nearly cancel, and key biases that vary by thousands: the biases'
+    part of a logit is a small difference, to which the sums of q have to be known."""
+    q = rng.standard_normal(c.q.shape).reshape(*c.q.shape[:2], -1, c.G)
+    q[..., 2:] *= wide / 4000
+    q[..., 0], q[..., 1] = wide, -wide
+    c.q = si.store(q.reshape(c.q.shape).astype(np.float32), c.act)
+    b = oracle.to_f64(c.k[2], c.act)
+    c.k[2][:] = si.store((b + offset * (1 + 0.3 * rng.standard_normal(b.shape))).astype(np.float32), c.act)
+
+
+@pytest.mark.parametrize("pages", [None, 160])
+@pytest.mark.parametrize("D,G,bits,share,act", [(128, 64, 4, 4, "f16"), (128, 32, 8, 8, "f16"), (64, 32, 2, 12, "f16"),
+                                                (256, 128, 4, 1, "f16"), (96, 32, 8, 20, "f16"), (128, 64, 4, 4, "bf16")])
+def test_key_biases_far_from_zero(D, G, bits, share, act, pages):
+    c = Case([200, 40, 150], share, 1, D, G, bits, 16, act=act, seed=55, max_pages=pages)
+    _offset_keys(c, np.random.default_rng(55), 5.0, 3000.0)
+    _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share} {act}", planted=False)
