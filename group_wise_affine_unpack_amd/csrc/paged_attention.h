@@ -12,7 +12,7 @@
 //              z[t,h]   = c (sum_g ks[t,g] C_g[t,h] + kb[t,g] Q_g[h])
 //              with Q_g[h] = sum_{d in group g} q[d,h]
 //     values   o[d,h] = sum_t code[t,d] A_g[t,h] + sum_t vb[t,g] p[t,h]
-//              with A_g[t,h] = p[t,h] vs[t,g] rounded to f16
+//              with A_g[t,h] = p[t,h] vs[t,g], times a power of two, rounded to f16
 // Codes: an f16 whose exponent bits are zero is its low ten bits times 2^-24,
 // and the matrix cores keep such numbers, so masking a code where it lies in
 // bits 0-9 of each 16-bit half (4-bit: bits 0-3 and, times 16, bits 4-7) is
@@ -35,12 +35,23 @@
 // q is scaled by a power of two per head so that its largest entry lies in
 // [2^14, 2^15): exact for f16 queries and, below 2^-29 of the largest, off by
 // at most 2^-39 of it for bf16 ones.
-// The softmax's reference mu is the largest logit seen plus the exponent of
-// the largest value scale seen, p = 2^(z - mu + 5): A stays below 2^15 while
-// z grows by no more than 4 and vs by no more than 2^6, so most steps need
-// neither a maximum over the lanes nor a rescaling; a step that passes the
-// limits (a wave-uniform branch) sets a new mu.  A's smallest step is 2^-24,
-// 2^-30 of the largest term.
+// The softmax's reference mu is the largest logit seen, rounded up to a whole
+// number, and p = 2^(z - mu - 30): sums of p vb and of p vs code then stay
+// finite for any number of tokens.  A_g's power of two is each head's and
+// group's own, from the products p vs of that group seen: it brings a wave's
+// largest to 2^4 or more, so a weight keeps its 11 bits down to 2^-18 of the
+// largest and is off by at most 2^-29 of it below.  (A power of two from the
+// largest logit and the largest scale by themselves loses the weights' bits
+// where a token with a scale far above the others has no weight, and where
+// one group's scales lie far below another's.)  Most steps need neither a
+// maximum over the lanes nor a rescaling: a wave's first one takes the value
+// scales of its largest logit's token, and only one in which a logit passes
+// mu by 4 or an A reaches 2^15 (wave-uniform branches) sets mu or the powers
+// of two anew.  (With 2^8 for 2^4 the second kind is so frequent that 16
+// sequences up to 4096 tokens take 18.5 us for 17.7; without the first step's
+// own, 17.9.  A power of two of each group costs one product a weight over one
+// of all groups: 64 sequences of 4096 tokens 61.2 -> 62.0 us at 4 bits and four
+// heads a key head, 84.7 -> 90.4 at twenty, whose columns hold no spare tokens.)
 //
 // Memory: each wave copies the 32 tokens after the ones at work straight
 // into LDS (16 bytes a lane, no register between, non-temporal: with the
@@ -74,9 +85,11 @@
 namespace qaff {
 namespace {
 
-constexpr float PBIAS = 5.f;    // log2 of p at the reference
-constexpr float MROOM = 4.f;    // how far a logit may pass the reference (log2)
-constexpr int VROOM = 6;        // how far a value scale may pass its power of two (log2)
+constexpr float PBIAS = -30.f;     // log2 of p at the reference
+constexpr float MROOM = 4.f;       // how far a logit may pass the reference (log2)
+constexpr int ATOP = 4;            // log2 of the largest A of a group at a new power of two
+constexpr uint32_t ALIM = 0x7800;  // f16 of 2^15, which no A may pass
+constexpr int VEMIN = -100, VEMAX = 120;  // exponents of A's power of two (sums times 2^24 / it stay finite)
 
 struct AttnMeta {
   int64_t start;  // a sequence's start on the line of one unit
@@ -116,15 +129,19 @@ struct Cfg {
   // batch of 64 sequences up to 8192 tokens 75 against 67 us.)
   static constexpr int STAGES = 2, LDS = WAVES * STAGES * STAGE;
   // Registers of a step: accumulators, q, what it reads of a stage, and about
-  // 64 more (the compiler takes up to 25 on top).  Past 240, values are read after the softmax (LATE).
+  // 64 more (the compiler takes up to 25 on top).  Past 240, values are read
+  // after the softmax (LATE), and where that makes room for a third workgroup
+  // a CU (D = 96, G = 32, 4-bit, 20 heads a key head: 124 us for 136).
   static constexpr int KEYS = 2 * NG * KW + 2 * BW + 2 * SW, VALS = 4 * SW + 8 * NG * VW;
-  static constexpr bool LATE = D / 4 + D / 8 + KEYS + VALS + 64 > 240;
+  static constexpr int ALL = D / 4 + D / 8 + 64 + KEYS + VALS;
+  static constexpr bool LATE = ALL > 240 || (ALL > 168 && ALL <= 176 && LDS * 3 <= 155 * 1024);
   static constexpr int REGS =
-      D / 4 + D / 8 + 64 + (LATE ? (KEYS > 4 * SW + 8 * VW ? KEYS : 4 * SW + 8 * VW) : KEYS + VALS);
+      LATE ? D / 4 + D / 8 + 64 + (KEYS > 4 * SW + 8 * VW ? KEYS : 4 * SW + 8 * VW) : ALL;
   // workgroups of four waves a CU, by LDS and registers (one more than the registers hold spills: D = 128, G = 32,
   // 4-bit, 16 heads, 3 instead of 2: five times the time; D = 256, G = 32, 2-bit, 2 instead of 1: 288 against 191 us.
-  // Four where REGS <= 116, D = 64: the same time)
-  static constexpr int PER_CU = LDS * 3 <= 155 * 1024 && REGS <= 165   ? 3
+  // Four where D = 64 leaves room, G = 64, 4-bit, 20 heads: 100 us, with three 108)
+  static constexpr int PER_CU = LDS * 4 <= 155 * 1024 && REGS <= 118   ? 4
+                                : LDS * 3 <= 155 * 1024 && REGS <= 165 ? 3
                                 : LDS * 2 <= 155 * 1024 && REGS <= 228 ? 2
                                                                        : 1;
   static constexpr int COPIES = (CODES + 1023) / 1024, PCOPIES = (8 * PARAMS + 1023) / 1024;
@@ -250,8 +267,8 @@ struct Wave {
   // running
   f32x4_t o[C::NG][C::VC];
   float l, bias[C::NG];   // sums over this lane's tokens
-  float mref, mu, mlim, vexp;
-  uint32_t vlim;          // bits of the 16-bit value scale that may not be passed
+  float ve[C::NG];        // A's power of two
+  float mref, mu, mlim;
 };
 
 // 16 bytes a lane from memory into LDS, without a register between: lane l's
@@ -384,42 +401,135 @@ __device__ __forceinline__ float fold_max(float v) {
   return v;
 }
 
-// New references for the heads of this wave, and everything summed so far
-// brought to them.
+// whether `x` holds in some lane, as one scalar
+__device__ __forceinline__ bool any_lane(bool x) {
+  const uint64_t b = __builtin_amdgcn_ballot_w64(x);
+  uint32_t any = (uint32_t)b | (uint32_t)(b >> 32);
+  asm volatile("" : "+s"(any));
+  return any != 0;
+}
+
+__device__ __forceinline__ int exponent(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }
+
+// maximum of pairs of 16-bit numbers over the lanes of a head
 template <class C>
-__device__ __forceinline__ void rescale(Wave<C>& w, const uint32_t (&vs)[2][C::SW], float zmax) {
-  float vm = 0.f;
+__device__ __forceinline__ uint32_t head_max_u16(uint32_t v) {
+  auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = pk_max_u16(r[0], r[1]);
+  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = pk_max_u16(r[0], r[1]);
+  if constexpr (C::FOLD >= 2) v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+  if constexpr (C::FOLD >= 4) v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  return v;
+}
+
+// A new reference for the logits of the heads of this wave, and everything
+// summed so far brought to it.
+template <class C>
+__device__ __forceinline__ void raise(Wave<C>& w, const float (&z)[2][C::TOK], const uint32_t (&vs)[2][C::SW], float zmax) {
+  const float top = fold_max<C>(quads_max(zmax));
+  const float m = fmaxf(w.mref, ceilf(top)), mu = m == -__builtin_inff() ? 0.f : m;
+  const bool fresh = w.mref == -__builtin_inff();  // nothing is summed yet
+  const int rise = fresh ? 300 : (int)fminf(mu - w.mu, 300.f);  // (an infinite logit makes its row NaN)
+  const float f = __builtin_amdgcn_ldexpf(1.f, -rise);
+  // the value scales of the largest logit's token
+  uint32_t s[C::BW];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int k = 0; k < C::BW; ++k) {
+    s[k] = 0;
 #pragma unroll
-    for (int i = 0; i < C::SW; ++i) {
-      // (opaque: shared with the unpacking after the branch, these would put a second side to it)
-      uint32_t word = vs[u][i];
-      asm("" : "+v"(word));
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float v = fabsf(half_at<C::ACT16>(&word, k));
-        vm = fmaxf(vm, v < __builtin_inff() ? v : 0.f);  // (one that is not finite makes its own columns so)
+      for (int i = 0; i < C::TOK; ++i) {
+        uint32_t x;  // groups 2 k and 2 k + 1 of the token
+        if constexpr (C::NG % 2 == 0)
+          x = vs[u][i * (C::NG / 2) + k];
+        else {
+          const int e = i * C::NG + 2 * k;
+          const uint32_t lo = (e & 1) ? vs[u][e / 2] >> 16 : vs[u][e / 2] & 0xffffu;
+          x = 2 * k + 1 < C::NG ? lo | ((e & 1) ? vs[u][(e + 1) / 2] << 16 : vs[u][e / 2] & 0xffff0000u) : lo;
+        }
+        s[k] = pk_max_u16(s[k], z[u][i] * w.zscale == top ? x & 0x7fff7fffu : 0u);
       }
-    }
-  vm = fold_max<C>(quads_max(vm));
-  const float m = fmaxf(w.mref, fold_max<C>(quads_max(zmax)));
-  // the exponent of the largest scale, kept where 2^(5 - mu) and its sums stay finite
-  const float e = fmaxf(w.vexp, fminf(fmaxf((float)((int)(__float_as_uint(vm) >> 23) - 127), -90.f), 110.f));
-  const float mu = (m == -__builtin_inff() ? 0.f : m) + e;
-  const float alpha = w.mref == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(w.mu - mu);
+    s[k] = head_max_u16<C>(s[k]);
+  }
   w.mref = m;
   w.mu = mu;
   w.mlim = m + MROOM;
-  w.vexp = e;
-  const float lim = __builtin_amdgcn_ldexpf(1.f, (int)e + VROOM);
-  w.vlim = C::ACT16 ? (lim < 65504.f ? f32_to_f16_bits(lim) : 0x7bffu) : __float_as_uint(lim) >> 16;
-  w.l *= alpha;
+  int e[C::NG];
+  bool past = false;
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
-    w.bias[g] *= alpha;
+    w.bias[g] *= f;
+    // the sums of A stay as they are for a power of two that grows by as much; the first one is that of the largest
+    // logit's token, whose p is at most a factor of two below the reference
+    e[g] = fresh ? ATOP + 1 - (int)PBIAS - exponent(half_at<C::ACT16>(s, g)) : exponent(w.ve[g]) + rise;
+    past |= !fresh && e[g] > VEMAX;
+    w.ve[g] = __builtin_amdgcn_ldexpf(1.f, max(min(e[g], VEMAX), VEMIN));
+  }
+  w.l *= f;
+  if (any_lane(past)) {  // (what was summed is nothing beside what comes)
 #pragma unroll
-    for (int c = 0; c < C::VC; ++c) w.o[g][c] *= alpha;
+    for (int g = 0; g < C::NG; ++g) {
+      const float fo = __builtin_amdgcn_ldexpf(1.f, fresh ? 0 : min(VEMAX - e[g], 0));
+#pragma unroll
+      for (int c = 0; c < C::VC; ++c) w.o[g][c] *= fo;
+    }
+  }
+}
+
+// A of this lane's tokens of a step: pairs of tokens of each 16, a token twice where the lane has one.
+template <class C>
+struct Weights {
+  static constexpr int W = C::TOK == 4 ? 2 : 1;
+  uint32_t a[C::NG][2 * W];
+};
+template <class C>
+__device__ __forceinline__ void weights(const float (&p)[2][C::TOK], const uint32_t (&vs)[2][C::SW], int g, float ve,
+                                        uint32_t (&out)[2 * Weights<C>::W]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    _Float16 a[C::TOK];
+#pragma unroll
+    for (int i = 0; i < C::TOK; ++i) a[i] = (_Float16)(p[u][i] * ve * half_at<C::ACT16>(vs[u], i * C::NG + g));
+#pragma unroll
+    for (int k = 0; k < Weights<C>::W; ++k)
+      out[Weights<C>::W * u + k] = __builtin_bit_cast(uint32_t, f16x2_t{a[2 * k % C::TOK], a[(2 * k + 1) % C::TOK]});
+  }
+}
+
+// A's powers of two anew where its limit is passed, and the sums of A brought to them.
+template <class C>
+__device__ __forceinline__ void retarget(Wave<C>& w, const float (&p)[2][C::TOK], const uint32_t (&vs)[2][C::SW],
+                                         Weights<C>& x) {
+#pragma unroll
+  for (int g = 0; g < C::NG; ++g) {
+    // (opaque, and a group after the other: shared with the weights before the branch these would put a second side
+    // to it, and all groups' at once take the registers of a workgroup a CU)
+    uint32_t s[2][C::SW];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < C::SW; ++i) {
+        s[u][i] = vs[u][i];
+        asm volatile("" : "+v"(s[u][i]));
+      }
+    float most = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < C::TOK; ++i) {
+        const float v = fabsf(p[u][i] * half_at<C::ACT16>(s[u], i * C::NG + g));
+        most = fmaxf(most, v < __builtin_inff() ? v : 0.f);  // (one that is not finite makes its own columns so)
+      }
+    most = fold_max<C>(quads_max(most));
+    const int from = exponent(w.ve[g]), to = max(min(ATOP - exponent(most), from), VEMIN);
+    const float f = __builtin_amdgcn_ldexpf(1.f, to - from);
+    w.ve[g] = __builtin_amdgcn_ldexpf(1.f, to);
+#pragma unroll
+    for (int c = 0; c < C::VC; ++c) w.o[g][c] *= f;
+    weights<C>(p, s, g, w.ve[g], x.a[g]);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -513,14 +623,21 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
 #pragma unroll
   for (int i = 1; i < C::TOK; ++i) zmax = fmaxf(zmax, fmaxf(z[0][i], z[1][i]));
   zmax *= w.zscale;
-  uint32_t vmax = vs[0][0];
+  if (any_lane(zmax > w.mlim)) raise<C>(w, z, vs, zmax);
+  const float off = PBIAS - w.mu;
 #pragma unroll
-  for (int i = 1; i < 2 * C::SW; ++i) vmax = pk_max_u16(vmax, vs[i / C::SW][i % C::SW]);
-  vmax = max(vmax >> 16, vmax & 0xffffu);  // (a scale below zero has its top bit set and passes every limit)
-  const uint64_t pass = __builtin_amdgcn_ballot_w64(zmax > w.mlim || vmax > w.vlim);
-  uint32_t any = (uint32_t)pass | (uint32_t)(pass >> 32);
-  asm volatile("" : "+s"(any));
-  if (any) rescale<C>(w, vs, zmax);
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < C::TOK; ++i) p[u][i] = __builtin_amdgcn_exp2f(fmaf(z[u][i], w.zscale, off));
+  Weights<C> x;
+#pragma unroll
+  for (int g = 0; g < C::NG; ++g) weights<C>(p, vs, g, w.ve[g], x.a[g]);
+  uint32_t amax = x.a[0][0];
+#pragma unroll
+  for (int i = 1; i < 2 * Weights<C>::W * C::NG; ++i)
+    amax = pk_max_u16(amax, x.a[i / (2 * Weights<C>::W)][i % (2 * Weights<C>::W)]);
+  // (a scale below zero sets the top bit and passes the limit every time)
+  if (any_lane(max(amax >> 16, amax & 0xffffu) > ALIM)) retarget<C>(w, p, vs, x);
   if constexpr (C::LATE) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_bytes<2 * C::TOK * C::NG>(st + 4 * C::CODES + (u * 4 + 3) * C::PARAMS + ln.par, vb[u]);
@@ -534,12 +651,10 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
           if (!counts(u, i, at)) hide(vb[u], i);
     }
   }
-  const float off = PBIAS - w.mu;
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int i = 0; i < C::TOK; ++i) {
-      p[u][i] = __builtin_amdgcn_exp2f(fmaf(z[u][i], w.zscale, off));
       w.l += p[u][i];
 #pragma unroll
       for (int g = 0; g < C::NG; ++g)
@@ -549,16 +664,9 @@ __device__ __forceinline__ void step(Wave<C>& w, const uint8_t* st, const Lanes<
   for (int g = 0; g < C::NG; ++g) {
     uint32_t aw[4];  // pairs of the quarter's tokens; zeros for those that are not this lane's
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      _Float16 a[C::TOK];
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < C::TOK; ++i) a[i] = (_Float16)(p[u][i] * half_at<C::ACT16>(vs[u], i * C::NG + g));
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t both = __builtin_bit_cast(uint32_t, f16x2_t{a[2 * k % C::TOK], a[(2 * k + 1) % C::TOK]});
-        aw[2 * u + k] = C::FOLD == 1 ? both : both & ln.keep[k];
-      }
-    }
+      for (int k = 0; k < 2; ++k) aw[2 * u + k] = C::FOLD == 1 ? x.a[g][2 * u + k] : x.a[g][u] & ln.keep[k];
     const f16x8_t A = as_f16x8(aw[0], aw[1], aw[2], aw[3]);
     constexpr int PIECES = C::VBITS <= 16 ? 1 : C::VBITS / 16;
     if constexpr (C::LATE) {
@@ -713,14 +821,13 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
     w.bias[g] = 0.f;
+    w.ve[g] = __builtin_amdgcn_ldexpf(1.f, VEMAX);
 #pragma unroll
     for (int v = 0; v < C::VC; ++v) w.o[g][v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   w.l = 0.f;
   w.mref = w.mlim = -__builtin_inff();
   w.mu = 0.f;
-  w.vexp = -90.f;
-  w.vlim = 0u;
 
   // this wave's steps: tokens begin + 32 (wave + WAVES i)
   const int t0 = begin + 32 * wave;
@@ -836,7 +943,7 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
   const int stride = C::D + 4;
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
-    const float bs = fold_sum<C>(quads_sum(w.bias[g]));
+    const float bs = fold_sum<C>(quads_sum(w.bias[g])), back = 0x1p24f / w.ve[g];
 #pragma unroll
     for (int v = 0; v < C::VC; ++v)
 #pragma unroll
@@ -847,7 +954,7 @@ __device__ __forceinline__ void attend(const AttnWork& wk, uint8_t* smem, float 
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int v = 0; v < C::VC; ++v)
-          dst[i * C::VC + v] = fmaf(w.o[g][v][i], 0x1p24f / (float)(1 << value_shift<C>(v)), bs);
+          dst[i * C::VC + v] = fmaf(w.o[g][v][i], back / (float)(1 << value_shift<C>(v)), bs);
     }
   }
   __syncthreads();

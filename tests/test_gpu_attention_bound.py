@@ -121,3 +121,69 @@ def test_key_biases_far_from_zero(D, G, bits, share, act, pages):
     c = Case([200, 40, 150], share, 1, D, G, bits, 16, act=act, seed=55, max_pages=pages)
     _offset_keys(c, np.random.default_rng(55), 5.0, 3000.0)
     _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share} {act}", planted=False)
+
+
+def _at(c, b, t):
+    return c.table[b, t // c.size], slice(None), t % c.size
+
+
+def _set_logits(c, b, ts, z):
+    """Keys that give the tokens `ts` a logit of about z in every head (of queries above zero)."""
+    for t in ts:
+        c.k[1][_at(c, b, t)] = 0
+        c.k[2][_at(c, b, t)] = si.store(np.full((c.kvh, c.D // c.G), z / (0.8 * np.sqrt(c.D)), np.float32), c.act)
+
+
+def _set_values(c, b, ts, factor):
+    """The value scales of the tokens `ts` (a group each in `factor`, if it has several) times a power of two."""
+    for t in ts:
+        for part in (1, 2):
+            x = oracle.to_f64(c.v[part][_at(c, b, t)], c.act)
+            c.v[part][_at(c, b, t)] = si.store((x * np.asarray(factor)).astype(np.float32), c.act)
+
+
+def _positive_case(lens, share, D, G, bits, act, pages, seed):
+    c = Case(lens, share, 1, D, G, bits, 16, act=act, seed=seed, max_pages=pages, scale_spread=0.1)
+    c.q = si.store(np.abs(oracle.to_f64(c.q, act)).astype(np.float32), act)
+    return c
+
+
+KINDS = [(128, 64, 4, 4), (128, 32, 8, 8), (64, 32, 2, 12), (256, 128, 4, 1), (256, 32, 2, 4), (96, 32, 8, 20)]
+
+
+@pytest.mark.parametrize("pages", [None, 160])
+@pytest.mark.parametrize("act,far", [("f16", 13), ("bf16", 40)])
+@pytest.mark.parametrize("D,G,bits,share", KINDS)
+def test_a_large_scale_without_weight(D, G, bits, share, act, far, pages):
+    # one token whose value scales stand far above all others and whose logit is far below them: early, in the middle, last
+    c = _positive_case([256, 256, 256], share, D, G, bits, act, pages, 56)
+    for b, t in enumerate((0, 100, 255)):
+        _set_values(c, b, set(range(256)) - {t}, 2.0**-8)
+        _set_values(c, b, [t], 2.0**far / 256 if act == "bf16" else 2.0**far)
+        _set_logits(c, b, [t], -100.0)
+    _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share} {act}", planted=False)
+
+
+@pytest.mark.parametrize("pages", [None, 160])
+@pytest.mark.parametrize("act,far", [("f16", 22), ("bf16", 50)])
+@pytest.mark.parametrize("D,G,bits,share", KINDS[:2] + KINDS[4:])
+def test_groups_of_scales_far_apart(D, G, bits, share, act, far, pages):
+    # every token's weights count in every group, wide or narrow
+    c = _positive_case([256, 40, 17], share, D, G, bits, act, pages, 57)
+    factor = 2.0**(10 - np.linspace(0, far, D // G))[None]
+    for b, n in enumerate(c.lens):
+        _set_values(c, b, range(n), factor)
+    _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share} {act}", planted=False)
+
+
+@pytest.mark.parametrize("pages", [None, 160])
+@pytest.mark.parametrize("D,G,bits,share", KINDS)
+def test_large_scales_whose_weight_is_gone_later(D, G, bits, share, pages):
+    # the first tokens' scales are large and lead at their time; then the logits rise by steps
+    c = _positive_case([900, 500], share, D, G, bits, "bf16", pages, 58)
+    for b, n in enumerate(c.lens):
+        _set_values(c, b, range(40), 2.0**30)
+        _set_logits(c, b, range(0, 40), -150.0)
+        _set_logits(c, b, range(40, n // 3), -75.3)
+        _set_logits(c, b, range(n // 3, n // 2), -37.7)
+    _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share}", planted=False)

@@ -67,7 +67,7 @@ def _kernel(case, q_units, own_groups):
     p = np.exp2((z - z.max()).astype(f)).astype(f)
     w = p[:, None] * vs
     if own_groups:
-        ref = np.floor(np.log2(np.abs(w).max(0))) - 8
+        ref = np.floor(np.log2(np.abs(w).max(0))) - 4
     else:
         ref = np.full(D // G, np.floor(np.log2(np.abs(vs).max())) - 5)
     A = (w * np.exp2(-ref).astype(f)).astype(np.float16).astype(f)
