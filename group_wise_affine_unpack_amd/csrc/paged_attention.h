@@ -1118,8 +1118,9 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   const PagedAttnArgs& a = w.a;
   const int gm = w.share < 16 ? w.share : 16;
   const int64_t units = (int64_t)a.c.kv_heads * w.htiles;
-  // the most tokens a sequence can see, with the rest of the window's first 16-token tile
+  // the most tokens a sequence can see, and with them the rest of the window's first 16-token tile
   const int64_t table = (int64_t)a.max_pages * a.c.page_size;
+  const int64_t seen = a.window > 0 ? std::min(table, a.window) : table;
   const int64_t tokens = a.window > 0 && a.window < table ? std::min(table, a.window + 15) : table;
   w.part_o = w.part_ml = nullptr;
   w.meta = nullptr;
@@ -1129,11 +1130,13 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
   // 2304 a workgroup (D = 128, 4-bit, 8 units: 576 tokens 8.1 against 8.8 us,
   // 1024 10.2 against 8.9; 64 units: 1024 10.7 against 11.5, 2048 15.2 against
   // 14.4; D = 256, 8 units: 320 9.7 against 10.3, 1024 14.1 against 10.5; 256
-  // units: 2048 29 against 33).  Eight waves share a unit, four when there are
+  // units: 2048 29 against 33).  Always up to 160 tokens, which callers who
+  // capture a first call rely on.  Eight waves share a unit, four when there are
   // more than the CUs (128 sequences of 512 tokens: 24.5 against 32 us).
   const int64_t wgs = units * a.B;
   const int64_t cost = tokens * D * (8 / S::WAVES);
-  if (tokens <= 2048 && cost <= std::max<int64_t>(80 * 1024, 2304 * wgs) && wgs < (1 << 24)) {  // (2^32 threads at most in a launch)
+  if (tokens <= 2048 && (seen <= 160 || cost <= std::max<int64_t>(80 * 1024, 2304 * wgs)) &&
+      wgs < (1 << 24)) {  // (2^32 threads at most in a launch)
     if (wgs > 256)
       hipLaunchKernelGGL(paged_attn_short_kernel<C>, dim3((unsigned)wgs), dim3(256), attn_lds<C>(gm), s, w);
     else

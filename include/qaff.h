@@ -500,7 +500,8 @@ int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void 
  * group's are below 2^-84, fewer bits are kept.
  * One launch, without scratch, for short tables (with a window, short
  * windows): always up to 160 tokens, never past 2048, between them by
- * head_dim and batch.  Otherwise two, with scratch (2 workgroups' parts a CU,
+ * head_dim and batch; B * kv_heads * ceil(heads / kv_heads / 16) below 2^24
+ * in any case.  Otherwise two, with scratch (2 workgroups' parts a CU,
  * a few MiB): capture a call after an eager one of the same shapes.  The same
  * call gives the same bits.
  */
