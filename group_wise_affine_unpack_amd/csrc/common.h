@@ -108,15 +108,17 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
   return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
 }
+// (a NaN in any lane reaches every lane)
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max_f32(float v) {
-  v = fmaxf(v, dpp_mov<0x128>(v));
-  v = fmaxf(v, dpp_mov<0x124>(v));
-  v = fmaxf(v, dpp_mov<0x122>(v));
-  v = fmaxf(v, dpp_mov<0x121>(v));
+  v = nan_max(v, dpp_mov<0x128>(v));
+  v = nan_max(v, dpp_mov<0x124>(v));
+  v = nan_max(v, dpp_mov<0x122>(v));
+  v = nan_max(v, dpp_mov<0x121>(v));
   auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  v = nan_max(__uint_as_float(r[0]), __uint_as_float(r[1]));
   r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return nan_max(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 }  // namespace qaff

@@ -5,6 +5,7 @@
 //     dense:  y = n rounded once
 //     codes:  s_x = max_k |n| / 127 (IEEE division),
 //             x_q = clamp(rint(n / s_x), -127, 127), zeros when s_x == 0
+//             (a NaN among the n makes s_x NaN, so that products with it are)
 // The norm reads h as stored, so the residual stream and the norm agree.
 // The squares are taken and summed in fp64 (each is exact there, and none
 // overflows) and rstd is rounded once to fp32: the sum's order then leaves rstd's
@@ -23,9 +24,10 @@ __device__ __forceinline__ float half_of(uint32_t w, int h) {
   else return __uint_as_float(h ? w & 0xffff0000u : w << 16);
 }
 
-// (mean square + eps)^-1/2 in fp64, rounded once
+// (mean square + eps)^-1/2 in fp64, rounded once; with codes 0 for a row of zeros, whose n are zeros then without an eps too
+template <bool CODES>
 __device__ __forceinline__ float rstd_of(double sum, const NormArgs& a) {
-  return (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
+  return CODES && sum == 0.0 ? 0.f : (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
 }
 
 // x_q = clamp(rint(n / s), -127, 127), 0 when s == 0, the division IEEE
@@ -113,7 +115,7 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_rows_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < WPR; ++k) sum += sums[wave - sub + k];
   }
-  const float rstd = rstd_of(sum, a);
+  const float rstd = rstd_of<CODES>(sum, a);
   auto n_of = [&](int i, int j) {
     float wv;
     if constexpr (W32)
@@ -140,14 +142,14 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_rows_kernel(NormArgs a) {
     for (int i = 0; i < CPT; ++i)
       if (in_row && c0 + 64 * WPR * i < K8)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(n_of(i, j)));
+        for (int j = 0; j < 8; ++j) mx = nan_max(mx, fabsf(n_of(i, j)));
     mx = wave_max_f32(mx);
     if constexpr (WPR > 1) {
       if ((t & 63) == 0) maxs[wave] = mx;
       __syncthreads();
       mx = 0.f;
 #pragma unroll
-      for (int k = 0; k < WPR; ++k) mx = fmaxf(mx, maxs[wave - sub + k]);
+      for (int k = 0; k < WPR; ++k) mx = nan_max(mx, maxs[wave - sub + k]);
     }
     const float s = __fdiv_rn(mx, 127.f);
     if (in_row && c0 == 0) a.s_x[m] = s;
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
   if ((t & 63) == 0) sums[t >> 6] = sum;
   __syncthreads();
   sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-  const float rstd = rstd_of(sum, a);
+  const float rstd = rstd_of<CODES>(sum, a);
   const uint16_t* hs = r ? ho : x;  // each thread reads back what it wrote
   auto n_of = [&](int k) { return __fmul_rn(__fmul_rn(load_as_f32(hs, k, DT), rstd), load_as_f32(a.w, k, a.w_dt)); };
   if constexpr (!CODES) {
@@ -207,11 +209,11 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
     for (int k = t; k < K; k += 256) y[k] = f32_to_act_bits(n_of(k), F16_);
   } else {
     float mx = 0.f;
-    for (int k = t; k < K; k += 256) mx = fmaxf(mx, fabsf(n_of(k)));
+    for (int k = t; k < K; k += 256) mx = nan_max(mx, fabsf(n_of(k)));
     mx = wave_max_f32(mx);
     if ((t & 63) == 0) maxs[t >> 6] = mx;
     __syncthreads();
-    mx = fmaxf(fmaxf(maxs[0], maxs[1]), fmaxf(maxs[2], maxs[3]));
+    mx = nan_max(nan_max(maxs[0], maxs[1]), nan_max(maxs[2], maxs[3]));
     const float s = __fdiv_rn(mx, 127.f);
     if (t == 0) a.s_x[m] = s;
     for (int k = t; k < K; k += 256) a.x_q[m * K + k] = (int8_t)code_of(n_of(k), s);

@@ -395,8 +395,10 @@ int qgemm_w4a8_codes(const int8_t *x_q, const float *s_x, const uint32_t *w_q4, 
  *   K >= 1; strides >= K; eps >= 0 and finite.  Any alignment of 2 bytes
  *   (16-byte aligned rows with K % 8 == 0 run faster).  The products and
  *   divisions are IEEE fp32 and the sum is fp64, so outputs do not depend on
- *   the launch.  A NaN in h makes its row's dense values NaN; the codes of a
- *   row that holds a NaN or an infinity are unspecified.
+ *   the launch.  A NaN or an infinity in h makes its row's dense values NaN
+ *   (an infinity: its own, the others zeros of their sign) and its s_x NaN, a
+ *   weight that is not finite every s_x; such rows' codes are unspecified but
+ *   keep to [-127, 127], so qgemm_w4a8_codes gives rows that are not finite.
  */
 int rmsnorm(const void *x, const void *resid, const void *weight, double eps, void *h_out, void *y, int64_t M,
             int64_t K, int64_t x_stride, int64_t resid_stride, int64_t h_stride, int32_t act_dtype, int32_t w_dtype,
