@@ -132,13 +132,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-# the current device, and the current stream's handle without making a torch.cuda.Stream (1.7 us of a 6 us call)
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _stream(device) -> int:
-    return _raw_stream(device.index)
+    # without making a torch.cuda.Stream (1.7 us of a 6 us call); looked up here, since a torch built without a GPU has
+    # no such name and this module is imported there too
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -157,12 +154,11 @@ def _u32(t: torch.Tensor) -> torch.Tensor:
 def _run(name: str, device, *args) -> None:
     """Calls an entry point on the current stream of `device`, with `device` the current one (a launch goes there)."""
     f = getattr(_lib or lib(), name)
-    index = device.index
-    if index == _current_device():
-        st = f(*args, _raw_stream(index))
+    if device.index == torch._C._cuda_getDevice():
+        st = f(*args, _stream(device))
     else:
         with torch.cuda.device(device):
-            st = f(*args, _raw_stream(index))
+            st = f(*args, _stream(device))
     if st != 0:
         _check(st, name)
 
