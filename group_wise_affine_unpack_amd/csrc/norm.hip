@@ -8,9 +8,11 @@
 //             (a NaN among the n makes s_x NaN, so that products with it are)
 // The norm reads h as stored, so the residual stream and the norm agree.
 // The squares are taken and summed in fp64 (each is exact there, and none
-// overflows) and rstd is rounded once to fp32: the sum's order then leaves rstd's
-// bits, and so the codes, unchanged.  Every other step is one IEEE fp32
-// operation.
+// overflows) and rstd is rounded once to fp32.  The sum's order moves it by
+// K 2^-53 of itself at most, so two orders round to the same rstd, and so to
+// the same outputs, but for a rstd within 2^-15 of a step (K = 16384) from a
+// rounding boundary, one row in 16384 at worst and far fewer in practice.
+// Every other step is one IEEE fp32 operation.
 #include <algorithm>
 
 #include "common.h"
@@ -28,6 +30,15 @@ __device__ __forceinline__ float half_of(uint32_t w, int h) {
 template <bool CODES>
 __device__ __forceinline__ float rstd_of(double sum, const NormArgs& a) {
   return CODES && sum == 0.0 ? 0.f : (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
+}
+
+// h rstd w, each product rounded to fp32.  (The barrier keeps the second one
+// from being folded into a rounding to f16, one v_fma_mix: dense outputs would
+// then depend on the compiler.)
+__device__ __forceinline__ float n_value(float h, float rstd, float w) {
+  float n = __fmul_rn(__fmul_rn(h, rstd), w);
+  asm("" : "+v"(n));
+  return n;
 }
 
 // x_q = clamp(rint(n / s), -127, 127), 0 when s == 0, the division IEEE
@@ -122,7 +133,7 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_rows_kernel(NormArgs a) {
       wv = __uint_as_float(w[i][j / 4][j & 3]);
     else
       wv = a.w_dt == F16 ? half_of<true>(w[i][0][j / 2], j & 1) : half_of<false>(w[i][0][j / 2], j & 1);
-    return __fmul_rn(__fmul_rn(half_of<F16_>(h[i][j / 2], j & 1), rstd), wv);
+    return n_value(half_of<F16_>(h[i][j / 2], j & 1), rstd, wv);
   };
   if constexpr (!CODES) {
 #pragma unroll
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(256) void rmsnorm_any_kernel(NormArgs a) {
   sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   const float rstd = rstd_of<CODES>(sum, a);
   const uint16_t* hs = r ? ho : x;  // each thread reads back what it wrote
-  auto n_of = [&](int k) { return __fmul_rn(__fmul_rn(load_as_f32(hs, k, DT), rstd), load_as_f32(a.w, k, a.w_dt)); };
+  auto n_of = [&](int k) { return n_value(load_as_f32(hs, k, DT), rstd, load_as_f32(a.w, k, a.w_dt)); };
   if constexpr (!CODES) {
     uint16_t* y = (uint16_t*)a.y + m * K;
     for (int k = t; k < K; k += 256) y[k] = f32_to_act_bits(n_of(k), F16_);

@@ -394,8 +394,10 @@ int qgemm_w4a8_codes(const int8_t *x_q, const float *s_x, const uint32_t *w_q4, 
  *   y, x_q  [M, K] dense;  s_x [M] f32.  They must not overlap the inputs.
  *   K >= 1; strides >= K; eps >= 0 and finite.  Any alignment of 2 bytes
  *   (16-byte aligned rows with K % 8 == 0 run faster).  The products and
- *   divisions are IEEE fp32 and the sum is fp64, so outputs do not depend on
- *   the launch.  A NaN or an infinity in h makes its row's dense values NaN
+ *   divisions are IEEE fp32 and the sum is fp64, in an order that K and the
+ *   alignment choose: the same call gives the same bits, and one of another
+ *   alignment too, unless rstd falls next to a rounding boundary of fp32
+ *   (within K 2^-53 of itself).  A NaN or an infinity in h makes its row's dense values NaN
  *   (an infinity: its own, the others zeros of their sign) and its s_x NaN, a
  *   weight that is not finite every s_x; such rows' codes are unspecified but
  *   keep to [-127, 127], so qgemm_w4a8_codes gives rows that are not finite.
