@@ -175,7 +175,10 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, uint16_t* __res
       for (int k2 = 0; k2 < 2; ++k2) {
         const int m = 2 * j + k2;
         const uint32_t q = BITS == 8 ? (w[u][m / 4] >> (8 * (m & 3))) & 255u : (w[u][0] >> (BITS * m)) & ((1u << BITS) - 1u);
-        e[k2] = f32_to_act_bits(__fmaf_rn((float)q, s, b), F16_);
+        float value = __fmaf_rn((float)q, s, b);
+        // (the compiler would fold it into the rounding to f16 and leave its own out: 8-bit codes, one value in 10^6)
+        if constexpr (F16_) asm("" : "+v"(value));
+        e[k2] = f32_to_act_bits(value, F16_);
       }
       o[j] = e[0] | e[1] << 16;
     }
