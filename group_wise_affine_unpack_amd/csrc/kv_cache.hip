@@ -8,6 +8,7 @@
 //          quantize_pack_affine gives that row
 //   read:  code*scale + bias in fp32 (the product is exact, the sum rounded),
 //          then rounded to the activation type
+// A NaN takes no part in its group's minimum and maximum and gets code 0.
 // A slot outside the cache is not written, and reads as zeros.
 // One thread per 8 columns (one 16-byte load or store of the dense row); the
 // G/8 threads of a group are neighbouring lanes.
@@ -94,7 +95,11 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows r, con
   if (slot < 0 || slot >= c.num_slots) return;  // (a group's lanes together: they share the token)
   float x[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = act_to_f32<F16_>(raw[j / 2] >> (16 * (j & 1)));
+  for (int j = 0; j < 8; ++j) {
+    x[j] = act_to_f32<F16_>(raw[j / 2] >> (16 * (j & 1)));
+    // a signaling NaN would make the minimum so far a NaN, and the next value then the minimum: only quiet ones take no part
+    if constexpr (!F16_) x[j] = __builtin_canonicalizef(x[j]);  // (f16's conversion has made them quiet)
+  }
   float lo = __builtin_inff(), hi = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

@@ -442,7 +442,9 @@ typedef struct qaff_kv_cache {
 /*
  * kv_cache_append_affine - quantize the keys and values of T tokens into
  * their slots.  Each row gets the codes, scales and biases, bit for bit,
- * that quantize_pack_affine gives that row (w_dtype = sb_dtype = dtype).
+ * that quantize_pack_affine gives that row (w_dtype = sb_dtype = dtype).  A
+ * NaN takes no part in its group's minimum and maximum and gets code 0 (a
+ * signaling one too: as quantize_pack_affine has it for a quiet one).
  *   k, v   [T, kv_heads, head_dim] dtype, 16-byte aligned; token and head
  *          strides in elements, multiples of 8 (0 is a broadcast): the
  *          slices of a fused q/k/v product need no copy
