@@ -29,3 +29,31 @@ def test_short_calls_are_captured_without_an_eager_one(D, G, bits, window, pages
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
     assert qa.release_workspaces() == 0
+
+
+def test_the_largest_batch():
+    # 65535 sequences: one launch, and shares of the line with a join over all of them (a table of more than 2048 tokens)
+    c = Case([32, 1, 17, 0, 29], 4, 2, 64, 64, 4, 16, seed=61, max_pages=2)
+    q, cache, table, lens = c.args()
+    B = 65535
+    at = torch.arange(B, device=c.dev) % 5
+    few = qa.paged_attention_affine(q, cache, table, lens)
+    long = torch.full((5, 130), -1, dtype=torch.int32, device=c.dev)
+    long[:, :2] = table
+    for t in (table, long):
+        out = qa.paged_attention_affine(q[at], cache, t[at], lens[at])
+        torch.cuda.synchronize()
+        assert torch.equal(out, few[at])
+    with pytest.raises(qa.QaffError):
+        qa.paged_attention_affine(q[torch.arange(B + 1, device=c.dev) % 5], cache, table[torch.arange(B + 1, device=c.dev) % 5],
+                                  lens[torch.arange(B + 1, device=c.dev) % 5])
+
+
+@pytest.mark.parametrize("pages", [3, 160])
+def test_queries_shared_by_heads_and_sequences(pages):
+    # strides of 0: one query for all heads, or for all sequences
+    c = Case([48, 33, 5], 8, 2, 64, 64, 4, 16, seed=62, max_pages=pages)
+    q, cache, table, lens = c.args()
+    for view in (q[:, :1].expand(3, 8, 64), q[:1].expand(3, 8, 64), q[:1, :1].expand(3, 8, 64)):
+        assert torch.equal(qa.paged_attention_affine(view, cache, table, lens),
+                           qa.paged_attention_affine(view.contiguous(), cache, table, lens))
