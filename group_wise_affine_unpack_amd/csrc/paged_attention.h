@@ -35,9 +35,10 @@
 // q is scaled by a power of two per head so that its largest entry lies in
 // [2^14, 2^15): exact for f16 queries and, below 2^-29 of the largest, off by
 // at most 2^-39 of it for bf16 ones.
-// The softmax's reference mu is the largest logit seen, rounded up to a whole
-// number, and p = 2^(z - mu - 30): sums of p vb and of p vs code then stay
-// finite for any number of tokens.  A_g's power of two is each head's and
+// The softmax's reference mu is the largest logit seen when it was set (p of
+// that token is a power of two, and its weights A exact), and
+// p = 2^(z - mu - 30): sums of p vb and of p vs code then stay finite for any
+// number of tokens.  A_g's power of two is each head's and
 // group's own, from the products p vs of that group seen: it brings a wave's
 // largest to 2^4 or more, so a weight keeps its 11 bits down to 2^-18 of the
 // largest and is off by at most 2^-29 of it below.  (A power of two from the
@@ -428,10 +429,10 @@ __device__ __forceinline__ uint32_t head_max_u16(uint32_t v) {
 template <class C>
 __device__ __forceinline__ void raise(Wave<C>& w, const float (&z)[2][C::TOK], const uint32_t (&vs)[2][C::SW], float zmax) {
   const float top = fold_max<C>(quads_max(zmax));
-  const float m = fmaxf(w.mref, ceilf(top)), mu = m == -__builtin_inff() ? 0.f : m;
+  const float m = fmaxf(w.mref, top), mu = m == -__builtin_inff() ? 0.f : m;
   const bool fresh = w.mref == -__builtin_inff();  // nothing is summed yet
-  const int rise = fresh ? 300 : (int)fminf(mu - w.mu, 300.f);  // (an infinite logit makes its row NaN)
-  const float f = __builtin_amdgcn_ldexpf(1.f, -rise);
+  const float fall = w.mu - mu, f = fresh ? 0.f : __builtin_amdgcn_exp2f(fall);  // (an infinite logit makes its row NaN)
+  const int rise = (int)fminf(floorf(mu) - floorf(w.mu), 300.f);  // in whole powers of two, without a drift
   // the value scales of the largest logit's token
   uint32_t s[C::BW];
 #pragma unroll
@@ -456,25 +457,22 @@ __device__ __forceinline__ void raise(Wave<C>& w, const float (&z)[2][C::TOK], c
   w.mref = m;
   w.mu = mu;
   w.mlim = m + MROOM;
-  int e[C::NG];
-  bool past = false;
+  float fo[C::NG];
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
     w.bias[g] *= f;
-    // the sums of A stay as they are for a power of two that grows by as much; the first one is that of the largest
-    // logit's token, whose p is at most a factor of two below the reference
-    e[g] = fresh ? ATOP + 1 - (int)PBIAS - exponent(half_at<C::ACT16>(s, g)) : exponent(w.ve[g]) + rise;
-    past |= !fresh && e[g] > VEMAX;
-    w.ve[g] = __builtin_amdgcn_ldexpf(1.f, max(min(e[g], VEMAX), VEMIN));
+    // A's power of two grows by as much; the first one is that of the largest logit's token, whose p is 2^PBIAS
+    const int e = fresh ? ATOP - (int)PBIAS - exponent(half_at<C::ACT16>(s, g)) : exponent(w.ve[g]) + rise;
+    const float ve = __builtin_amdgcn_ldexpf(1.f, max(min(e, VEMAX), VEMIN));
+    fo[g] = fresh ? 1.f : __builtin_amdgcn_exp2f(fall + (float)(exponent(ve) - exponent(w.ve[g])));
+    w.ve[g] = ve;
   }
   w.l *= f;
-  if (any_lane(past)) {  // (what was summed is nothing beside what comes)
+  if (any_lane(!fresh)) {
 #pragma unroll
-    for (int g = 0; g < C::NG; ++g) {
-      const float fo = __builtin_amdgcn_ldexpf(1.f, fresh ? 0 : min(VEMAX - e[g], 0));
+    for (int g = 0; g < C::NG; ++g)
 #pragma unroll
-      for (int c = 0; c < C::VC; ++c) w.o[g][c] *= fo;
-    }
+      for (int c = 0; c < C::VC; ++c) w.o[g][c] *= fo[g];
   }
 }
 
