@@ -33,22 +33,22 @@
 // tokens' codes of the same columns are put into the halves of one register
 // first.
 // q is scaled by a power of two per head so that its largest entry lies in
-// [2^14, 2^15): exact for f16 queries and, below 2^-29 of the largest, off by
-// at most 2^-39 of it for bf16 ones.
+// [2^14, 2^15): entries are exact down to 2^-22 of the largest (2^-28 for 8-bit
+// codes, whose factors are 1) and off by at most 2^-33 of it below.
 // The softmax's reference mu is the largest logit seen when it was set (p of
 // that token is a power of two, and its weights A exact), and
 // p = 2^(z - mu - 30): sums of p vb and of p vs code then stay finite for any
-// number of tokens.  A_g's power of two is each head's and
-// group's own, from the products p vs of that group seen: it brings a wave's
-// largest to 2^4 or more, so a weight keeps its 11 bits down to 2^-18 of the
-// largest and is off by at most 2^-29 of it below.  (A power of two from the
-// largest logit and the largest scale by themselves loses the weights' bits
-// where a token with a scale far above the others has no weight, and where
-// one group's scales lie far below another's.)  Most steps need neither a
+// number of tokens.  A_g's power of two is each head's and group's own, from
+// the products p vs of that group seen: it brings a wave's largest to 2^3 or
+// more, so a weight keeps its 11 bits down to 2^-17 of the largest and is off
+// by at most 2^-28 of it below.  (A power of two from the largest logit and
+// the largest scale by themselves loses the weights' bits where a token with a
+// scale far above the others has no weight, and where one group's scales lie
+// far below another's.)  Most steps need neither a
 // maximum over the lanes nor a rescaling: a wave's first one takes the value
 // scales of its largest logit's token, and only one in which a logit passes
 // mu by 4 or an A reaches 2^15 (wave-uniform branches) sets mu or the powers
-// of two anew.  (With 2^8 for 2^4 the second kind is so frequent that 16
+// of two anew.  (With 2^7 for 2^3 the second kind is so frequent that 16
 // sequences up to 4096 tokens take 18.5 us for 17.7; without the first step's
 // own, 17.9.  A power of two of each group costs one product a weight over one
 // of all groups: 64 sequences of 4096 tokens 61.2 -> 62.0 us at 4 bits and four

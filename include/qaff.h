@@ -501,7 +501,7 @@ int kv_cache_read_affine(const qaff_kv_cache *cache, const int64_t *slots, void 
  * with that sequence (in a value's group, with that group's columns).
  * Accuracy: logits, softmax and sums in fp32; each softmax weight times the
  * value's scale is rounded to 11 bits before the products with the integer
- * codes, or to 2^-29 of the largest such product of its head and group of
+ * codes, or to 2^-28 of the largest such product of its head and group of
  * columns where that is more.  Value scales must stay below 2^110; where a
  * group's are below 2^-84, fewer bits are kept.
  * One launch, without scratch, for short tables (with a window, short

@@ -116,7 +116,7 @@ def attention_bound(q, k, v, dtype: str, G: int, bits: int, table, lens, scale: 
               largest.  c: three roundings, the same for every token.
       weight  p = 2^(z - ref): u of the argument's size (the distance from the
               largest logit, and 64), 2 u for the power.
-      sums    each weight p s rounded to 11 bits, 2^-11 relative, or 2^-29 of
+      sums    each weight p s rounded to 11 bits, 2^-11 relative, or 2^-28 of
               the group's largest p s; products with code summed, 2 u for
               each 8 tokens; sum p b and sum p a rounding a token and lane.
     An error d of a token's logit moves the output by p d (v - out).  Errors
@@ -172,7 +172,7 @@ def attention_bound(q, k, v, dtype: str, G: int, bits: int, table, lens, scale: 
                 # sums
                 w = p[:, None] * va
                 err += 2.0**-11 * (1 + 2.0**-10) * np.minimum(w.sum(0), lam * root(w))
-                err += 2.0**-29 * np.repeat((p[:, None] * np.abs(vs)).max(0), G) * np.minimum(vc.sum(0), lam * root(vc))
+                err += 2.0**-28 * np.repeat((p[:, None] * np.abs(vs)).max(0), G) * np.minimum(vc.sum(0), lam * root(vc))
                 steps = n / 8 + 32
                 err += lam * np.sqrt(steps) * 2 * u * w.sum(0)
                 err += lam * np.sqrt(2 * steps) * u * (p @ vb + np.abs(o)) + 32 * u * (w.sum(0) + p @ vb)
