@@ -139,11 +139,12 @@ struct Cfg {
   static constexpr int REGS =
       LATE ? D / 4 + D / 8 + 64 + (KEYS > 4 * SW + 8 * VW ? KEYS : 4 * SW + 8 * VW) : ALL;
   // workgroups of four waves a CU, by LDS and registers (one more than the registers hold spills: D = 128, G = 32,
-  // 4-bit, 16 heads, 3 instead of 2: five times the time; D = 256, G = 32, 2-bit, 2 instead of 1: 288 against 191 us.
+  // 4-bit, 16 heads, 3 instead of 2: five times the time; D = 256, G = 32, 2-bit, 2 instead of 1: 288 against 191 us,
+  // with eight heads 99 against 93.
   // Four where D = 64 leaves room, G = 64, 4-bit, 20 heads: 100 us, with three 108)
   static constexpr int PER_CU = LDS * 4 <= 155 * 1024 && REGS <= 118   ? 4
                                 : LDS * 3 <= 155 * 1024 && REGS <= 165 ? 3
-                                : LDS * 2 <= 155 * 1024 && REGS <= 228 ? 2
+                                : LDS * 2 <= 155 * 1024 && REGS <= 228 && !(LATE && REGS + NG > 206) ? 2
                                                                        : 1;
   static constexpr int COPIES = (CODES + 1023) / 1024, PCOPIES = (8 * PARAMS + 1023) / 1024;
   // rows of 2^n 16-byte pieces keep piece c of row r at c ^ swizzle(r), so that a piece of many rows is spread over the banks
