@@ -91,6 +91,9 @@ class QaffError(RuntimeError):
 
 
 _lib = None
+# the current device, and the current stream's handle without making a torch.cuda.Stream (1.7 us of a 6 us call): set by
+# lib(), None where torch is built without a GPU and has no such names
+_current_device = _raw_stream = None
 
 
 def library_path() -> str:
@@ -99,7 +102,7 @@ def library_path() -> str:
 
 def lib():
     """The loaded libqaff.so (ctypes), with argument types declared."""
-    global _lib
+    global _lib, _current_device, _raw_stream
     if _lib is None:
         if not os.path.exists(_LIB_PATH):
             raise RuntimeError(f"{_LIB_PATH} is not built; run __graft_entry__.build() (hipcc, gfx950)")
@@ -113,6 +116,8 @@ def lib():
         L.qaff_version.restype = C.c_int
         L.qaff_release_workspaces.restype = C.c_int
         L.qaff_release_workspaces.argtypes = [C.POINTER(C.c_uint64)]
+        _current_device = getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _lib = L
     return _lib
 
@@ -133,9 +138,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    # without making a torch.cuda.Stream (1.7 us of a 6 us call); looked up here, since a torch built without a GPU has
-    # no such name and this module is imported there too
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(device.index)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -154,11 +157,12 @@ def _u32(t: torch.Tensor) -> torch.Tensor:
 def _run(name: str, device, *args) -> None:
     """Calls an entry point on the current stream of `device`, with `device` the current one (a launch goes there)."""
     f = getattr(_lib or lib(), name)
-    if device.index == torch._C._cuda_getDevice():
-        st = f(*args, _stream(device))
+    index = device.index
+    if index == _current_device():
+        st = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = f(*args, _stream(device))
+            st = f(*args, _raw_stream(index))
     if st != 0:
         _check(st, name)
 
