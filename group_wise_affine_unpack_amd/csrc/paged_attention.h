@@ -62,9 +62,9 @@
 // to 16 bytes a step.
 // What bounds it: at 8 bits memory (64 sequences of 4096 tokens, D = 128:
 // 571 MB in 95 us, 6.0 TB/s), at 4 bits the waits of 12 waves a CU on their
-// copies and on each other's vector instructions, 237 a step of 4.6 KB with
-// four heads a key head (302 MB in 59 to 62 us, 5.0 TB/s; vector pipes busy
-// 58% of the time), for few tokens the chain lengths -> page table -> rows ->
+// copies and on each other's vector instructions, 250 a step of 4.6 KB with
+// four heads a key head (302 MB in 60 to 62 us, 4.9 TB/s; vector pipes busy
+// 62% of the time), for few tokens the chain lengths -> page table -> rows ->
 // join.
 // Measured and not kept: operands loaded from memory into registers with one
 // step of look-ahead (70 us for those 302 MB where the copies took 64), three
@@ -1171,7 +1171,7 @@ hipError_t launch_cfg(AttnWork& w, hipStream_t s) {
 template <int D, int G, int BITS, bool F16_>
 hipError_t launch_heads(AttnWork& w, hipStream_t s) {
   // a head takes as many columns as there are (64 sequences of 4096 tokens, D = 128, G = 64, 4-bit, four heads a key
-  // head: 60.8 us, with one column each 64.1; eight heads: 65.5 and 67.4, with G = 32 80 and 87)
+  // head: 60.8 us, with one column each 69.3; eight heads: 67.4 and 73.4, with G = 32 86 and 95)
   return w.share <= 4   ? launch_cfg<D, G, BITS, F16_, 4>(w, s)
          : w.share <= 8 ? launch_cfg<D, G, BITS, F16_, 2>(w, s)
                         : launch_cfg<D, G, BITS, F16_, 1>(w, s);
