@@ -522,7 +522,7 @@ __device__ __forceinline__ void retarget(Wave<C>& w, const float (&p)[2][C::TOK]
         most = fmaxf(most, v < __builtin_inff() ? v : 0.f);  // (one that is not finite makes its own columns so)
       }
     most = fold_max<C>(quads_max(most));
-    const int from = exponent(w.ve[g]), to = max(min(ATOP - exponent(most), from), VEMIN);
+    const int from = exponent(w.ve[g]), e = exponent(most), to = from + e < 15 ? from : max(ATOP - e, VEMIN);
     const float f = __builtin_amdgcn_ldexpf(1.f, to - from);
     w.ve[g] = __builtin_amdgcn_ldexpf(1.f, to);
 #pragma unroll

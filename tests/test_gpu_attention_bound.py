@@ -187,3 +187,20 @@ def test_large_scales_whose_weight_is_gone_later(D, G, bits, share, pages):
         _set_logits(c, b, range(40, n // 3), -75.3)
         _set_logits(c, b, range(n // 3, n // 2), -37.7)
     _check(c, qa.paged_attention_affine(*c.args()), what=f"{D} {G} {bits} {share}", planted=False)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("share", [4, 12])
+@pytest.mark.parametrize("pages", [57, 160])
+def test_a_value_scale_that_is_not_finite_leaves_other_groups_their_bits(pages, share, bad):
+    # among many steps: new powers of two for its group are none for the others
+    c = Case([900, 500], share, 1, 128, 32, 4, 16, seed=59, max_pages=pages, scale_spread=2.0)
+    q, cache, table, lens = c.args()
+    clean = qa.paged_attention_affine(q, cache, table, lens)
+    for t in (0, 70, 450, 899):
+        cache.v[1][c.table[0, t // 16], 0, t % 16, 1] = bad
+    out = qa.paged_attention_affine(q, cache, table, lens)
+    assert torch.equal(out[1], clean[1])
+    other = [i for i in range(128) if i // 32 != 1]
+    assert torch.equal(out[0][:, other], clean[0][:, other])
+    assert not torch.isfinite(out[0, :, 32:64]).all()
