@@ -204,3 +204,28 @@ def test_a_value_scale_that_is_not_finite_leaves_other_groups_their_bits(pages, 
     other = [i for i in range(128) if i // 32 != 1]
     assert torch.equal(out[0][:, other], clean[0][:, other])
     assert not torch.isfinite(out[0, :, 32:64]).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G,bits,share", KINDS)
+@pytest.mark.parametrize("pages", [1, 160])
+def test_a_single_token_is_its_value(D, G, bits, share, act, pages):
+    # the largest logit's weights are exact: code * scale + bias, with eight roundings of fp32 (products, sums, joins, the
+    # quotient) before the one to the type.  Its p is a power of two but for the roundings of its argument z - mu - 30,
+    # which the division by p shows where A's rounding has taken them back: with |z| < 98 (base 2) mu, which is z rounded,
+    # and -30 - mu are off by at most 2^-18 each and their sum, about -30, by 2^-20: 9 * 2^-20, times log 2 below 7 * 2^-20
+    c = Case([1, 1, 1], share, 1, D, G, bits, 16, act=act, seed=63, max_pages=pages)
+    out = qa.paged_attention_affine(*c.args())
+    torch.cuda.synchronize()
+    at = c.table[:, 0], 0, 0
+    packed, scales, biases = (t[at] for t in c.v)
+    want = od.values(packed, scales, biases, act, G, bits)[:, None]
+    size = (od.codes(packed, bits) * np.repeat(np.abs(oracle.to_f64(scales, act)), G, -1)
+            + np.repeat(np.abs(oracle.to_f64(biases, act)), G, -1))[:, None]
+    got = oracle.to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16), act)
+    keys = od.values(*(t[at] for t in c.k), act, G, bits)
+    z = np.einsum("bhd,bd->bh", oracle.to_f64(c.q, act), keys) * D**-0.5 / np.log(2)
+    assert np.abs(z).max() < 98
+    near = (8 * 2.0**-24 + 7 * 2.0**-20) * size
+    tol = HALF_STEP[act] * np.abs(want) + near * (1 + HALF_STEP[act]) + (F16_GRAIN if act == "f16" else 0)
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
