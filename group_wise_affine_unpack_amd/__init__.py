@@ -9,7 +9,8 @@ Functions mirror the C entry points:
     qmm_affine, qgemv_affine, qgemv_affine_grouped, qmm_gptq, qgemm_w4a8,
     gptq_to_affine_repack, quantize_pack_affine, rmsnorm, rmsnorm_w4a8,
     qgemm_w4a8_codes, kv_cache_append_affine, kv_cache_read_affine,
-    paged_attention_affine
+    paged_attention_affine, kv_pages_assign, kv_pages_trim, rotary,
+    kv_cache_append_rotary_affine
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ import torch
 __all__ = ["QaffError", "qmm_affine", "qmm_affine_noalloc", "qgemv_affine", "qgemv_affine_grouped", "GroupedGemv", "qmm_gptq", "qgemm_w4a8", "qgemm_w4a8_tiled", "gptq_to_affine_repack",
            "quantize_pack_affine", "dequantize_affine", "qgemv_affine_silu_gate", "smoothquant_factors",
            "w4a8_quantize_weights", "qgemm_w4a8_smooth", "qgemm_w4a8_codes", "rmsnorm", "rmsnorm_w4a8", "AffineKVCache",
-           "kv_cache_append_affine", "kv_cache_read_affine", "paged_attention_affine",
+           "kv_cache_append_affine", "kv_cache_read_affine", "paged_attention_affine", "KVPagePool", "kv_pages_assign",
+           "kv_pages_trim", "Rotary", "rotary", "kv_cache_append_rotary_affine",
            "release_workspaces", "GemvChain", "library_path", "lib",
            "STATUS", "DTYPE"]
 
@@ -57,6 +59,11 @@ _SIGS = {
     "kv_cache_read_affine": [_VP] * 4 + [_I64, _VP],
     "paged_attention_affine": [_VP, _VP] + [_I64] * 2 + [_VP] + [_I64] * 2 + [_VP] * 2 + [_I64, _I32, C.c_double, _I64,
                                                                                        _VP],
+    "kv_pages_assign": [_VP] + [_I64] * 2 + [_VP] * 5 + [_I64, _I32, _I64] + [_VP] * 3 + [_I64, _VP],
+    "kv_pages_trim": [_VP] + [_I64] * 2 + [_VP] * 5 + [_I64, _I32, _I64, _VP],
+    "rotary_frequencies": [_VP, _I32, C.c_double, _I32] + [C.c_double] * 4 + [_VP],
+    "rotary": [_VP] + [_VP, _I64, _I64] * 4 + [_VP, _I64] + [_I32] * 4 + [_VP],
+    "kv_cache_append_rotary_affine": [_VP] * 2 + [_VP, _I64, _I64] * 4 + [_VP] * 2 + [_I64, _I32, _VP],
     "qaff_stream_read": [_VP, C.c_uint64, _VP, _I32, _VP],
     "qgemv_affine_chain_plan": [_VP, _I32, _I32, _I32, _I32, C.POINTER(_VP)],
     "qgemv_affine_chain_run": [_VP, _VP],
@@ -82,6 +89,11 @@ class KVCacheArrays(C.Structure):
     _fields_ = [(n, _VP) for n in ("k_packed", "k_scales", "k_biases", "v_packed", "v_scales", "v_biases")] + \
                [("num_pages", _I64)] + \
                [(n, _I32) for n in ("page_size", "kv_heads", "head_dim", "group_size", "bits", "dtype")]
+
+
+class RotarySpec(C.Structure):
+    """qaff_rotary (include/qaff.h)."""
+    _fields_ = [("inv_freq", _VP), ("rotary_dim", _I32), ("interleaved", _I32), ("magnitude", C.c_double)]
 
 
 class QaffError(RuntimeError):
@@ -187,7 +199,7 @@ def _out(out: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
 
 def _row_ptr(t: torch.Tensor) -> int:
     """Address of a tensor whose last dimension is dense; the others go by their strides."""
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError("the last dimension must be contiguous")
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
@@ -581,6 +593,139 @@ def paged_attention_affine(q: torch.Tensor, cache: AffineKVCache, page_table: to
     _run("paged_attention_affine", dev, cache.ref, _row_ptr(q), *_strides(q), _row_ptr(page_table),
          page_table.stride(0) if B > 1 else per, per, _ptr(seq_lens), _ptr(o), B, heads,
          D ** -0.5 if scale is None else scale, window)
+    return o
+
+
+class KVPagePool:
+    """The free pages of a paged cache: a stack that kv_pages_assign takes from and kv_pages_trim returns to.
+
+    free_pages [num_pages] int32, of which the first state[0] are free; state
+    [4] int32: free pages, pages short at the last assign, the library's word.
+    Made with every page free, page 0 on top.
+    """
+
+    def __init__(self, num_pages: int, page_size: int, device="cuda"):
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.free_pages = torch.arange(self.num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+        self.state[0] = self.num_pages
+        self.device = self.free_pages.device
+
+
+def _pages(fn: str, pool: KVPagePool, page_table, seq_lens, other, lens_out, *outputs):
+    dev = pool.device
+    B, per = page_table.shape
+    if (page_table.device != dev or seq_lens.shape != (B,) or seq_lens.device != dev or other.shape != (B,)
+            or other.device != dev):
+        _check_shapes(pool.state, page_table=(page_table, (B, per)), lengths=(seq_lens, (B,)), new_or_kept=(other, (B,)))
+    if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32 or other.dtype != torch.int32:
+        raise ValueError("page_table and lengths must be int32")
+    free, state = pool.free_pages, pool.state
+    if (free.shape != (pool.num_pages,) or state.shape != (4,) or free.dtype != torch.int32 or state.dtype != torch.int32
+            or free.device != dev or state.device != dev):
+        raise ValueError("the pool's free_pages and state must stay as they were made")
+    lens_out = _out(lens_out, seq_lens)
+    _run(fn, dev, _row_ptr(page_table), page_table.stride(0) if B > 1 else per, per, _ptr(seq_lens), _ptr(other),
+         _ptr(lens_out), _ptr(free), _ptr(state), pool.num_pages, pool.page_size, B, *outputs)
+    return lens_out
+
+
+def kv_pages_assign(pool: KVPagePool, page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, rows: int,
+                    lens_out: Optional[torch.Tensor] = None):
+    """Pages for new_lens [B] int32 further tokens of every sequence: (slots int64, positions int32, seq_ids int32 [rows], lens).
+
+    page_table [B, max_pages] int32 (rows dense) gets the new pages; lens [B]
+    are the lengths with them (lens_out, which may be seq_lens itself).  Rows
+    lists the new tokens sequence by sequence; the ones behind the last get
+    slot -1, position 0 and sequence -1.
+    """
+    new = pool.state.new_empty
+    slots, positions, seq_ids = new(rows, dtype=torch.int64), new(rows), new(rows)
+    lens = _pages("kv_pages_assign", pool, page_table, seq_lens, new_lens, lens_out, slots.data_ptr(), positions.data_ptr(),
+                  seq_ids.data_ptr(), rows)
+    return slots, positions, seq_ids, lens
+
+
+def kv_pages_trim(pool: KVPagePool, page_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
+                  lens_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Every sequence keeps its first keep_lens [B] tokens (0: it ends); the pages behind them return to the pool."""
+    return _pages("kv_pages_trim", pool, page_table, seq_lens, keep_lens, lens_out)
+
+
+ROTARY_SCALINGS = {None: 0, "linear": 1, "base": 2, "bands": 3}
+
+
+class Rotary:
+    """Rotary positions (qaff_rotary): inv_freq [rotary_dim / 2] float64 on the GPU, radians a position of each pair.
+
+    Pairs are columns (j, j + rotary_dim / 2), or (2j, 2j + 1) when
+    interleaved; magnitude multiplies both turned tensors.  Holds a reference
+    to inv_freq.  `Rotary.make` computes the frequencies.
+    """
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0):
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a vector of float64")
+        self.inv_freq, self.interleaved, self.magnitude = inv_freq, bool(interleaved), float(magnitude)
+        self.rotary_dim, self.device = 2 * inv_freq.shape[0], inv_freq.device
+        self.spec = RotarySpec(_ptr(inv_freq), self.rotary_dim, int(self.interleaved), self.magnitude)
+        self.ref = C.addressof(self.spec)
+
+    @classmethod
+    def make(cls, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None,
+             factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 4.0, magnitude: float = 1.0,
+             device="cuda") -> "Rotary":
+        """base^(-2j / rotary_dim), scaled: None, "linear", "base" or "bands" (rotary_frequencies in include/qaff.h)."""
+        if scaling not in ROTARY_SCALINGS:
+            raise ValueError(f"unknown scaling {scaling!r}")
+        f = torch.empty(rotary_dim // 2, dtype=torch.float64, device=device)
+        _run("rotary_frequencies", f.device, _ptr(f), rotary_dim, base, ROTARY_SCALINGS[scaling], factor, original_len, low,
+             high)
+        return cls(f, interleaved, magnitude)
+
+
+def _check_positions(first: torch.Tensor, rot: Rotary, positions: torch.Tensor):
+    if positions.shape != first.shape[:1] or positions.device != first.device or rot.device != first.device:
+        _check_shapes(first, positions=(positions, first.shape[:1]), inv_freq=(rot.inv_freq, rot.inv_freq.shape))
+    if positions.dtype != torch.int32:
+        raise ValueError("positions must be int32")
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rot: Rotary, q_out: Optional[torch.Tensor] = None,
+           k_out: Optional[torch.Tensor] = None):
+    """(q_out, k_out): q [T, heads, D] and k [T, kv_heads, D] (rows dense) turned by positions [T] int32.
+
+    An output may be its input (turned in place); strides of both are free.
+    """
+    T, H, D = q.shape
+    HK = k.shape[1]
+    if k.shape != (T, HK, D) or k.device != q.device:
+        _check_shapes(q, k=(k, (T, HK, D)))
+    if k.dtype != q.dtype:
+        raise ValueError("q and k must have one dtype")
+    _check_positions(q, rot, positions)
+    q_out, k_out = _out(q_out, q), _out(k_out, k)
+    _run("rotary", q.device, rot.ref, _row_ptr(q), *_strides(q), _row_ptr(k), *_strides(k), _row_ptr(q_out), *_strides(q_out),
+         _row_ptr(k_out), *_strides(k_out), _ptr(positions), T, H, HK, D, _dt(q))
+    return q_out, k_out
+
+
+def kv_cache_append_rotary_affine(cache: AffineKVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                  positions: torch.Tensor, slots: torch.Tensor, rot: Rotary,
+                                  q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """rotary and kv_cache_append_affine in one launch: q turned (q_out), the turned k and v into slots [T] int64."""
+    dev = cache.device
+    T, H, D = q.shape
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if (D != cache.head_dim or k.shape != shape or v.shape != shape or slots.shape != (T,) or q.device != dev
+            or k.device != dev or v.device != dev or slots.device != dev):
+        _check_shapes(cache.k[0], q=(q, (T, H, cache.head_dim)), k=(k, shape), v=(v, shape), slots=(slots, (T,)))
+    if q.dtype != cache.dtype or k.dtype != cache.dtype or v.dtype != cache.dtype or slots.dtype != torch.int64:
+        raise ValueError(f"q, k and v must be {cache.dtype}, slots int64")
+    _check_positions(q, rot, positions)
+    o = _out(q_out, q)
+    _run("kv_cache_append_rotary_affine", dev, cache.ref, rot.ref, _row_ptr(q), *_strides(q), _row_ptr(k), *_strides(k),
+         _row_ptr(v), *_strides(v), _row_ptr(o), *_strides(o), _ptr(positions), _ptr(slots), T, H)
     return o
 
 

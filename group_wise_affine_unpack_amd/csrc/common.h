@@ -272,6 +272,38 @@ struct KvRows {
 hipError_t launch_kv_append(const KvCache& c, const KvRows& r, const int64_t* slots, int64_t T, hipStream_t s);
 hipError_t launch_kv_read(const KvCache& c, const int64_t* slots, void* k, void* v, int64_t T, hipStream_t s);
 
+struct PagesArgs {
+  int32_t* table;          // [B, max_pages], row stride table_stride
+  const int32_t* lens;     // [B]
+  const int32_t* news;     // [B] new tokens, or the tokens to keep
+  int32_t* lens_out;       // [B], may be lens
+  int32_t* free_pages;     // [num_pages], a stack
+  int32_t* state;          // the pool's words
+  int64_t* slots;          // [T]
+  int32_t* positions;      // [T] or null
+  int32_t* seq_ids;        // [T] or null
+  int64_t table_stride, T;
+  int B, max_pages, page_size, num_pages;
+};
+hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s);
+hipError_t launch_pages_trim(const PagesArgs& a, hipStream_t s);
+
+struct RotArgs {
+  const double* inv_freq;    // [R/2]
+  const int32_t* positions;  // [T]
+  const int64_t* slots;      // [T], to a cache
+  const void *q, *k, *v;     // [T, heads, D]; strides of tokens and heads
+  void *qo, *ko;
+  int64_t qts, qhs, kts, khs, vts, vhs, qots, qohs, kots, kohs, T;
+  double magnitude;
+  int heads, kv_heads, D, R, interleaved, dt;
+};
+hipError_t launch_rotary_frequencies(double* out, int rotary_dim, double base, int scaling, double factor,
+                                     double original, double low, double high, hipStream_t s);
+hipError_t launch_rotary(const RotArgs& a, hipStream_t s);
+// k and v into the cache, 16-byte aligned rows
+hipError_t launch_rotary_append(const RotArgs& a, const KvCache& c, hipStream_t s);
+
 struct PagedAttnArgs {
   KvCache c;
   const void* q;          // [B, heads, D], strides qts (sequence), qhs (head)

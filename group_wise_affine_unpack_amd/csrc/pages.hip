@@ -1,0 +1,213 @@
+// Pages of the key-value cache handed to sequences and taken back, from
+// their lengths alone, on the device: a captured step follows the lengths of
+// its replay.  The free pages are a stack, free_pages[0 .. n).
+//   assign: sequence by sequence, page by page, the k-th page needed is
+//           free_pages[n - 1 - k]; a token's slot is its page * page_size +
+//           its offset.  Which pages a sequence takes follows from two
+//           exclusive sums over the batch (rows, then pages).
+//   trim:   the same order backwards, so that it undoes an assign.
+// Bound by the launch and by a chain of dependent loads (lengths, sums, the
+// table's or the list's entry): every workgroup makes both sums for itself
+// (a few hundred cycles for a batch of 64) rather than wait for another
+// launch's, and takes a share of the rows and pages; the last one to finish
+// writes the new lengths and the pool's state, so that both may be updated in
+// place.
+#include "common.h"
+
+namespace qaff {
+namespace {
+
+// [0]: free pages, [1]: pages short at the last assign, [2]: workgroups done (0 between launches)
+struct PoolState {
+  static constexpr int COUNT = 0, SHORT = 1, TICKET = 2;
+};
+
+struct PagesGrid {
+  FastDiv page;
+  int cap;  // tokens a row of the table holds
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+// Exclusive sum over the workgroup's threads of a value each, the total to
+// all; sums stay below 2^32 (a cut sum: below or at `cut`, which counts for
+// anything above).  `part` holds a word a wave, twice.
+template <int WAVES>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t cut, uint32_t* part, uint32_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t s = min(v, cut);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(s, d);
+    if (lane >= d) s = min(s + o, cut);
+  }
+  uint32_t ex = __shfl_up(s, 1);
+  if (lane == 0) ex = 0;
+  __syncthreads();  // (the last call's words have been read)
+  if (lane == 63) part[wave] = s;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w == wave) before = all;
+    all = min(all + part[w], cut);
+  }
+  *total = all;
+  return min(ex + before, cut);
+}
+
+// last of the n entries of an exclusive sum that is at most v (the entry that holds item v: empty ones come before it)
+__device__ __forceinline__ int find(const uint32_t* sum, int n, uint32_t v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sum[mid] <= v) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ __launch_bounds__(256) void pages_assign_kernel(PagesArgs a, PagesGrid g) {
+  extern __shared__ uint32_t lds[];
+  uint32_t* rows_before = lds;             // [B] rows of the sequences before
+  uint32_t* pages_before = lds + a.B;      // [B] pages they need
+  int* had_len = (int*)(lds + 2 * a.B);    // [B] tokens cached so far
+  __shared__ uint32_t part[4];
+  __shared__ uint32_t last;
+  const uint32_t P = g.page.d, T = (uint32_t)a.T;
+  const int each = (a.B + 255) / 256, b0 = min((int)threadIdx.x * each, a.B), b1 = min(b0 + each, a.B);
+  const uint32_t n = (uint32_t)clampi(a.state[PoolState::COUNT], 0, a.num_pages);
+  const auto ceil_pages = [&](int tokens) { return (int)g.page.div((uint32_t)tokens + P - 1); };  // (below 2^31)
+  uint32_t sum = 0, total_rows, total_pages;
+  for (int b = b0; b < b1; ++b) {
+    rows_before[b] = sum;
+    sum = min(sum + (uint32_t)max(a.news[b], 0), T);
+  }
+  uint32_t base = block_scan<4>(sum, T, part, &total_rows);
+  sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t at = min(base + rows_before[b], T);
+    const int len = clampi(a.lens[b], 0, g.cap);
+    const int stored = min((int)min((uint32_t)max(a.news[b], 0), T - at), g.cap - len);
+    rows_before[b] = at;
+    had_len[b] = len;
+    pages_before[b] = sum;
+    sum += ceil_pages(len + stored) - ceil_pages(len);
+  }
+  base = block_scan<4>(sum, 0xffffffffu, part, &total_pages);
+  for (int b = b0; b < b1; ++b) pages_before[b] += base;
+  __syncthreads();
+
+  // the rows: a slot, a position and a sequence each
+  const uint32_t step = gridDim.x * 256u, me = blockIdx.x * 256u + threadIdx.x;
+  for (uint32_t r = me; r < T; r += step) {
+    int64_t slot = -1;
+    int pos = 0, seq = -1;
+    if (r < total_rows) {
+      seq = find(rows_before, a.B, r);
+      const int len = had_len[seq], i = (int)(r - rows_before[seq]);
+      pos = (int)min((uint32_t)len + (uint32_t)i, 0x7fffffffu);
+      if (i < g.cap - len) {
+        const int p = (int)g.page.div((uint32_t)pos), k = p - ceil_pages(len);
+        int page = -1;
+        if (k < 0) {
+          page = a.table[seq * a.table_stride + p];
+        } else if (pages_before[seq] + (uint32_t)k < n) {
+          page = a.free_pages[n - 1 - (pages_before[seq] + (uint32_t)k)];
+        }
+        if (page >= 0 && page < a.num_pages) slot = (int64_t)page * P + (pos - p * (int)P);
+      }
+    }
+    a.slots[r] = slot;
+    if (a.positions) a.positions[r] = pos;
+    if (a.seq_ids) a.seq_ids[r] = seq;
+  }
+  // the table's new entries
+  const uint32_t given = min(total_pages, n);
+  for (uint32_t k = me; k < given; k += step) {
+    const int b = find(pages_before, a.B, k);
+    a.table[b * a.table_stride + ceil_pages(had_len[b]) + (int)(k - pages_before[b])] = a.free_pages[n - 1 - k];
+  }
+  // the last workgroup, when every other has read what it needs
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      last = atomicAdd((uint32_t*)a.state + PoolState::TICKET, 1u);
+    }
+    __syncthreads();
+    if (last != gridDim.x - 1) return;
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int len = had_len[b], had = ceil_pages(len);
+    const uint32_t at = rows_before[b], pb = pages_before[b];
+    int stored = (int)((b + 1 < a.B ? rows_before[b + 1] : total_rows) - at);
+    stored = min(stored, g.cap - len);
+    const int need = ceil_pages(len + stored) - had, got = pb < n ? (int)min(n - pb, (uint32_t)need) : 0;
+    if (got < need) stored = (had + got) * (int)P - len;
+    a.lens_out[b] = len + stored;
+  }
+  if (threadIdx.x == 0) {
+    a.state[PoolState::COUNT] = (int)(n - given);
+    a.state[PoolState::SHORT] = (int)(total_pages - given);
+    a.state[PoolState::TICKET] = 0;
+  }
+}
+
+// One workgroup: the entries that go back, from the last to the first, each
+// to the top of the stack.  Entries outside the cache are dropped, so their
+// number is only known as they are read.
+__global__ __launch_bounds__(1024) void pages_trim_kernel(PagesArgs a, PagesGrid g) {
+  extern __shared__ uint32_t lds[];
+  uint32_t* before = lds;               // [B] entries of the sequences before
+  int* first = (int*)(lds + a.B);       // [B] first entry that goes back
+  __shared__ uint32_t part[16];
+  const int each = (a.B + 1023) / 1024, b0 = min((int)threadIdx.x * each, a.B), b1 = min(b0 + each, a.B);
+  const uint32_t P = g.page.d;
+  uint32_t n = (uint32_t)clampi(a.state[PoolState::COUNT], 0, a.num_pages);
+  uint32_t sum = 0, total;
+  for (int b = b0; b < b1; ++b) {
+    const int len = clampi(a.lens[b], 0, g.cap), keep = clampi(a.news[b], 0, len);
+    before[b] = sum;
+    first[b] = (int)g.page.div((uint32_t)keep + P - 1);
+    sum += (uint32_t)((int)g.page.div((uint32_t)len + P - 1) - first[b]);
+    a.lens_out[b] = keep;  // (may be a.lens: this thread's own entry, read already)
+  }
+  const uint32_t base = block_scan<16>(sum, 0xffffffffu, part, &total);
+  for (int b = b0; b < b1; ++b) before[b] += base;
+  __syncthreads();
+  for (uint32_t done = 0; done < total; done += 1024) {
+    const uint32_t i = done + threadIdx.x;
+    int page = -1;
+    if (i < total) {
+      const uint32_t j = total - 1 - i;
+      const int b = find(before, a.B, j);
+      int32_t* entry = a.table + b * a.table_stride + first[b] + (int)(j - before[b]);
+      page = *entry;
+      *entry = -1;
+    }
+    uint32_t there;
+    const bool ok = page >= 0 && page < a.num_pages;
+    const uint32_t at = n + block_scan<16>(ok ? 1u : 0u, 0xffffffffu, part, &there);
+    if (ok && at < (uint32_t)a.num_pages) a.free_pages[at] = page;
+    n = min(n + there, (uint32_t)a.num_pages);
+  }
+  if (threadIdx.x == 0) a.state[PoolState::COUNT] = (int)n;
+}
+
+}  // namespace
+
+hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
+  const PagesGrid g{FastDiv((uint32_t)a.page_size), a.max_pages * a.page_size};
+  const int64_t wgs = (a.T + 255) / 256;
+  hipLaunchKernelGGL(pages_assign_kernel, dim3((unsigned)(wgs < 1 ? 1 : wgs > 512 ? 512 : wgs)), dim3(256),
+                     12u * (unsigned)a.B, s, a, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_trim(const PagesArgs& a, hipStream_t s) {
+  const PagesGrid g{FastDiv((uint32_t)a.page_size), a.max_pages * a.page_size};
+  hipLaunchKernelGGL(pages_trim_kernel, dim3(1), dim3(1024), 8u * (unsigned)a.B, s, a, g);
+  return hipGetLastError();
+}
+
+}  // namespace qaff

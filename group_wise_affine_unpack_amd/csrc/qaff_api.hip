@@ -642,6 +642,200 @@ int paged_attention_affine(const qaff_kv_cache* cache, const void* q, int64_t q_
   return ok();
 }
 
+static bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1u)) == 0; }
+
+// the checks that assign and trim share
+static int check_pages(const int32_t* table, int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                       const int32_t* other, const int32_t* lens_out, const int32_t* free_pages, const int32_t* state,
+                       int64_t num_pages, int32_t page_size, int64_t B) {
+  if (B < 0 || max_pages < 0) return fail(QAFF_E_INVAL, "B and max_pages must be >= 0");
+  if (num_pages < 1 || page_size < 1) return fail(QAFF_E_INVAL, "num_pages and page_size must be >= 1");
+  if (page_size % 16 || page_size > (1 << 16))
+    return fail(QAFF_E_UNSUPPORTED, "page_size must be a multiple of 16 and at most 65536 (got %d)", page_size);
+  if (num_pages >= (int64_t(1) << 31) / page_size) return fail(QAFF_E_UNSUPPORTED, "2^31 slots or more");
+  if (B > 4096) return fail(QAFF_E_UNSUPPORTED, "B above 4096 (got %lld)", (long long)B);
+  if (max_pages > ((int64_t(1) << 31) - (1 << 16)) / page_size || (B > 0 && max_pages >= (int64_t(1) << 31) / B))
+    return fail(QAFF_E_UNSUPPORTED, "max_pages * page_size above 2^31 - 2^16, or a table of 2^31 entries or more");
+  if (B > 1 && (table_stride < max_pages || table_stride > (int64_t(1) << 40)))
+    return fail(QAFF_E_INVAL, "table_stride must lie in [max_pages, 2^40]");
+  if (!free_pages || !state || (B > 0 && (!lens || !other || !lens_out)) || (B > 0 && max_pages > 0 && !table))
+    return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(other, 4) || !aligned(lens_out, 4) || !aligned(free_pages, 4) ||
+      !aligned(state, 4))
+    return fail(QAFF_E_ALIGN, "int32 arrays must be 4-byte aligned");
+  if (B > 0 && lens_out == other) return fail(QAFF_E_INVAL, "lens_out must not be new_lens or keep_lens");
+  return QAFF_OK;
+}
+
+int kv_pages_assign(int32_t* page_table, int64_t table_stride, int64_t max_pages, const int32_t* seq_lens,
+                    const int32_t* new_lens, int32_t* lens_out, const int32_t* free_pages, int32_t* pool_state,
+                    int64_t num_pages, int32_t page_size, int64_t B, int64_t* slots, int32_t* positions,
+                    int32_t* seq_ids, int64_t T, void* stream) {
+  const int rc = check_pages(page_table, table_stride, max_pages, seq_lens, new_lens, lens_out, free_pages, pool_state,
+                             num_pages, page_size, B);
+  if (rc != QAFF_OK) return rc;
+  if (T < 0) return fail(QAFF_E_INVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > kMaxDim) return fail(QAFF_E_UNSUPPORTED, "T above 2^30");
+  if (T > 0 && !slots) return fail(QAFF_E_INVAL, "null tensor pointer (slots)");
+  if (!aligned(slots, 8)) return fail(QAFF_E_ALIGN, "slots must be 8-byte aligned");
+  if (!aligned(positions, 4) || !aligned(seq_ids, 4)) return fail(QAFF_E_ALIGN, "int32 arrays must be 4-byte aligned");
+  if (B == 0 && T == 0) return ok();
+  qaff::PagesArgs a{page_table, seq_lens, new_lens, lens_out, const_cast<int32_t*>(free_pages), pool_state, slots,
+                    positions, seq_ids, table_stride, T, (int)B, (int)max_pages, page_size, (int)num_pages};
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_pages_assign(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "page assignment launch");
+  return ok();
+}
+
+int kv_pages_trim(int32_t* page_table, int64_t table_stride, int64_t max_pages, const int32_t* seq_lens,
+                  const int32_t* keep_lens, int32_t* lens_out, int32_t* free_pages, int32_t* pool_state,
+                  int64_t num_pages, int32_t page_size, int64_t B, void* stream) {
+  const int rc = check_pages(page_table, table_stride, max_pages, seq_lens, keep_lens, lens_out, free_pages, pool_state,
+                             num_pages, page_size, B);
+  if (rc != QAFF_OK) return rc;
+  if (B == 0) return ok();
+  qaff::PagesArgs a{page_table, seq_lens, keep_lens, lens_out, free_pages, pool_state, nullptr, nullptr, nullptr,
+                    table_stride, 0, (int)B, (int)max_pages, page_size, (int)num_pages};
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_pages_trim(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "page release launch");
+  return ok();
+}
+
+int rotary_frequencies(double* inv_freq_out, int32_t rotary_dim, double base, int32_t scaling, double factor,
+                       double original_len, double low, double high, void* stream) {
+  if (rotary_dim < 2 || rotary_dim % 2) return fail(QAFF_E_INVAL, "rotary_dim must be even and >= 2 (got %d)", rotary_dim);
+  if (rotary_dim > 1024) return fail(QAFF_E_UNSUPPORTED, "rotary_dim above 1024 (got %d)", rotary_dim);
+  if (scaling < QAFF_ROTARY_PLAIN || scaling > QAFF_ROTARY_BANDS) return fail(QAFF_E_INVAL, "unknown scaling %d", scaling);
+  if (!(base > 0 && base < 1e30)) return fail(QAFF_E_INVAL, "base must be positive and finite");
+  if (scaling != QAFF_ROTARY_PLAIN && !(factor > 0 && factor < 1e30))
+    return fail(QAFF_E_INVAL, "factor must be positive and finite");
+  if (scaling == QAFF_ROTARY_BASE && rotary_dim == 2) return fail(QAFF_E_INVAL, "QAFF_ROTARY_BASE needs rotary_dim > 2");
+  if (scaling == QAFF_ROTARY_BANDS && !(original_len > 0 && original_len < 1e30 && low >= 0 && high > low && high < 1e30))
+    return fail(QAFF_E_INVAL, "QAFF_ROTARY_BANDS needs original_len > 0 and 0 <= low < high");
+  if (!inv_freq_out) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned(inv_freq_out, 8)) return fail(QAFF_E_ALIGN, "inv_freq_out must be 8-byte aligned");
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_rotary_frequencies(inv_freq_out, rotary_dim, base, scaling, factor, original_len,
+                                                       low, high, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "rotary frequencies launch");
+  return ok();
+}
+
+static bool row_stride_ok(int64_t s) { return s >= 0 && s <= (int64_t(1) << 40); }
+
+// the checks that the rotary entry points share; fills `a` but for the tensors
+static int check_rotary(const qaff_rotary* rot, const int32_t* positions, int64_t T, int32_t heads, int32_t kv_heads,
+                        int32_t head_dim, int32_t dtype, qaff::RotArgs* a) {
+  if (!rot) return fail(QAFF_E_INVAL, "null rotary");
+  if (!act_dtype_ok(dtype)) return fail(QAFF_E_INVAL, "dtype must be QAFF_BF16 or QAFF_F16 (got %d)", dtype);
+  if (T < 0 || heads < 0 || kv_heads < 0) return fail(QAFF_E_INVAL, "T, heads and kv_heads must be >= 0");
+  if (head_dim < 2) return fail(QAFF_E_INVAL, "head_dim must be >= 2 (got %d)", head_dim);
+  if (rot->rotary_dim < 2 || rot->rotary_dim % 2 || rot->rotary_dim > head_dim)
+    return fail(QAFF_E_INVAL, "rotary_dim=%d must be even and in [2, head_dim=%d]", rot->rotary_dim, head_dim);
+  if (rot->interleaved != 0 && rot->interleaved != 1) return fail(QAFF_E_INVAL, "interleaved must be 0 or 1");
+  if (!(rot->magnitude > -1e30 && rot->magnitude < 1e30)) return fail(QAFF_E_INVAL, "magnitude must be finite");
+  if (T >= (1 << 24)) return fail(QAFF_E_UNSUPPORTED, "T of 2^24 or more");
+  if (heads > 4096 || kv_heads > 4096 || head_dim > 1024)
+    return fail(QAFF_E_UNSUPPORTED, "heads or kv_heads above 4096, or head_dim above 1024");
+  if (T > 0 && (!rot->inv_freq || !positions)) return fail(QAFF_E_INVAL, "null tensor pointer (inv_freq, positions)");
+  if (!aligned(rot->inv_freq, 8) || !aligned(positions, 4))
+    return fail(QAFF_E_ALIGN, "inv_freq must be 8-byte and positions 4-byte aligned");
+  a->inv_freq = rot->inv_freq;
+  a->positions = positions;
+  a->T = T;
+  a->magnitude = rot->magnitude;
+  a->heads = heads;
+  a->kv_heads = kv_heads;
+  a->D = head_dim;
+  a->R = rot->rotary_dim;
+  a->interleaved = rot->interleaved;
+  a->dt = dtype;
+  return QAFF_OK;
+}
+
+int rotary(const qaff_rotary* rot, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+           int64_t k_token_stride, int64_t k_head_stride, void* q_out, int64_t q_out_token_stride,
+           int64_t q_out_head_stride, void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+           const int32_t* positions, int64_t T, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
+           void* stream) {
+  qaff::RotArgs a{};
+  const int rc = check_rotary(rot, positions, T, heads, kv_heads, head_dim, dtype, &a);
+  if (rc != QAFF_OK) return rc;
+  if (T == 0 || heads + kv_heads == 0) return ok();
+  if ((heads > 0 && (!q || !q_out)) || (kv_heads > 0 && (!k || !k_out))) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned(q, 2) || !aligned(k, 2) || !aligned(q_out, 2) || !aligned(k_out, 2))
+    return fail(QAFF_E_ALIGN, "q, k and their outputs must be 2-byte aligned");
+  for (int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, q_out_token_stride, q_out_head_stride,
+                    k_out_token_stride, k_out_head_stride})
+    if (!row_stride_ok(s)) return fail(QAFF_E_INVAL, "strides must lie in [0, 2^40]");
+  if ((q == q_out && heads > 0 && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride)) ||
+      (k == k_out && kv_heads > 0 && (k_token_stride != k_out_token_stride || k_head_stride != k_out_head_stride)))
+    return fail(QAFF_E_INVAL, "an output in place needs the input's strides");
+  a.q = q;
+  a.k = k;
+  a.qo = q_out;
+  a.ko = k_out;
+  a.qts = q_token_stride;
+  a.qhs = q_head_stride;
+  a.kts = k_token_stride;
+  a.khs = k_head_stride;
+  a.qots = q_out_token_stride;
+  a.qohs = q_out_head_stride;
+  a.kots = k_out_token_stride;
+  a.kohs = k_out_head_stride;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_rotary(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "too many rows for one call");
+  if (e != hipSuccess) return hip_fail(e, "rotary launch");
+  return ok();
+}
+
+int kv_cache_append_rotary_affine(const qaff_kv_cache* cache, const qaff_rotary* rot, const void* q,
+                                  int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                                  int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                  void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                  const int32_t* positions, const int64_t* slots, int64_t T, int32_t heads,
+                                  void* stream) {
+  qaff::KvCache c;
+  int rc = check_cache(cache, &c);
+  if (rc != QAFF_OK) return rc;
+  qaff::RotArgs a{};
+  rc = check_rotary(rot, positions, T, heads, c.kv_heads, c.head_dim, c.dt, &a);
+  if (rc != QAFF_OK) return rc;
+  if (a.R % (a.interleaved ? 8 : 16))
+    return fail(QAFF_E_UNSUPPORTED, "rotary_dim must be a multiple of 16, or of 8 interleaved (got %d)", a.R);
+  if (T == 0) return ok();
+  if (!k || !v || !slots || (heads > 0 && (!q || !q_out))) return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
+    return fail(QAFF_E_ALIGN, "q, k, v and q_out must be 16-byte aligned");
+  if (!aligned(slots, 8)) return fail(QAFF_E_ALIGN, "slots must be 8-byte aligned");
+  for (int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                    q_out_token_stride, q_out_head_stride})
+    if (!stride_ok(s)) return fail(QAFF_E_ALIGN, "strides must be non-negative multiples of 8 elements");
+  if (q == q_out && heads > 0 && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+    return fail(QAFF_E_INVAL, "an output in place needs the input's strides");
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qo = q_out;
+  a.slots = slots;
+  a.qts = q_token_stride;
+  a.qhs = q_head_stride;
+  a.kts = k_token_stride;
+  a.khs = k_head_stride;
+  a.vts = v_token_stride;
+  a.vhs = v_head_stride;
+  a.qots = q_out_token_stride;
+  a.qohs = q_out_head_stride;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_rotary_append(a, c, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "too many rows for one call");
+  if (e != hipSuccess) return hip_fail(e, "rotary append launch");
+  return ok();
+}
+
 int gptq_to_affine_repack(const int32_t* qweight, const int32_t* qzeros, const void* scales, const int32_t* g_idx,
                           uint32_t* w_packed_out, void* scales_out, void* biases_out, int32_t bias_dtype,
                           int32_t* k_perm_out, int64_t K, int64_t N, int32_t group_size, void* stream) {

@@ -1,0 +1,304 @@
+// Rotary positions: pairs (a, b) of a head's first R columns turned by the
+// token's position times the pair's frequency,
+//     a' = a c - b s,  b' = b c + a s,   (c, s) = magnitude (cos, sin)(pos f_j)
+// with the pair (j, j + R/2), or (2j, 2j + 1) interleaved; and the same with
+// the turned keys and the values quantized into their cache rows at once.
+//
+// Everything is fp64 up to the one rounding: positions of a million leave an
+// fp32 angle with an error of 2^-4, and a key that falls on the other side of
+// a rounding border moves its group's codes.  A multiply-add of fp64 costs
+// here what an fp32 one costs, so this is free where memory bounds (see
+// below).  The angle is taken in turns, pos * (f / 2 pi), whose whole part is
+// dropped exactly.  The rounding to 16 bits goes through a double that keeps
+// 20 bits, the last of them set where any below is: no second rounding error
+// down to fp32's smallest normal number.
+//
+// Bound by memory for long batches and by the launch and one sine for short
+// ones.  A workgroup takes a few tokens (or some heads of one): one pair of
+// (c, s) a thread into LDS, shared by all heads, then 16-byte loads and
+// stores.
+#include <math.h>
+
+#include "common.h"
+#include "kv_codes.h"
+
+namespace qaff {
+namespace {
+
+struct RotGrid {
+  FastDiv units;    // per head of q (and of k when it goes to a dense array)
+  FastDiv half;     // R/2
+  FastDiv chunks;   // D/8
+  FastDiv items;    // per token
+  FastDiv page;
+  uint32_t q_items, k_items;  // of the items: q's, then k's (the rest are v's)
+  uint32_t tokens;  // per workgroup
+  uint32_t per_wg;  // items of a workgroup: blockIdx.y takes its share of the tokens' items
+};
+
+// v rounded to the type: the double's upper word, its last bit set where anything below is, converts to fp32 exactly
+template <bool F16_>
+__device__ __forceinline__ uint32_t round_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t hi = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
+  return f32_to_act_bits((float)__builtin_bit_cast(double, (uint64_t)hi << 32), F16_);
+}
+
+template <bool F16_>
+__device__ __forceinline__ void unpack8(const u32x4_t& raw, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = act_to_f32<F16_>(raw[j / 2] >> (16 * (j & 1)));
+}
+
+__device__ __forceinline__ u32x4_t pack8(const uint32_t (&e)[8]) {
+  u32x4_t o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = e[2 * j] | e[2 * j + 1] << 16;
+  return o;
+}
+
+// 8 columns `a` of the first half (second: of the second) and their partners, turned, as bits
+template <bool F16_, bool SECOND>
+__device__ __forceinline__ void turn_half(const u32x4_t& own, const u32x4_t& other, const double2* cs, uint32_t (&e)[8]) {
+  float x[8], y[8];
+  unpack8<F16_>(own, x);
+  unpack8<F16_>(other, y);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double2 t = cs[j];
+    const double v = SECOND ? (double)x[j] * t.x + (double)y[j] * t.y : (double)x[j] * t.x - (double)y[j] * t.y;
+    e[j] = round_f64<F16_>(v);
+  }
+}
+
+// 8 columns of interleaved pairs
+template <bool F16_>
+__device__ __forceinline__ void turn_pairs(const u32x4_t& own, const double2* cs, uint32_t (&e)[8]) {
+  float x[8];
+  unpack8<F16_>(own, x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const double2 t = cs[j];
+    const double a = x[2 * j], b = x[2 * j + 1];
+    e[2 * j] = round_f64<F16_>(a * t.x - b * t.y);
+    e[2 * j + 1] = round_f64<F16_>(b * t.x + a * t.y);
+  }
+}
+
+// (c, s) of every pair of the workgroup's tokens
+__device__ __forceinline__ void make_angles(const RotArgs& a, const RotGrid& g, uint32_t t0, double2* cs) {
+  const uint32_t count = g.tokens * g.half.d;
+  for (uint32_t i = threadIdx.x; i < count; i += 256u) {
+    const uint32_t t = g.half.div(i), j = i - t * g.half.d;
+    if (t0 + t >= (uint32_t)a.T) break;
+    const double turns = (double)a.positions[t0 + t] * (a.inv_freq[j] * 0.15915494309189533577);  // 1 / (2 pi)
+    const double x = 2.0 * (turns - rint(turns));
+    double s, c;
+    sincospi(x, &s, &c);
+    cs[i] = double2{a.magnitude * c, a.magnitude * s};
+  }
+}
+
+// Rows whose 8-column chunks are 16-byte aligned and hold no pair's end.
+// Units of a head: half layout R/16 pairs of chunks, then the chunks that
+// stay; interleaved, chunks.  BITS = 0: q and k to dense arrays; else k and v
+// go to the cache, chunk by chunk.
+template <bool F16_, int BITS, int G>
+__global__ __launch_bounds__(256) void rotary_kernel(RotArgs a, RotGrid g, KvCache c) {
+  extern __shared__ double2 cs[];  // [tokens][R/2]
+  const uint32_t t0 = blockIdx.x * g.tokens;
+  make_angles(a, g, t0, cs);
+  __syncthreads();
+  const uint32_t R = 2 * g.half.d, chunks = g.chunks.d, end = min((blockIdx.y + 1) * g.per_wg, g.tokens * g.items.d);
+  for (uint32_t i = blockIdx.y * g.per_wg + threadIdx.x; i < end; i += 256u) {
+    const uint32_t t = g.items.div(i), it = i - t * g.items.d, tok = t0 + t;
+    if (tok >= (uint32_t)a.T) break;
+    const double2* angles = cs + t * g.half.d;
+    if (BITS == 0 || it < g.q_items) {
+      uint32_t h = g.units.div(it);
+      const uint32_t u = it - h * g.units.d;
+      const bool is_k = BITS == 0 && h >= (uint32_t)a.heads;
+      if (is_k) h -= a.heads;
+      if (BITS != 0 && h >= (uint32_t)a.heads) continue;  // (the padding of q's items)
+      const uint16_t* src = (const uint16_t*)(is_k ? a.k : a.q) + (int64_t)tok * (is_k ? a.kts : a.qts) + (int64_t)h * (is_k ? a.khs : a.qhs);
+      uint16_t* dst = (uint16_t*)(is_k ? a.ko : a.qo) + (int64_t)tok * (is_k ? a.kots : a.qots) + (int64_t)h * (is_k ? a.kohs : a.qohs);
+      uint32_t e[8];
+      if (a.interleaved) {
+        u32x4_t own = *reinterpret_cast<const u32x4_t*>(src + 8 * u);
+        if (8 * u < R) {
+          turn_pairs<F16_>(own, angles + 4 * u, e);
+          own = pack8(e);
+        }
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = own;
+      } else if (16 * u < R) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 8 * u);
+        const u32x4_t y = *reinterpret_cast<const u32x4_t*>(src + 8 * u + R / 2);
+        turn_half<F16_, false>(x, y, angles + 8 * u, e);
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = pack8(e);
+        turn_half<F16_, true>(y, x, angles + 8 * u, e);
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u + R / 2) = pack8(e);
+      } else {
+        const uint32_t at = 8 * u + R / 2;
+        *reinterpret_cast<u32x4_t*>(dst + at) = *reinterpret_cast<const u32x4_t*>(src + at);
+      }
+    } else if constexpr (BITS != 0) {
+      // a row's chunk into the cache; the lanes of a group are neighbours and share their token, head and kind
+      const uint32_t kv = it - g.q_items;
+      const bool is_v = kv >= g.k_items;
+      const uint32_t j = is_v ? kv - g.k_items : kv, h = g.chunks.div(j), ch = j - h * chunks;
+      if (h >= (uint32_t)c.kv_heads) continue;  // (the padding of a token's items)
+      const int64_t slot = a.slots[tok];
+      if (slot < 0 || slot >= c.num_slots) continue;
+      const uint16_t* src = is_v ? (const uint16_t*)a.v + (int64_t)tok * a.vts + (int64_t)h * a.vhs
+                                 : (const uint16_t*)a.k + (int64_t)tok * a.kts + (int64_t)h * a.khs;
+      u32x4_t own = *reinterpret_cast<const u32x4_t*>(src + 8 * ch);
+      if (!is_v && 8 * ch < R) {
+        uint32_t e[8];
+        if (a.interleaved) {
+          turn_pairs<F16_>(own, angles + 4 * ch, e);
+        } else {
+          const bool second = 16 * ch >= R;
+          const uint32_t first = second ? ch - R / 16 : ch;
+          const u32x4_t other = *reinterpret_cast<const u32x4_t*>(src + 8 * first + (second ? 0 : R / 2));
+          if (second) turn_half<F16_, true>(own, other, angles + 8 * first, e);
+          else turn_half<F16_, false>(own, other, angles + 8 * first, e);
+        }
+        own = pack8(e);
+      }
+      float x[8];
+      unpack8<F16_>(own, x);
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        if constexpr (!F16_) x[m] = __builtin_canonicalizef(x[m]);  // only quiet NaN stay out of the minimum
+      const uint32_t pg = g.page.div((uint32_t)slot), off = (uint32_t)slot - pg * g.page.d;
+      const KvRowAt at{((size_t)pg * c.kv_heads + h) * c.page_size + off, ch, chunks};
+      write_codes<BITS, G, F16_>(x, at, is_v ? c.v_packed : c.k_packed, is_v ? c.v_scales : c.k_scales,
+                                 is_v ? c.v_biases : c.k_biases);
+    }
+  }
+}
+
+// Any even R, alignment of 2 bytes: a pair, or a column that stays, a thread.
+template <bool F16_>
+__global__ __launch_bounds__(256) void rotary_any_kernel(RotArgs a, RotGrid g) {
+  extern __shared__ double2 cs[];
+  const uint32_t t0 = blockIdx.x * g.tokens;
+  make_angles(a, g, t0, cs);
+  __syncthreads();
+  const uint32_t half = g.half.d, end = min((blockIdx.y + 1) * g.per_wg, g.tokens * g.items.d);
+  for (uint32_t i = blockIdx.y * g.per_wg + threadIdx.x; i < end; i += 256u) {
+    const uint32_t t = g.items.div(i), it = i - t * g.items.d, tok = t0 + t;
+    if (tok >= (uint32_t)a.T) break;
+    uint32_t h = g.units.div(it);
+    const uint32_t u = it - h * g.units.d;
+    const bool is_k = h >= (uint32_t)a.heads;
+    if (is_k) h -= a.heads;
+    const uint16_t* src = (const uint16_t*)(is_k ? a.k : a.q) + (int64_t)tok * (is_k ? a.kts : a.qts) + (int64_t)h * (is_k ? a.khs : a.qhs);
+    uint16_t* dst = (uint16_t*)(is_k ? a.ko : a.qo) + (int64_t)tok * (is_k ? a.kots : a.qots) + (int64_t)h * (is_k ? a.kohs : a.qohs);
+    if (u < half) {
+      const uint32_t ia = a.interleaved ? 2 * u : u, ib = a.interleaved ? 2 * u + 1 : u + half;
+      const double x = act_to_f32<F16_>(src[ia]), y = act_to_f32<F16_>(src[ib]);
+      const double2 r = cs[t * half + u];
+      dst[ia] = (uint16_t)round_f64<F16_>(x * r.x - y * r.y);
+      dst[ib] = (uint16_t)round_f64<F16_>(y * r.x + x * r.y);
+    } else {
+      dst[u + half] = src[u + half];
+    }
+  }
+}
+
+// Scalings of the frequencies base^(-2j/R):
+//   linear  f / factor
+//   base    base * factor^(R/(R-2)) in the place of base: the slowest pair
+//           ends at f / factor, the fastest keeps f
+//   bands   pairs that turn at least `high` times over original_len keep f, those that
+//           turn at most `low` times take f / factor, between them linear in the turns
+__global__ __launch_bounds__(64) void frequencies_kernel(double* __restrict__ out, int half, double base, int scaling,
+                                                         double factor, double original, double low, double high) {
+  const int j = blockIdx.x * 64 + threadIdx.x;
+  if (j >= half) return;
+  const double r = 2.0 * half;
+  if (scaling == 2) base *= pow(factor, r / (r - 2.0));
+  double f = pow(base, -2.0 * j / r);
+  if (scaling == 1) f /= factor;
+  if (scaling == 3) {
+    const double keep = fmin(1.0, fmax(0.0, (original * f * 0.15915494309189533577 - low) / (high - low)));
+    f *= keep + (1.0 - keep) / factor;
+  }
+  out[j] = f;
+}
+
+bool strides8(int64_t a, int64_t b) { return a % 8 == 0 && b % 8 == 0; }
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+hipError_t launch_rotary_frequencies(double* out, int rotary_dim, double base, int scaling, double factor,
+                                     double original, double low, double high, hipStream_t s) {
+  const int half = rotary_dim / 2;
+  hipLaunchKernelGGL(frequencies_kernel, dim3((unsigned)((half + 63) / 64)), dim3(64), 0, s, out, half, base, scaling,
+                     factor, original, low, high);
+  return hipGetLastError();
+}
+
+namespace {
+
+// the grid of T tokens of `items` each: workgroups of a few tokens, or of a share of one token's items
+struct RotLaunch {
+  RotGrid g;
+  dim3 grid;
+  unsigned lds;
+};
+RotLaunch rot_launch(const RotArgs& a, uint32_t units, uint32_t chunks, uint32_t items, uint32_t q_items, uint32_t k_items,
+                     int page_size) {
+  // Tokens a workgroup, a power of two: enough that its angles occupy the
+  // threads (256 pairs) while the device's CUs all keep several workgroups.
+  uint32_t tokens = 1;
+  while (tokens * 2 * (uint32_t)(a.R / 2) <= 256u && a.T / (2 * tokens) >= 1024) tokens *= 2;
+  // one token's items are split while there are few workgroups: 256 items each
+  const int64_t wgs = (a.T + tokens - 1) / tokens;
+  uint32_t per_wg = tokens * items;
+  if (wgs < 512 && per_wg > 256u) per_wg = 256u;
+  RotLaunch l{RotGrid{FastDiv(units), FastDiv((uint32_t)a.R / 2), FastDiv(chunks), FastDiv(items),
+                      FastDiv((uint32_t)page_size), q_items, k_items, tokens, per_wg},
+              dim3((unsigned)wgs, (tokens * items + per_wg - 1) / per_wg), (unsigned)(tokens * (a.R / 2) * 16)};
+  return l;
+}
+
+uint32_t head_units(const RotArgs& a) { return a.interleaved ? a.D / 8 : a.R / 16 + (a.D - a.R) / 8; }
+
+template <int BITS, int G, bool F16_>
+void launch_append_dt(const RotArgs& a, const KvCache& c, const RotLaunch& l, hipStream_t s) {
+  hipLaunchKernelGGL((rotary_kernel<F16_, BITS, G>), l.grid, dim3(256), l.lds, s, a, l.g, c);
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const RotArgs& a, hipStream_t s) {
+  const bool wide = a.D % 8 == 0 && a.R % (a.interleaved ? 8 : 16) == 0 && strides8(a.qts, a.qhs) &&
+                    strides8(a.kts, a.khs) && strides8(a.qots, a.qohs) && strides8(a.kots, a.kohs) && at16(a.q) &&
+                    at16(a.k) && at16(a.qo) && at16(a.ko);
+  const uint32_t units = wide ? head_units(a) : (uint32_t)(a.D - a.R / 2), items = (uint32_t)(a.heads + a.kv_heads) * units;
+  const RotLaunch l = rot_launch(a, units, a.D >= 8 ? a.D / 8 : 1, items, items, 0, 16);
+  if (l.grid.y > 65535u) return hipErrorNotSupported;
+  if (wide) {
+    if (a.dt == F16) hipLaunchKernelGGL((rotary_kernel<true, 0, 32>), l.grid, dim3(256), l.lds, s, a, l.g, KvCache{});
+    else hipLaunchKernelGGL((rotary_kernel<false, 0, 32>), l.grid, dim3(256), l.lds, s, a, l.g, KvCache{});
+  } else {
+    if (a.dt == F16) hipLaunchKernelGGL(rotary_any_kernel<true>, l.grid, dim3(256), l.lds, s, a, l.g);
+    else hipLaunchKernelGGL(rotary_any_kernel<false>, l.grid, dim3(256), l.lds, s, a, l.g);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rotary_append(const RotArgs& a, const KvCache& c, hipStream_t s) {
+  // q's items and a token's are rounded up to 16, so that the lanes of a group stay together
+  const uint32_t units = head_units(a), q = ((uint32_t)a.heads * units + 15) & ~15u;
+  const uint32_t kv = (uint32_t)a.kv_heads * (a.D / 8), items = (q + 2 * kv + 15) & ~15u;
+  const RotLaunch l = rot_launch(a, units, a.D / 8, items, q, kv, c.page_size);
+  if (l.grid.y > 65535u) return hipErrorNotSupported;
+  QAFF_KV_CASES(launch_append_dt, a, c, l, s)
+  return hipGetLastError();
+}
+
+}  // namespace qaff

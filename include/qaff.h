@@ -517,6 +517,116 @@ int paged_attention_affine(const qaff_kv_cache *cache, const void *q, int64_t q_
                            void *stream);
 
 /*
+ * kv_pages_assign, kv_pages_trim - the pages of such a cache handed to
+ * sequences, and taken back, from their lengths alone.  Everything is read on
+ * the device: a captured call follows the lengths of the replay.
+ *   A pool is free_pages [num_pages] int32, a stack of which the first
+ *   pool_state[0] entries are free pages (distinct, in [0, num_pages)), and
+ *   pool_state [4] int32: free pages, pages short at the last assign, and a
+ *   word the library keeps at 0 between calls; the caller sets the first
+ *   and clears the rest once.  page_size as in the cache, at most 65536.
+ *   page_table  [B, max_pages] int32, rows table_stride >= max_pages apart;
+ *               sequence b's first ceil(len / page_size) entries are its pages
+ *   seq_lens    [B] int32: tokens cached so far, cut to [0, max_pages * page_size]
+ * kv_pages_assign - room for new_lens[b] >= 0 (less counts as 0) further
+ * tokens of every sequence.  Row r of the T rows is a new token: sequence
+ * 0's first, then sequence 1's, in order (sum of new_lens <= T: tokens behind
+ * row T are not taken; rows behind the last token get slot -1, position 0,
+ * sequence -1).
+ *   slots [T] int64: where the token's row goes, -1 where it has no page;
+ *   positions [T] int32 or NULL: its place in its sequence;  seq_ids [T] int32
+ *   or NULL: its sequence;  lens_out [B] int32, may be seq_lens: the lengths
+ *   with the new tokens that have room;  page_table: the new pages are
+ *   entered, nothing else is written.
+ *   The k-th page needed, counted sequence by sequence, comes off the stack
+ *   k-th.  Where the stack or a table row ends first, the tokens that are left
+ *   over get slot -1 and do not count in lens_out; pool_state[1] is the number of
+ *   pages that the stack was short of.
+ * kv_pages_trim - every sequence keeps its first min(len, keep_lens[b]) tokens
+ * (less than 0 counts as 0: the sequence ends).  The pages behind them go
+ * back to the stack, their table entries become -1; lens_out as above.  It
+ * undoes an assign: with keep_lens the lengths before it, pool and table end
+ * as they were.  An entry outside [0, num_pages) is dropped, not returned.
+ * One launch each.  Calls on one pool must not overlap.  B at most 4096,
+ * max_pages * page_size at most 2^31 - 2^16, B * max_pages below 2^31, T at
+ * most 2^30 (QAFF_E_UNSUPPORTED).  Pages shared by sequences are not counted.
+ */
+int kv_pages_assign(int32_t *page_table, int64_t table_stride, int64_t max_pages, const int32_t *seq_lens,
+                    const int32_t *new_lens, int32_t *lens_out, const int32_t *free_pages, int32_t *pool_state,
+                    int64_t num_pages, int32_t page_size, int64_t B, int64_t *slots, int32_t *positions,
+                    int32_t *seq_ids, int64_t T, void *stream);
+int kv_pages_trim(int32_t *page_table, int64_t table_stride, int64_t max_pages, const int32_t *seq_lens,
+                  const int32_t *keep_lens, int32_t *lens_out, int32_t *free_pages, int32_t *pool_state,
+                  int64_t num_pages, int32_t page_size, int64_t B, void *stream);
+
+/*
+ * rotary_frequencies - the radians a position of each of rotary_dim / 2
+ * pairs, in fp64 (setup call; asynchronous on `stream`):
+ *     f[j] = base^(-2j / rotary_dim), then by `scaling`
+ *   QAFF_ROTARY_LINEAR  f / factor
+ *   QAFF_ROTARY_BASE    base * factor^(rotary_dim / (rotary_dim - 2)) as the base
+ *   QAFF_ROTARY_BANDS   f * (g + (1 - g) / factor), g = (original_len * f / (2 pi)
+ *                       - low) / (high - low) cut to [0, 1]: pairs that turn
+ *                       `high` times or more over original_len positions stay,
+ *                       those that turn `low` times or less are slowed
+ *   inv_freq_out [rotary_dim / 2] f64; rotary_dim even, at most 1024.
+ */
+typedef enum {
+    QAFF_ROTARY_PLAIN = 0,
+    QAFF_ROTARY_LINEAR = 1,
+    QAFF_ROTARY_BASE = 2,
+    QAFF_ROTARY_BANDS = 3
+} qaff_rotary_scaling;
+int rotary_frequencies(double *inv_freq_out, int32_t rotary_dim, double base, int32_t scaling, double factor,
+                       double original_len, double low, double high, void *stream);
+
+/*
+ * rotary - queries and keys turned by their positions: pair j of a head's
+ * first rotary_dim columns, (a, b) = columns (j, j + rotary_dim / 2), or (2j,
+ * 2j + 1) when interleaved, becomes
+ *     (a c - b s, b c + a s),  c, s = magnitude * cos, sin(positions[t] * inv_freq[j]);
+ * the other columns stay.
+ *   inv_freq   [rotary_dim / 2] f64 (rotary_frequencies, or the caller's own)
+ *   q, k       [T, heads, head_dim], [T, kv_heads, head_dim] dtype (BF16 or
+ *              F16), rows dense, token and head strides in elements; heads or
+ *              kv_heads of 0 leaves one out
+ *   q_out, k_out  the same shapes; each may be its input (with its strides),
+ *              and must not overlap it otherwise
+ *   positions  [T] int32, any value
+ * Computed in fp64 and rounded once.  Alignment of 2 bytes; 16-byte aligned
+ * rows with head_dim % 8 == 0 and rotary_dim % 16 == 0 (8 interleaved) run
+ * faster.  A NaN or an infinity stays in its pair.  T below 2^24, heads and
+ * kv_heads at most 4096, head_dim at most 1024 (QAFF_E_UNSUPPORTED).  One launch.
+ */
+typedef struct qaff_rotary {
+    const double *inv_freq;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    double magnitude; /* 1, or the factor that a scaling puts on both turned tensors */
+} qaff_rotary;
+int rotary(const qaff_rotary *rot, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+           int64_t k_token_stride, int64_t k_head_stride, void *q_out, int64_t q_out_token_stride,
+           int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+           const int32_t *positions, int64_t T, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
+           void *stream);
+
+/*
+ * kv_cache_append_rotary_affine - rotary and kv_cache_append_affine in one
+ * launch: q turned into q_out, and the cache rows of the turned keys and of
+ * the values, bit for bit as the two calls give them; the turned keys are
+ * never written.  Arguments as for those; all pointers 16-byte aligned and
+ * strides multiples of 8; rotary_dim % 16 == 0, or % 8 interleaved; heads
+ * may be 0.  A slot outside the cache is skipped (its q row is turned all the
+ * same); T below 2^24, heads and kv_heads at most 4096 (QAFF_E_UNSUPPORTED).
+ */
+int kv_cache_append_rotary_affine(const qaff_kv_cache *cache, const qaff_rotary *rot, const void *q,
+                                  int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                                  int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                  void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                  const int32_t *positions, const int64_t *slots, int64_t T, int32_t heads,
+                                  void *stream);
+
+/*
  * gptq_to_affine_repack - rewrite a GPTQ layer in the affine layout
  * (setup call; it MAY SYNCHRONIZE `stream`: it reads g_idx back to the host
  * to build the permutation and to check it).

@@ -178,3 +178,81 @@ def attention_bound(q, k, v, dtype: str, G: int, bits: int, table, lens, scale: 
                 err += lam * np.sqrt(2 * steps) * u * (p @ vb + np.abs(o)) + 32 * u * (w.sum(0) + p @ vb)
                 bound[b, h] = err
     return out, bound
+
+
+def pages_assign(table, lens, news, free, count: int, page_size: int, pages: int, T: int):
+    """kv_pages_assign token by token; returns (table, slots, positions, seq_ids, lens, count, short)."""
+    table, free, cap = table.copy(), list(free[:count]), table.shape[1] * page_size
+    slots, positions, ids = np.full(T, -1, np.int64), np.zeros(T, np.int32), np.full(T, -1, np.int32)
+    out, short, r = [], 0, 0
+    for b, (n, m) in enumerate(zip(lens.tolist(), news.tolist())):
+        n = min(max(n, 0), cap)
+        end, dry = n, False
+        for t in range(n, n + max(m, 0)):
+            if r == T:
+                break
+            positions[r], ids[r] = t, b
+            if t < cap:
+                p = t // page_size
+                if t % page_size == 0:  # the token opens a page
+                    if free:
+                        table[b, p] = free.pop()
+                    else:
+                        short += 1
+                        dry = True
+                if not dry:
+                    end = t + 1
+                    if 0 <= table[b, p] < pages:
+                        slots[r] = table[b, p] * page_size + t % page_size
+            r += 1
+        out.append(end)
+    return table, slots, positions, ids, np.array(out, np.int32), len(free), short
+
+
+def pages_trim(table, lens, keep, free, count: int, page_size: int, pages: int):
+    """kv_pages_trim: (table, free, lens, count), entries from the last to the first."""
+    table, free, cap = table.copy(), free.copy(), table.shape[1] * page_size
+    out = np.zeros_like(lens)
+    for b in range(len(lens) - 1, -1, -1):
+        n = min(max(int(lens[b]), 0), cap)
+        out[b] = min(max(int(keep[b]), 0), n)
+        for p in range(-(-n // page_size) - 1, -(-int(out[b]) // page_size) - 1, -1):
+            if 0 <= table[b, p] < pages and count < len(free):
+                free[count] = table[b, p]
+                count += 1
+            table[b, p] = -1
+    return table, free, out, count
+
+
+def rotary_frequencies(rotary_dim: int, base: float, scaling=None, factor=1.0, original_len=0.0, low=1.0, high=4.0):
+    r = np.arange(0, rotary_dim, 2) / rotary_dim
+    if scaling == "base":
+        return (base * factor ** (rotary_dim / (rotary_dim - 2))) ** -r
+    f = base**-r
+    if scaling == "linear":
+        return f / factor
+    if scaling == "bands":
+        turns = original_len * f / (2 * np.pi)
+        g = np.clip((turns - low) / (high - low), 0, 1)
+        return (1 - g) * f / factor + g * f
+    return f
+
+
+def rotary(x, positions, inv_freq, dtype: str, interleaved: bool, magnitude: float = 1.0):
+    """(values fp64, slack) of x bits [T, H, D] turned; slack: what fp64 itself may be off by, per value.
+
+    An angle pos * f of fp64 is off by its rounding, 2^-53 of it, a frequency's
+    own 2^-53 and the turns' 2^-53 twice; sines and cosines by a few 2^-53, the
+    products and their sum by 2^-53 each of |a| + |b|.  Together below
+    2^-50 (1 + |angle|) (|a| + |b|) magnitude.
+    """
+    v = oracle.to_f64(x, dtype)
+    half = len(inv_freq)
+    angle = positions.astype(np.float64)[:, None, None] * inv_freq
+    c, s = magnitude * np.cos(angle), magnitude * np.sin(angle)
+    ia, ib = (np.arange(0, 2 * half, 2), np.arange(1, 2 * half, 2)) if interleaved else (np.arange(half), np.arange(half) + half)
+    a, b = v[..., ia], v[..., ib]
+    out, slack = v.copy(), np.zeros_like(v)
+    out[..., ia], out[..., ib] = a * c - b * s, b * c + a * s
+    slack[..., ia] = slack[..., ib] = 2.0**-50 * (1 + np.abs(angle)) * (np.abs(a) + np.abs(b)) * abs(magnitude)
+    return out, slack
