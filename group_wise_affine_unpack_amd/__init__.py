@@ -10,7 +10,7 @@ Functions mirror the C entry points:
     gptq_to_affine_repack, quantize_pack_affine, rmsnorm, rmsnorm_w4a8,
     qgemm_w4a8_codes, kv_cache_append_affine, kv_cache_read_affine,
     paged_attention_affine, kv_pages_assign, kv_pages_trim, rotary,
-    kv_cache_append_rotary_affine
+    kv_cache_append_rotary_affine, qmoe_affine
 """
 from __future__ import annotations
 
@@ -24,7 +24,8 @@ __all__ = ["QaffError", "qmm_affine", "qmm_affine_noalloc", "qgemv_affine", "qge
            "quantize_pack_affine", "dequantize_affine", "qgemv_affine_silu_gate", "smoothquant_factors",
            "w4a8_quantize_weights", "qgemm_w4a8_smooth", "qgemm_w4a8_codes", "rmsnorm", "rmsnorm_w4a8", "AffineKVCache",
            "kv_cache_append_affine", "kv_cache_read_affine", "paged_attention_affine", "KVPagePool", "kv_pages_assign",
-           "kv_pages_trim", "Rotary", "rotary", "kv_cache_append_rotary_affine",
+           "kv_pages_trim", "Rotary", "rotary", "kv_cache_append_rotary_affine", "AffineExperts",
+           "qmoe_affine",
            "release_workspaces", "GemvChain", "library_path", "lib",
            "STATUS", "DTYPE"]
 
@@ -64,6 +65,7 @@ _SIGS = {
     "rotary_frequencies": [_VP, _I32, C.c_double, _I32] + [C.c_double] * 4 + [_VP],
     "rotary": [_VP] + [_VP, _I64, _I64] * 4 + [_VP, _I64] + [_I32] * 4 + [_VP],
     "kv_cache_append_rotary_affine": [_VP] * 2 + [_VP, _I64, _I64] * 4 + [_VP] * 2 + [_I64, _I32, _VP],
+    "qmoe_affine": [_VP] * 3 + [_I32] + [_VP] * 2 + [_I64, _I32, _I32, C.c_double, _VP],
     "qaff_stream_read": [_VP, C.c_uint64, _VP, _I32, _VP],
     "qgemv_affine_chain_plan": [_VP, _I32, _I32, _I32, _I32, C.POINTER(_VP)],
     "qgemv_affine_chain_run": [_VP, _VP],
@@ -94,6 +96,14 @@ class KVCacheArrays(C.Structure):
 class RotarySpec(C.Structure):
     """qaff_rotary (include/qaff.h)."""
     _fields_ = [("inv_freq", _VP), ("rotary_dim", _I32), ("interleaved", _I32), ("magnitude", C.c_double)]
+
+
+class ExpertArrays(C.Structure):
+    """qaff_experts (include/qaff.h)."""
+    _fields_ = [(n, _VP) for n in ("gate_up_packed", "gate_up_scales", "gate_up_biases", "down_packed", "down_scales",
+                                   "down_biases")] + \
+               [("hidden", _I64), ("inner", _I64)] + \
+               [(n, _I32) for n in ("num_experts", "group_size", "bits", "dtype")]
 
 
 class QaffError(RuntimeError):
@@ -727,6 +737,62 @@ def kv_cache_append_rotary_affine(cache: AffineKVCache, q: torch.Tensor, k: torc
     _run("kv_cache_append_rotary_affine", dev, cache.ref, rot.ref, _row_ptr(q), *_strides(q), _row_ptr(k), *_strides(k),
          _row_ptr(v), *_strides(v), _row_ptr(o), *_strides(o), _ptr(positions), _ptr(slots), T, H)
     return o
+
+
+class AffineExperts:
+    """The experts of a mixture-of-experts block in the affine layout (qaff_experts).
+
+    `gate_up` and `down` are triples (packed, scales, biases): packed
+    [E, 2 * inner, hidden * bits / 32] (the gate's rows, then up's) and
+    [E, hidden, inner * bits / 32] int32, scales and biases [.., columns /
+    group_size] in bf16 or f16, the type of the activations.  Holds references
+    to them.
+    """
+
+    def __init__(self, gate_up, down, group_size: int, bits: int):
+        self.gate_up, self.down = tuple(gate_up), tuple(down)
+        if bits not in (2, 4, 8) or group_size not in (32, 64, 128):
+            raise ValueError("bits must be 2, 4 or 8 and group_size 32, 64 or 128")
+        first = self.gate_up[0]
+        E, rows, words = first.shape
+        self.num_experts, self.hidden, self.inner = E, words * 32 // bits, rows // 2
+        self.group_size, self.bits, self.dtype, self.device = group_size, bits, self.gate_up[1].dtype, first.device
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("scales must be bfloat16 or float16")
+        if rows % 2:
+            raise ValueError("gate_up must hold as many rows of up as of the gate")
+        for name, (p, s, b), n, k in (("gate_up", self.gate_up, rows, self.hidden), ("down", self.down, self.hidden, self.inner)):
+            _check_shapes(first, **{name + " packed": (_u32(p), (E, n, k * bits // 32)),
+                                    name + " scales": (s, (E, n, k // group_size)),
+                                    name + " biases": (b, (E, n, k // group_size))})
+            if s.dtype != self.dtype or b.dtype != self.dtype:
+                raise ValueError("scales and biases must have one dtype")
+        self.arrays = ExpertArrays(*[_ptr(t) for t in self.gate_up + self.down], self.hidden, self.inner, E, group_size, bits,
+                                   DTYPE[self.dtype])
+        self.ref = C.addressof(self.arrays)
+
+
+def qmoe_affine(x: torch.Tensor, logits: torch.Tensor, experts: AffineExperts, top_k: int, renormalize: bool = True,
+                scale: float = 1.0, resid: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = resid + scale * sum_e p_e Down_e(silu(Gate_e x) * (Up_e x)) over the top_k experts of each row.
+
+    x [M, hidden], logits [M, E] float32 or x's type (ties go to the lowest
+    index, minus infinity is never chosen); p is the softmax over the chosen
+    (renormalize) or over all experts.  M is at most 256.  out may be resid.
+    """
+    dev = experts.device
+    M = x.shape[0]
+    shape = (M, experts.hidden)
+    if x.shape != shape or x.device != dev or logits.shape != (M, experts.num_experts) or logits.device != dev:
+        _check_shapes(experts.down[0], x=(x, shape), logits=(logits, (M, experts.num_experts)))
+    if x.dtype != experts.dtype or (resid is not None and resid.dtype != x.dtype):
+        raise ValueError(f"x and resid must be {experts.dtype}")
+    if resid is not None:
+        _check_shapes(x, resid=(resid, shape))
+    y = _out(out, x)
+    _run("qmoe_affine", dev, experts.ref, _ptr(x), _ptr(logits), _dt(logits), _ptr(resid), _ptr(y), M, top_k,
+         int(bool(renormalize)), scale)
+    return y
 
 
 def gptq_to_affine_repack(qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tensor,

@@ -304,6 +304,33 @@ hipError_t launch_rotary(const RotArgs& a, hipStream_t s);
 // k and v into the cache, 16-byte aligned rows
 hipError_t launch_rotary_append(const RotArgs& a, const KvCache& c, hipStream_t s);
 
+// A mixture-of-experts block (moe.h, moe.hip)
+struct MoeArgs {
+  const void* x;        // [M, N]
+  const void* logits;   // [M, E]
+  const void* resid;    // [M, N] or null
+  void* y;              // [M, N]
+  const uint32_t *gate_up_packed, *down_packed;  // [E, 2 I, N*bits/32], [E, N, I*bits/32]
+  const uint16_t *gate_up_scales, *gate_up_biases, *down_scales, *down_biases;
+  int M, N, I, E, top_k, G, bits, act_dt, logit_dt, renormalize;
+  float scale;
+  // scratch
+  int* counts;     // [slots][tokens of the slot's expert, expert]
+  int* lists;      // [slots, M] its pairs, token * top_k + rank
+  float* weights;  // [pairs] exp(logit - largest)
+  float* h;        // [pairs, I]
+  float* part;     // [pairs, N]
+};
+struct MoeShape {
+  int K;             // columns of the product
+  int pairs;         // slots are pairs, not experts
+  int rows;          // x rows a pass
+  int chunk_steps;   // steps of four spans between two fillings of LDS
+  int chunk_groups;  // groups of a row in LDS
+  int x_bytes;       // x rows' part of LDS
+};
+hipError_t launch_moe(MoeArgs& a, hipStream_t s);
+
 struct PagedAttnArgs {
   KvCache c;
   const void* q;          // [B, heads, D], strides qts (sequence), qhs (head)

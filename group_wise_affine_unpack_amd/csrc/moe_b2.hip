@@ -1,0 +1,8 @@
+// Mixture-of-experts products on 2-bit codes.
+#include "moe.h"
+
+namespace qaff {
+
+hipError_t launch_moe_b2(const MoeArgs& a, bool down, hipStream_t s) { return launch_moe_bits<2>(a, down, s); }
+
+}  // namespace qaff

@@ -1,0 +1,8 @@
+// Mixture-of-experts products on 8-bit codes.
+#include "moe.h"
+
+namespace qaff {
+
+hipError_t launch_moe_b8(const MoeArgs& a, bool down, hipStream_t s) { return launch_moe_bits<8>(a, down, s); }
+
+}  // namespace qaff

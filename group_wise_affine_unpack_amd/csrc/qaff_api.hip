@@ -836,6 +836,68 @@ int kv_cache_append_rotary_affine(const qaff_kv_cache* cache, const qaff_rotary*
   return ok();
 }
 
+int qmoe_affine(const qaff_experts* w, const void* x, const void* logits, int32_t logit_dtype, const void* resid, void* y,
+                int64_t M, int32_t top_k, int32_t renormalize, double scale, void* stream) {
+  if (!w) return fail(QAFF_E_INVAL, "null experts");
+  if (!(w->bits == 2 || w->bits == 4 || w->bits == 8)) return fail(QAFF_E_INVAL, "bits must be 2, 4 or 8 (got %d)", w->bits);
+  if (!group_ok(w->group_size)) return fail(QAFF_E_INVAL, "group_size must be 32, 64 or 128 (got %d)", w->group_size);
+  if (!act_dtype_ok(w->dtype)) return fail(QAFF_E_INVAL, "dtype must be QAFF_BF16 or QAFF_F16 (got %d)", w->dtype);
+  if (logit_dtype != QAFF_F32 && logit_dtype != w->dtype)
+    return fail(QAFF_E_INVAL, "logit_dtype must be QAFF_F32 or the experts' dtype (got %d)", logit_dtype);
+  if (w->num_experts < 1 || w->hidden < 1 || w->inner < 1)
+    return fail(QAFF_E_INVAL, "num_experts, hidden and inner must be >= 1");
+  if (w->hidden % w->group_size || w->inner % w->group_size)
+    return fail(QAFF_E_INVAL, "hidden=%lld and inner=%lld must be multiples of group_size=%d", (long long)w->hidden,
+                (long long)w->inner, w->group_size);
+  if (M < 0) return fail(QAFF_E_INVAL, "M must be >= 0 (got %lld)", (long long)M);
+  if (top_k < 1 || top_k > w->num_experts)
+    return fail(QAFF_E_INVAL, "top_k=%d must lie in [1, num_experts=%d]", top_k, w->num_experts);
+  if (renormalize != 0 && renormalize != 1) return fail(QAFF_E_INVAL, "renormalize must be 0 or 1");
+  if (!(scale > -1e30 && scale < 1e30)) return fail(QAFF_E_INVAL, "scale must be finite");
+  if (w->num_experts > 1024) return fail(QAFF_E_UNSUPPORTED, "num_experts above 1024 (got %d)", w->num_experts);
+  if (w->hidden > (1 << 16) || w->inner > (1 << 16)) return fail(QAFF_E_UNSUPPORTED, "hidden or inner above 65536");
+  if (w->hidden * w->bits % 128 || w->inner * w->bits % 128)
+    return fail(QAFF_E_UNSUPPORTED, "weight rows must be whole 16-byte chunks (hidden * bits and inner * bits multiples of 128)");
+  if (M > 256) return fail(QAFF_E_UNSUPPORTED, "M above 256 (got %lld): split the batch", (long long)M);
+  if (M == 0) return ok();
+  if (!x || !logits || !y || !w->gate_up_packed || !w->gate_up_scales || !w->gate_up_biases || !w->down_packed ||
+      !w->down_scales || !w->down_biases)
+    return fail(QAFF_E_INVAL, "null tensor pointer");
+  if (!aligned16(x) || !aligned16(y) || !aligned16(w->gate_up_packed) || !aligned16(w->gate_up_scales) ||
+      !aligned16(w->gate_up_biases) || !aligned16(w->down_packed) || !aligned16(w->down_scales) ||
+      !aligned16(w->down_biases))
+    return fail(QAFF_E_ALIGN, "x, y and the experts' arrays must be 16-byte aligned");
+  if (!aligned(resid, 2) || !aligned(logits, logit_dtype == QAFF_F32 ? 4 : 2))
+    return fail(QAFF_E_ALIGN, "resid and logits must be aligned to their elements");
+  qaff::MoeArgs a{};
+  a.x = x;
+  a.logits = logits;
+  a.resid = resid;
+  a.y = y;
+  a.gate_up_packed = w->gate_up_packed;
+  a.gate_up_scales = static_cast<const uint16_t*>(w->gate_up_scales);
+  a.gate_up_biases = static_cast<const uint16_t*>(w->gate_up_biases);
+  a.down_packed = w->down_packed;
+  a.down_scales = static_cast<const uint16_t*>(w->down_scales);
+  a.down_biases = static_cast<const uint16_t*>(w->down_biases);
+  a.M = (int)M;
+  a.N = (int)w->hidden;
+  a.I = (int)w->inner;
+  a.E = w->num_experts;
+  a.top_k = top_k;
+  a.G = w->group_size;
+  a.bits = w->bits;
+  a.act_dt = w->dtype;
+  a.logit_dt = logit_dtype;
+  a.renormalize = renormalize;
+  a.scale = (float)scale;
+  (void)hipGetLastError();
+  const hipError_t e = qaff::launch_moe(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return fail(QAFF_E_UNSUPPORTED, "this shape has no kernel");
+  if (e != hipSuccess) return hip_fail(e, "mixture-of-experts launch");
+  return ok();
+}
+
 int gptq_to_affine_repack(const int32_t* qweight, const int32_t* qzeros, const void* scales, const int32_t* g_idx,
                           uint32_t* w_packed_out, void* scales_out, void* biases_out, int32_t bias_dtype,
                           int32_t* k_perm_out, int64_t K, int64_t N, int32_t group_size, void* stream) {

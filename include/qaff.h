@@ -627,6 +627,48 @@ int kv_cache_append_rotary_affine(const qaff_kv_cache *cache, const qaff_rotary 
                                   void *stream);
 
 /*
+ * qmoe_affine - a mixture-of-experts block on affine experts for a few tokens,
+ * from the router's logits to the block's output:
+ *     y[m,:] = resid[m,:] + scale * sum over m's choices e of
+ *              p[m,e] * Down_e ( silu(Gate_e x[m,:]) * (Up_e x[m,:]) )
+ *   choices: the top_k largest logits, ties to the lowest index; minus
+ *     infinity (or a NaN) is never chosen: a row of them is resid alone, or 0
+ *   p = exp(logit) over its sum, over the choices with renormalize = 1, over
+ *     all experts with 0
+ *   x [M, hidden], resid [M, hidden] or NULL, y [M, hidden] dtype (y may be
+ *   resid); logits [M, num_experts] F32 or dtype.  x, y 16-byte aligned.
+ *   experts: per expert Gate's inner rows, then Up's, and Down, as qmm_affine
+ *   has a weight; every array 16-byte aligned, scales and biases in dtype
+ *   (BF16 or F16); hidden and inner multiples of group_size (G in {32, 64,
+ *   128}), at most 65536, with rows of whole 16-byte chunks
+ *   num_experts at most 1024; M at most 256 (QAFF_E_UNSUPPORTED)
+ * Accuracy: x is held exactly down to 2^-25 of its row's largest entry, the
+ * inner row to 22 bits, sums in fp32, one rounding at the end; for finite
+ * inputs within a few 2^-20 of the sum of the products' sizes, before it.  A
+ * token whose logits hold a NaN, or whose x is not finite, gives a row that is
+ * not finite (the former NaN); other tokens' rows are not touched by it.
+ * Weights are read once per 16 tokens of an expert (Down: 8), only those of
+ * chosen experts.  Uses library scratch: capture after an eager call of the
+ * same shapes.  The same call gives the same bits.
+ */
+typedef struct qaff_experts {
+    const uint32_t *gate_up_packed; /* [num_experts, 2*inner, hidden*bits/32] */
+    const void *gate_up_scales;     /* [num_experts, 2*inner, hidden/G] */
+    const void *gate_up_biases;
+    const uint32_t *down_packed;    /* [num_experts, hidden, inner*bits/32] */
+    const void *down_scales;        /* [num_experts, hidden, inner/G] */
+    const void *down_biases;
+    int64_t hidden;
+    int64_t inner;
+    int32_t num_experts;
+    int32_t group_size;
+    int32_t bits;
+    int32_t dtype;
+} qaff_experts;
+int qmoe_affine(const qaff_experts *experts, const void *x, const void *logits, int32_t logit_dtype, const void *resid,
+                void *y, int64_t M, int32_t top_k, int32_t renormalize, double scale, void *stream);
+
+/*
  * gptq_to_affine_repack - rewrite a GPTQ layer in the affine layout
  * (setup call; it MAY SYNCHRONIZE `stream`: it reads g_idx back to the host
  * to build the permutation and to check it).

@@ -256,3 +256,47 @@ def rotary(x, positions, inv_freq, dtype: str, interleaved: bool, magnitude: flo
     out[..., ia], out[..., ib] = a * c - b * s, b * c + a * s
     slack[..., ia] = slack[..., ib] = 2.0**-50 * (1 + np.abs(angle)) * (np.abs(a) + np.abs(b)) * abs(magnitude)
     return out, slack
+
+
+def moe(x, logits, gate_up, down, dtype: str, G: int, bits: int, top_k: int, renormalize: bool, scale: float = 1.0, resid=None):
+    """(y fp64, size, chosen) of qmoe_affine; logits fp64 [M, E], triples of expert arrays (bits with a dtype tag).
+
+    size: what the kernel's roundings are relative to, of each output: the sum
+    over the chosen experts of p scale times, per group of columns, code sums
+    and bias sums taken by their sizes (sum |x| code |s| + |sum x| |b|), as
+    the kernel adds them, through both products (silu(g) u moves with g by at
+    most 1.1 |u| + |silu(g)|, per step of the larger of them).
+    """
+    M, E = logits.shape
+    xv = oracle.to_f64(x, dtype)
+    y = np.zeros((M, xv.shape[1])) if resid is None else oracle.to_f64(resid, dtype)
+    size, chosen = np.zeros_like(y), []
+    inner = down[0].shape[2] * 32 // bits
+
+    def product(v, triple, e, err):
+        """v W^T and the size of its roundings; err: the size of v's own"""
+        w, s, b = (t[e] for t in triple)
+        c, sv, bv = codes(w, bits).astype(np.float64), oracle.to_f64(s, dtype), oracle.to_f64(b, dtype)
+        big = np.abs(np.repeat(sv, G, -1)) * c + np.repeat(np.abs(bv), G, -1)
+        full = c * np.repeat(sv, G, -1) + np.repeat(bv, G, -1)
+        return v @ full.T, np.abs(v) @ big.T + err @ np.abs(full).T
+
+    for m in range(M):
+        z = logits[m]
+        order = [e for e in sorted(range(E), key=lambda e: (-z[e], e)) if z[e] > -np.inf][:top_k]
+        chosen.append(order)
+        if not order:
+            continue
+        w = np.exp(z - z[order[0]])
+        total = w[order].sum() if renormalize else w.sum()
+        for e in order:
+            a, ea = product(xv[m:m + 1], gate_up, e, np.zeros_like(xv[m:m + 1]))
+            g, u = a[:, :inner], a[:, inner:]
+            sg = g / (1 + np.exp(-g))
+            h = sg * u
+            eh = 1.1 * ea[:, :inner] * np.abs(u) + ea[:, inner:] * np.abs(sg) + 4 * np.abs(h)
+            d, ed = product(h, down, e, eh)
+            p = w[e] / total * scale
+            y[m] += p * d[0]
+            size[m] += abs(p) * ed[0]
+    return y, size, chosen

@@ -164,3 +164,61 @@ def test_oracle_rotary_by_hand():
     assert bands[0] == plain[0] and np.isclose(bands[-1], plain[-1] / 8)
     based = od.rotary_frequencies(64, 1e4, "base", 8.0)
     assert based[0] == plain[0] and np.isclose(based[-1], plain[-1] / 8)
+
+
+def _moe(x=A, logits=A, ldt=2, resid=A, y=A, M=1, top_k=2, renorm=1, scale=1.0, **kw):
+    d = dict(gate_up_packed=A, gate_up_scales=A, gate_up_biases=A, down_packed=A, down_scales=A, down_biases=A, hidden=256,
+             inner=128, num_experts=8, group_size=64, bits=4, dtype=0)
+    return qa.lib().qmoe_affine(C.byref(qa.ExpertArrays(**{**d, **kw})), x, logits, ldt, resid, y, M, top_k, renorm, scale, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(bits=3), INVAL), (dict(group_size=48), INVAL), (dict(dtype=2), INVAL), (dict(ldt=1), INVAL), (dict(ldt=3), INVAL),
+    (dict(num_experts=0), INVAL), (dict(hidden=0), INVAL), (dict(inner=0), INVAL), (dict(hidden=96), INVAL),
+    (dict(inner=96), INVAL), (dict(M=-1), INVAL), (dict(M=257), UNSUP), (dict(top_k=0), INVAL), (dict(top_k=9), INVAL),
+    (dict(renorm=2), INVAL), (dict(scale=float("inf")), INVAL), (dict(scale=float("nan")), INVAL),
+    (dict(num_experts=1025), UNSUP), (dict(hidden=65600), UNSUP), (dict(inner=1 << 17), UNSUP),
+    (dict(hidden=96, inner=96, group_size=32, bits=2), UNSUP), (dict(x=None), INVAL), (dict(logits=None), INVAL),
+    (dict(y=None), INVAL), (dict(gate_up_packed=None), INVAL), (dict(down_biases=None), INVAL), (dict(x=A + 8), ALIGN),
+    (dict(y=A + 2), ALIGN), (dict(down_packed=A + 4), ALIGN), (dict(gate_up_scales=A + 2), ALIGN), (dict(logits=A + 2), ALIGN),
+    (dict(resid=A + 1), ALIGN)])
+def test_moe_argument_errors(kw, code):
+    assert _moe(**kw) == code
+    assert _msg() != ""
+
+
+def test_moe_of_nothing():
+    assert _moe(M=0, x=None, logits=None, y=None, gate_up_packed=None) == OK
+    assert qa.lib().qmoe_affine(None, A, A, 2, None, A, 1, 1, 1, 1.0, None) == INVAL
+
+
+def test_moe_binding_refusals():
+    def triple(e, n, k, dt=torch.float16):
+        return torch.zeros((e, n, k // 8), dtype=torch.int32), torch.zeros((e, n, k // 64), dtype=dt), torch.zeros((e, n, k // 64), dtype=dt)
+    with pytest.raises(ValueError, match="shape"):
+        qa.AffineExperts(triple(2, 256, 64), triple(2, 64, 192), 64, 4)
+    with pytest.raises(ValueError, match="dtype"):
+        qa.AffineExperts(triple(2, 256, 64), triple(2, 64, 128, torch.bfloat16), 64, 4)
+    with pytest.raises(ValueError, match="bits"):
+        qa.AffineExperts(triple(2, 256, 64), triple(2, 64, 128), 64, 3)
+    with pytest.raises(ValueError, match="rows of up"):
+        qa.AffineExperts(triple(2, 255, 64), triple(2, 64, 128), 64, 4)
+    with pytest.raises(ValueError, match="float32"):
+        qa.AffineExperts(triple(2, 256, 64, torch.float32), triple(2, 64, 128, torch.float32), 64, 4)
+
+
+def test_oracle_moe_by_hand():
+    # one column group, weights 1 and 2 times a unit: y = silu(g) u summed over the inner rows, mixed by the softmax
+    import oracle
+    one = oracle.f64_to_f16(np.ones((1, 64)))
+
+    def weight(e, n, k, value):
+        return (np.zeros((e, n, k // 8), np.uint32), np.zeros((e, n, k // 64), np.uint16),
+                np.broadcast_to(oracle.f64_to_f16(np.asarray(value, np.float64)), (e, n, k // 64)).copy())
+    up = weight(2, 128, 64, np.array([1 / 64, 1 / 32])[:, None, None])
+    down = weight(2, 64, 64, 1 / 64)
+    y, _, chosen = od.moe(one, np.array([[0.0, np.log(3)]]), up, down, "f16", 64, 4, 2, True)
+    silu = lambda t: t / (1 + np.exp(-t))
+    assert chosen == [[1, 0]] and np.allclose(y, 0.25 * silu(1) * 1 + 0.75 * silu(2) * 2)
+    y, _, chosen = od.moe(one, np.array([[0.0, np.log(3)]]), up, down, "f16", 64, 4, 1, False, 2.0, one)
+    assert chosen == [[1]] and np.allclose(y, 1 + 2 * 0.75 * silu(2) * 2)

@@ -1,0 +1,261 @@
+"""GPU tests of qmoe_affine against the fp64 definition (oracle.decoder.moe).
+
+Tolerance, derived from the kernel's roundings: a rounding of fp32 is u =
+2^-24 of what it rounds (2 u where the matrix cores may cut).  A group's sums
+of G products and the sum over K/G groups are taken as random walks with a
+factor 6, 6 (2 sqrt(G) + sqrt(K/G)) u of the sizes of what is added (for the
+larger of the two products' K): `size` of the oracle, which carries the first
+product's error through silu and the second product.  x is exact, h is held to
+2^-22, exp, the division and the weights are off by a few u: all below the
+factor's least value, 6 (2 sqrt(32) + 1) = 73.  Then half a step of the output
+type.  The tests show that a lost token's expert or a scale 5% off would fail."""
+import numpy as np
+import pytest
+import torch
+
+import group_wise_affine_unpack_amd as qa
+import oracle
+import oracle.decoder as od
+import synth_inputs as si
+from gpu_util import TORCH_DT, dev16, dev32, host_f64, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0**-24
+HALF = {"bf16": 2.0**-8, "f16": 2.0**-11}
+
+
+def _experts(E, K, I, G, bits, act, seed, spread=1.0):
+    rng = np.random.default_rng(seed)
+    triples = []
+    for rows, cols in ((2 * I, K), (K, I)):
+        packed = rng.integers(0, 2**32, (E, rows, cols * bits // 32), dtype=np.uint32)
+        sigma = np.exp(rng.uniform(-spread, spread, (E, rows, cols // G))) / np.sqrt(cols)
+        s = sigma * 5.5 / (2**bits - 1) * np.where(rng.random(sigma.shape) < 0.1, -1, 1)  # scales below zero too
+        b = -sigma * rng.uniform(2.5, 3.0, sigma.shape)
+        triples.append((packed, si.store(s.astype(np.float32), act), si.store(b.astype(np.float32), act)))
+    return triples
+
+
+def _to_device(triples, act, dev, G, bits):
+    return qa.AffineExperts(*[(dev32(w, dev), dev16(s, act, dev), dev16(b, act, dev)) for w, s, b in triples], G, bits)
+
+
+def _compare(got, ref, size, K, I, G, act):
+    factor = 6 * (2 * np.sqrt(G) + np.sqrt(max(K, I) / G)) * U
+    err, tol = np.abs(got - ref), factor * size * 1.001 + HALF[act] * np.abs(ref) + 2.0**-25
+    # a value past the type's largest by half a step or more rounds to infinity: f16, 65520
+    over = {"f16": 65520.0, "bf16": 2.0**128 * (1 - 2.0**-9)}[act]
+    beyond = np.abs(ref) - factor * size > over
+    assert (got[beyond] == np.copysign(np.inf, ref[beyond])).all()
+    err = np.where(np.isinf(got) & (np.abs(ref) + factor * size >= over), 0.0, err)
+    assert np.isfinite(got[np.abs(ref) + factor * size < over]).all() and not np.isnan(got).any()
+    worst = np.unravel_index(np.argmax(err / tol), err.shape)
+    print(f"[parity] worst {(err / tol)[worst]:.3f} of the bound at {worst}", flush=True)
+    assert (err <= tol).all(), f"{(err > tol).sum()} beyond, worst {(err / tol)[worst]} at {worst}"
+    return tol
+
+
+def _check(M, K, I, E, top_k, G, bits, act, renormalize=True, logit="f32", resid=True, seed=0, scale=1.0, logits=None, x=None):
+    dev = require_gpu()
+    print(f"[case] moe M={M} K={K} I={I} E={E} top_k={top_k} G={G} bits={bits} {act} renorm={renormalize} {logit}", flush=True)
+    rng = np.random.default_rng((seed, M, K, E))
+    triples = _experts(E, K, I, G, bits, act, (seed, 1))
+    if x is None:
+        x = si.store(rng.standard_normal((M, K)).astype(np.float32), act)
+    if logits is None:
+        logits = (1.5 * rng.standard_normal((M, E))).astype(np.float32)
+    zb = logits.astype(np.float32) if logit == "f32" else si.store(logits.astype(np.float32), act)
+    z = zb.astype(np.float64) if logit == "f32" else oracle.to_f64(zb, act)
+    r = si.store(rng.standard_normal((M, K)).astype(np.float32), act) if resid else None
+    experts = _to_device(triples, act, dev, G, bits)
+    zd = torch.from_numpy(zb).to(dev) if logit == "f32" else dev16(zb, act, dev)
+    y = qa.qmoe_affine(dev16(x, act, dev), zd, experts, top_k, renormalize, scale, resid=None if r is None else dev16(r, act, dev))
+    torch.cuda.synchronize()
+    ref, size, chosen = od.moe(x, z, *triples, act, G, bits, top_k, renormalize, scale, r)
+    got = host_f64(y)
+    tol = _compare(got, ref, size, K, I, G, act)
+    # what the bound can tell: outputs with one choice less, and with the experts' part 5% off, are far outside
+    base = ref - (0 if r is None else oracle.to_f64(r, act))
+    part = np.abs(base).max(1) > 1e-3
+    assert ((np.abs(0.05 * base) > 2 * tol).any(1) | ~part).all()
+    return got, chosen
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("bits", [2, 4, 8])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 3, 7])
+def test_widths_groups_types(M, G, bits, act):
+    _check(M, 256, 384, 6, 2, G, bits, act, seed=G + bits)
+    _check(M, 384, 128, 5, 3, G, bits, act, renormalize=False, logit=act, resid=False, seed=G + bits + 1)
+
+
+@pytest.mark.parametrize("bits,G,K,I", [(4, 32, 32, 32), (4, 32, 96, 160), (8, 32, 32, 96), (8, 64, 64, 192), (4, 64, 192, 64),
+                                        (4, 128, 128, 640), (2, 64, 64, 192), (2, 128, 384, 128), (2, 32, 320, 64),
+                                        (4, 64, 2048, 64), (8, 128, 128, 2176), (2, 32, 64, 4160)])
+@pytest.mark.parametrize("M", [1, 5, 20])
+def test_odd_sizes(M, bits, G, K, I):
+    _check(M, K, I, 4, 2, G, bits, "bf16", seed=K + I)
+
+
+@pytest.mark.parametrize("M,E,top_k", [(1, 1, 1), (1, 8, 8), (1, 300, 4), (2, 64, 6), (4, 4, 1), (9, 2, 2), (16, 3, 1), (17, 2, 1),
+                                       (33, 64, 2), (64, 4, 2), (65, 130, 8), (256, 3, 2), (255, 1024, 1), (3, 1024, 20)])
+def test_batches_and_routes(M, E, top_k):
+    _check(M, 64, 64, E, top_k, 32, 4, "f16", seed=M + E)
+    _check(M, 64, 64, E, top_k, 32, 8, "bf16", renormalize=False, logit="bf16", seed=M + E + 1)
+
+
+def test_every_token_to_one_expert():
+    rng = np.random.default_rng(8)
+    z = rng.standard_normal((40, 6)).astype(np.float32)
+    z[:, 4] = 9
+    _check(40, 128, 128, 6, 1, 64, 4, "bf16", logits=z)
+    _check(40, 128, 128, 6, 2, 64, 4, "f16", logits=z)
+
+
+@pytest.mark.parametrize("M", [1, 2, 12])
+def test_ties_go_to_the_lowest_index(M):
+    rng = np.random.default_rng(9)
+    z = rng.integers(0, 2, (M, 16)).astype(np.float32)  # many equal logits
+    z[0] = 1
+    for renormalize in (True, False):
+        _, chosen = _check(M, 64, 96, 16, 5, 32, 4, "f16", renormalize, logits=z)
+        assert chosen[0] == [0, 1, 2, 3, 4]
+
+
+@pytest.mark.parametrize("M", [1, 3, 9])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_masked_logits(M, renormalize):
+    # minus infinity is never chosen: fewer choices than top_k, or none, which leaves the residual
+    rng = np.random.default_rng(10)
+    z = rng.standard_normal((M, 8)).astype(np.float32)
+    z[:, 2:] = -np.inf
+    z[M - 1] = -np.inf
+    got, chosen = _check(M, 64, 64, 8, 4, 32, 4, "bf16", renormalize, logits=z, seed=3)
+    assert chosen[M - 1] == [] and all(len(c) == 2 for c in chosen[:-1])
+    dev = require_gpu()
+    experts = _to_device(_experts(8, 64, 64, 32, 4, "bf16", 1), "bf16", dev, 32, 4)
+    x = torch.randn((M, 64), device=dev).bfloat16()
+    zd = torch.full((M, 8), float("-inf"), device=dev)
+    assert (qa.qmoe_affine(x, zd, experts, 4, renormalize) == 0).all()
+    assert torch.equal(qa.qmoe_affine(x, zd, experts, 4, renormalize, resid=x), x)
+    # the type's lowest value is a number like any other
+    zd[:] = torch.finfo(torch.float32).min
+    y = qa.qmoe_affine(x, zd, experts, 4, renormalize)
+    assert torch.isfinite(y).all() and (y != 0).any()
+
+
+def test_nan_and_infinities_stay_in_their_rows():
+    dev = require_gpu()
+    experts = _to_device(_experts(6, 128, 64, 32, 4, "f16", 2), "f16", dev, 32, 4)
+    x, z = torch.randn((9, 128), device=dev).half(), torch.randn((9, 6), device=dev)
+    good = qa.qmoe_affine(x, z, experts, 2)
+    bad_x, bad_z = x.clone(), z.clone()
+    bad_x[2, 5], bad_x[4, 7] = float("nan"), float("inf")
+    bad_z[6, 1] = float("nan")
+    y = qa.qmoe_affine(bad_x, bad_z, experts, 2)
+    keep = [0, 1, 3, 5, 7, 8]
+    assert torch.equal(y[keep], good[keep])
+    assert torch.isnan(y[6]).all() and not torch.isfinite(y[[2, 4]]).any()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_rows_of_any_size(act):
+    # one wide entry among small ones, tiny and large rows, zeros
+    rng = np.random.default_rng(11)
+    v = rng.standard_normal((8, 256))
+    v[0, 3] = 3000
+    v[1] *= 1e-3 if act == "f16" else 1e-6
+    v[2] *= 200 if act == "f16" else 1e4
+    v[3] = 0
+    v[4] *= np.exp(rng.uniform(-9, 2, 256))
+    _check(8, 256, 128, 3, 2, 64, 4, act, x=si.store(v.astype(np.float32), act), resid=False, seed=5)
+
+
+def test_weights_that_are_not_finite_stay_in_their_column():
+    # a scale next to a row's end is not read for the row before it
+    dev = require_gpu()
+    triples = _experts(2, 96, 96, 32, 4, "bf16", 3)
+    clean = _to_device(triples, "bf16", dev, 32, 4)
+    x, z = torch.randn((2, 96), device=dev).bfloat16(), torch.zeros((2, 2), device=dev)
+    good = qa.qmoe_affine(x, z, clean, 2)
+    triples[1][1][1, 17, 0] = 0x7FC0
+    y = qa.qmoe_affine(x, z, _to_device(triples, "bf16", dev, 32, 4), 2)
+    bad = torch.zeros(96, dtype=torch.bool)
+    bad[17] = True
+    assert torch.isnan(y[:, bad]).all() and torch.equal(y[:, ~bad], good[:, ~bad])
+
+
+def test_in_place_and_repeated():
+    dev = require_gpu()
+    experts = _to_device(_experts(9, 256, 96, 32, 4, "bf16", 4), "bf16", dev, 32, 4)
+    for M in (1, 2, 30):
+        x, z, r = torch.randn((M, 256), device=dev).bfloat16(), torch.randn((M, 9), device=dev), torch.randn((M, 256), device=dev).bfloat16()
+        first = qa.qmoe_affine(x, z, experts, 3, resid=r)
+        for _ in range(3):
+            assert torch.equal(qa.qmoe_affine(x, z, experts, 3, resid=r), first)
+        out = r.clone()
+        assert qa.qmoe_affine(x, z, experts, 3, resid=out, out=out) is out and torch.equal(out, first)
+
+
+def test_batch_rows_do_not_depend_on_each_other():
+    # a row of a batch against the same row alone: other launches, the same sums to within the bound of both
+    dev = require_gpu()
+    triples = _experts(5, 256, 256, 64, 4, "f16", 6)
+    experts = _to_device(triples, "f16", dev, 64, 4)
+    x, z = torch.randn((50, 256), device=dev).half(), torch.randn((50, 5), device=dev)
+    y = qa.qmoe_affine(x, z, experts, 2)
+    one = torch.cat([qa.qmoe_affine(x[i:i + 1].contiguous(), z[i:i + 1].contiguous(), experts, 2) for i in range(50)])
+    ref, size, _ = od.moe(x.cpu().view(torch.int16).numpy().view(np.uint16), z.cpu().double().numpy(), *triples, "f16", 64, 4, 2, True)
+    for got in (y, one):
+        _compare(host_f64(got), ref, size, 256, 256, 64, "f16")
+
+
+def test_empty_batch():
+    dev = require_gpu()
+    experts = _to_device(_experts(2, 64, 64, 32, 4, "f16", 4), "f16", dev, 32, 4)
+    assert qa.qmoe_affine(torch.zeros((0, 64), device=dev).half(), torch.zeros((0, 2), device=dev), experts, 1).shape == (0, 64)
+
+
+def test_captured_call_follows_its_replays():
+    # the routes of the replay, not of the capture; eager work on other shapes in between
+    dev = require_gpu()
+    experts = _to_device(_experts(16, 256, 128, 64, 4, "bf16", 7), "bf16", dev, 64, 4)
+    for M in (1, 6):
+        x, z = torch.randn((M, 256), device=dev).bfloat16(), torch.randn((M, 16), device=dev)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            qa.qmoe_affine(x, z, experts, 4, resid=x)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                y = qa.qmoe_affine(x, z, experts, 4, resid=x)
+        for i in range(6):
+            x.normal_()
+            z.normal_()
+            if i == 3:
+                z[0] = float("-inf")
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            want = qa.qmoe_affine(x, z, experts, 4, resid=x)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), (M, i)
+
+
+def test_two_streams():
+    dev = require_gpu()
+    experts = _to_device(_experts(16, 256, 128, 64, 4, "bf16", 7), "bf16", dev, 64, 4)
+    xs, zs = torch.randn((2, 8, 20, 256), device=dev).bfloat16(), torch.randn((2, 8, 20, 16), device=dev)
+    want = [[qa.qmoe_affine(xs[s, i], zs[s, i], experts, 4) for i in range(8)] for s in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for i in range(8):
+        for s, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[s].append(qa.qmoe_affine(xs[s, i], zs[s, i], experts, 4))
+    torch.cuda.synchronize()
+    for a, b in zip(want[0] + want[1], got[0] + got[1]):
+        assert torch.equal(a, b)
