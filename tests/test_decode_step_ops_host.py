@@ -203,7 +203,7 @@ def test_moe_binding_refusals():
         qa.AffineExperts(triple(2, 256, 64), triple(2, 64, 128), 64, 3)
     with pytest.raises(ValueError, match="rows of up"):
         qa.AffineExperts(triple(2, 255, 64), triple(2, 64, 128), 64, 4)
-    with pytest.raises(ValueError, match="float32"):
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
         qa.AffineExperts(triple(2, 256, 64, torch.float32), triple(2, 64, 128, torch.float32), 64, 4)
 
 
