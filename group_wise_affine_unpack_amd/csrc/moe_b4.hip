@@ -3,6 +3,6 @@
 
 namespace qaff {
 
-hipError_t launch_moe_b4(const MoeArgs& a, bool down, hipStream_t s) { return launch_moe_bits<4>(a, down, s); }
+hipError_t launch_moe_b4(const MoeArgs& a, MoeStep step, hipStream_t s) { return launch_moe_bits<4>(a, step, s); }
 
 }  // namespace qaff

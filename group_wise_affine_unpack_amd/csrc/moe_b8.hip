@@ -3,6 +3,6 @@
 
 namespace qaff {
 
-hipError_t launch_moe_b8(const MoeArgs& a, bool down, hipStream_t s) { return launch_moe_bits<8>(a, down, s); }
+hipError_t launch_moe_b8(const MoeArgs& a, MoeStep step, hipStream_t s) { return launch_moe_bits<8>(a, step, s); }
 
 }  // namespace qaff

@@ -858,6 +858,7 @@ int qmoe_affine(const qaff_experts* w, const void* x, const void* logits, int32_
   if (w->hidden > (1 << 16) || w->inner > (1 << 16)) return fail(QAFF_E_UNSUPPORTED, "hidden or inner above 65536");
   if (w->hidden * w->bits % 128 || w->inner * w->bits % 128)
     return fail(QAFF_E_UNSUPPORTED, "weight rows must be whole 16-byte chunks (hidden * bits and inner * bits multiples of 128)");
+  if (top_k > 64) return fail(QAFF_E_UNSUPPORTED, "top_k above 64 (got %d)", top_k);
   if (M > 256) return fail(QAFF_E_UNSUPPORTED, "M above 256 (got %lld): split the batch", (long long)M);
   if (M == 0) return ok();
   if (!x || !logits || !y || !w->gate_up_packed || !w->gate_up_scales || !w->gate_up_biases || !w->down_packed ||

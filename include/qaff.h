@@ -641,7 +641,8 @@ int kv_cache_append_rotary_affine(const qaff_kv_cache *cache, const qaff_rotary 
  *   has a weight; every array 16-byte aligned, scales and biases in dtype
  *   (BF16 or F16); hidden and inner multiples of group_size (G in {32, 64,
  *   128}), at most 65536, with rows of whole 16-byte chunks
- *   num_experts at most 1024; M at most 256 (QAFF_E_UNSUPPORTED)
+ *   num_experts at most 1024; top_k at most 64 and num_experts; M at most 256
+ *   (QAFF_E_UNSUPPORTED)
  * Accuracy: x is held exactly down to 2^-25 of its row's largest entry, the
  * inner row to 22 bits, sums in fp32, one rounding at the end; for finite
  * inputs within a few 2^-20 of the sum of the products' sizes, before it.  A

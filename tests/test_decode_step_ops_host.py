@@ -176,7 +176,7 @@ def _moe(x=A, logits=A, ldt=2, resid=A, y=A, M=1, top_k=2, renorm=1, scale=1.0, 
     (dict(bits=3), INVAL), (dict(group_size=48), INVAL), (dict(dtype=2), INVAL), (dict(ldt=1), INVAL), (dict(ldt=3), INVAL),
     (dict(num_experts=0), INVAL), (dict(hidden=0), INVAL), (dict(inner=0), INVAL), (dict(hidden=96), INVAL),
     (dict(inner=96), INVAL), (dict(M=-1), INVAL), (dict(M=257), UNSUP), (dict(top_k=0), INVAL), (dict(top_k=9), INVAL),
-    (dict(renorm=2), INVAL), (dict(scale=float("inf")), INVAL), (dict(scale=float("nan")), INVAL),
+    (dict(top_k=65, num_experts=128), UNSUP), (dict(renorm=2), INVAL), (dict(scale=float("inf")), INVAL), (dict(scale=float("nan")), INVAL),
     (dict(num_experts=1025), UNSUP), (dict(hidden=65600), UNSUP), (dict(inner=1 << 17), UNSUP),
     (dict(hidden=96, inner=96, group_size=32, bits=2), UNSUP), (dict(x=None), INVAL), (dict(logits=None), INVAL),
     (dict(y=None), INVAL), (dict(gate_up_packed=None), INVAL), (dict(down_biases=None), INVAL), (dict(x=A + 8), ALIGN),
