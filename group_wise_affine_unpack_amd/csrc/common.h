@@ -315,20 +315,21 @@ struct MoeArgs {
   int M, N, I, E, top_k, G, bits, act_dt, logit_dt, renormalize;
   float scale;
   // scratch
-  int* counts;     // [slots][tokens of the slot's expert, expert]
-  int* lists;      // [slots, M] its pairs, token * top_k + rank
-  int* choices;    // [M] experts chosen
-  float* sums;     // [M] what its weights are divided by; NaN where a logit is
-  float* weights;  // [pairs] exp(logit - largest)
-  float* h;        // [pairs, I]
-  float* part;     // [pairs, N]
+  int* counts;       // [slots][tokens of the slot's expert, expert]
+  int* lists;        // [slots, M] its pairs, token * top_k + rank
+  int* chosen;       // [M] experts chosen
+  float* sums;       // [M] what its weights are divided by; NaN where a logit is
+  float* weights;    // [pairs] exp(logit - largest)
+  uint16_t* choice;  // [pairs] expert, 0xffff for none
+  float* h;          // [pairs, I]
+  float* part;       // [pairs, N]
 };
 struct MoeShape {
   int K;        // columns of the product
+  int pairs;    // slots are pairs, not experts
   int rows;     // x rows a pass
   int tiles;    // a wave's, where it takes whole rows
-  int chunk;    // quads of columns between two fillings of LDS, where it takes a part
-  int x_bytes;  // of a wave's x in LDS
+  int x_bytes;  // x in LDS, a wave's where it takes a part of the columns
 };
 enum MoeStep : int { MOE_UP, MOE_DOWN, MOE_FEW_UP, MOE_FEW_DOWN };
 hipError_t launch_moe(MoeArgs& a, hipStream_t s);

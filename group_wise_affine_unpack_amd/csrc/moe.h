@@ -4,35 +4,36 @@
 // the sum over a token's top_k experts, every matrix codes * scale + bias in
 // groups of G columns.
 //
-// Kernels, for a batch: route (one workgroup: every token's choices, and the
-// tokens of every chosen expert), up (G, U and silu: one f32 row h of each pair
-// of token and choice), down (D on those rows: one f32 partial row a pair),
-// join (a token's pairs added in the order of their logits, the residual, the
-// one rounding).  For up to four tokens two: up, each workgroup of which finds
-// its expert itself, and down, whose workgroups go through all chosen experts
-// and finish y.  No atomics: the same call gives the same bits.
+// Kernels, for a batch: route (a wave a token: its choices), up (G, U and
+// silu: one f32 row h of each pair of token and choice), down (D on those rows:
+// one f32 partial row a pair), join (a token's pairs added in the order of
+// their logits, the residual, the one rounding).  For up to four tokens two:
+// up, each workgroup of which finds its expert itself, and down, whose
+// workgroups go through all chosen experts and finish y.  No atomics: the same
+// call gives the same bits.
 //
 // The products run on the matrix cores for every number of tokens, 16 weight
 // rows a tile and 16 rows of x (M = 1 uses one of them: the matrix cores are
 // idle anyway, and the codes need no arithmetic of their own).  Codes are
 // masked where they lie into f16 pairs, subnormal numbers code * 2^-24 * 2^s;
-// the 2^s is taken out of the x entry that meets it.  x is scaled per row by
-// a power of two so that its largest entry is near 2^15 and held in f16,
-// exact for entries down to 2^-25 of the largest; h, which is f32, as two f16
-// rows, high and low part, 22 bits.  Per group of columns the scale
+// the 2^s is taken out of the x entry that meets it.  x is scaled per row and
+// quad of columns by a power of two so that its largest entry there is near
+// 2^15 and held in f16, exact for entries down to 2^-25 of the largest; h, which
+// is f32, as two f16 rows, high and low part, 22 bits.  Per group of columns the scale
 // multiplies the sum of codes * x, the bias the sum of x, both in fp32.
 //
 // Bound by memory: every chosen expert's weights once.  A wave streams 16 or
 // 32 rows of weights in quads of four spans, a span being 64 bytes of every
-// row: the loads of a quad are issued while the one before is computed.  The
-// parameters of a row's groups come with them, one load a lane: its four lanes
-// take the scales and biases of both tiles and hand them round.  A matrix
-// instruction takes codes of one group only, so the 16-byte pieces that the
-// four lanes of a row hold are exchanged (two or four swaps per four words)
-// where a span is longer than a group.  With many rows a wave takes whole rows
-// (KS = 1) and x, shared by the workgroup, fills LDS once; with few, or long
-// ones, the four waves take a part of the columns each (KS = 4), with their own
-// part of x.
+// row: a quad's loads are issued before the one ahead of it is computed, and
+// unconditionally (past the end they address nothing and return zeros), since
+// a load that may not have been issued makes the compiler wait for all.  The
+// parameters of a row's groups come with them, a lane taking scales and biases
+// of one of two tiles for its neighbour too.  A matrix instruction takes codes of one group only, so
+// the 16-byte pieces that the four lanes of a row hold are exchanged (two or
+// four swaps per four words) where a span is longer than a group.  With many
+// rows a wave takes whole rows (KS = 1) and x, shared by the workgroup, fills
+// LDS once; with few, or long ones, the four waves take a part of the columns
+// each (KS = 4), with their own part of x.
 #pragma once
 
 #include <algorithm>
@@ -136,83 +137,93 @@ struct Span {
   }
 };
 
-// ---- x into LDS -----------------------------------------------------------
+// ---- a quad of x ----------------------------------------------------------
 
-// power of two that brings a row's largest entry into [2^14, 2^15): 1 for a row of zeros, NaN for one that is not finite
-__device__ __forceinline__ float moe_row_scale(float amax) {
+// power of two that brings a quad's largest entry into [2^14, 2^15): 1 for zeros, NaN for one that is not finite
+__device__ __forceinline__ float moe_scale(float amax) {
   if (!(amax <= 0x1.fffffep127f)) return __builtin_nanf("");
   if (amax == 0.f) return 1.f;
   const int e = __builtin_amdgcn_frexp_expf(amax);  // amax in [2^(e-1), 2^e)
   return __builtin_ldexpf(1.f, min(15 - e, 126));
 }
 
-// 4 columns of row `src` from column k as floats; zeros from `end` on
-template <bool DOWN, bool F16_>
-__device__ __forceinline__ void moe_load4(const void* src, int k, int end, float (&v)[4]) {
-  if (k >= end) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 0.f;
-  } else if constexpr (DOWN) {
-    const f32x4_t t = *reinterpret_cast<const f32x4_t*>((const float*)src + k);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = t[i];
-  } else {
-    const u32x2_t t = *reinterpret_cast<const u32x2_t*>((const uint16_t*)src + k);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = (t[i / 2] >> (16 * (i & 1))) & 0xffffu;
-      v[i] = F16_ ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
-    }
-  }
-}
-
-template <bool DOWN, bool F16_>
-__device__ __forceinline__ float moe_amax(const void* src, int k, int end, int step) {
-  float most = 0.f;
-  for (; k < end; k += step) {
-    float v[4];
-    moe_load4<DOWN, F16_>(src, k, end, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) most = nan_max(most, fabsf(v[i]));
-  }
-  return most;
-}
-
-// Fragments `from`, from + step, ... below `count` of a row from column col0
-// on, times sc: fragment un = (span * NJ + instruction) * 4 + lane quarter lies
-// at (un * rows + v) * 16 bytes.  In down a row is two, high and low part.
+// COLS columns of a row of x (UP) or h (DOWN), as the fragments that a quad's
+// codes meet: fragment un = (span * NJ + instruction) * 4 + lane quarter.  A
+// wave loads and converts them, 64 fragments at a time.
 template <int BITS, int G, bool F16_, bool DOWN>
-__device__ __forceinline__ void moe_stage(const void* src, float sc, int col0, int K, int from, int step, int count,
-                                          unsigned char* xs, int rows, int v) {
+struct XQuad {
   using S = Span<BITS, G>;
-  for (int un = from; un < count; un += step) {
-    const int hh = un & 3, sj = un >> 2, span = sj / S::NJ, j = sj % S::NJ;
-    int lo, hi;
-    S::columns(j, hh, lo, hi);
-    const int base = col0 + span * S::CODES;
-    float va[4], vb[4];
-    moe_load4<DOWN, F16_>(src, base + lo, K, va);
-    moe_load4<DOWN, F16_>(src, base + hi, K, vb);
-    u32x4_t top, low;
+  static constexpr int COLS = 4 * S::CODES, UNITS = 16 * S::NJ, UPL = (UNITS + 63) / 64, ELEM = DOWN ? 4 : 2;
+  typedef typename std::conditional<DOWN, u32x4_t, u32x2_t>::type raw_t;
+  raw_t lo[UPL], hi[UPL];
+
+  // quad q of the row at `row` (uniform) of K columns; there = false: zeros, and nothing is read
+  __device__ __forceinline__ void load(const void* row, int K, int q, int lane, bool there) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(row, there ? (uint32_t)(K * ELEM) : 0u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = va[i] * sc, y = vb[i] * sc;
-      const _Float16 xh = (_Float16)x, yh = (_Float16)y;
-      top[i] = f32_to_f16_bits((float)xh * S::unit(i)) | (uint32_t)f32_to_f16_bits((float)yh * S::unit(i)) << 16;
-      if constexpr (DOWN)
-        low[i] = f32_to_f16_bits((x - (float)xh) * S::unit(i)) |
-                 (uint32_t)f32_to_f16_bits((y - (float)yh) * S::unit(i)) << 16;
+    for (int u = 0; u < UPL; ++u) {
+      const int un = lane + 64 * u, sj = un >> 2;
+      int l, h;
+      S::columns(sj % S::NJ, un & 3, l, h);
+      const int base = q * COLS + sj / S::NJ * S::CODES;
+      const uint32_t ol = un < UNITS ? (uint32_t)(base + l) * ELEM : MOE_OOB, oh = un < UNITS ? (uint32_t)(base + h) * ELEM : MOE_OOB;
+      if constexpr (DOWN) {
+        lo[u] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)ol, 0, 0));
+        hi[u] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)oh, 0, 0));
+      } else {
+        lo[u] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)ol, 0, 0));
+        hi[u] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)oh, 0, 0));
+      }
     }
-    unsigned char* dst = xs + ((size_t)un * rows + v) * 16;
-    *reinterpret_cast<u32x4_t*>(dst) = top;
-    if constexpr (DOWN) *reinterpret_cast<u32x4_t*>(dst + 16) = low;
   }
+
+  __device__ static __forceinline__ float value(const raw_t& r, int i) {
+    if constexpr (DOWN) {
+      return __uint_as_float(r[i]);
+    } else {
+      const uint32_t b = (r[i / 2] >> (16 * (i & 1))) & 0xffffu;
+      return F16_ ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
+    }
+  }
+
+  // row v (and v + 1 in down) of xs [UNITS][rows][16 bytes]; returns what takes the sums back, 1 / scale
+  __device__ __forceinline__ float put(unsigned char* xs, int rows, int v, int lane) const {
+    float most = 0.f;
+#pragma unroll
+    for (int u = 0; u < UPL; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most = nan_max(most, nan_max(fabsf(value(lo[u], i)), fabsf(value(hi[u], i))));
+    const float sc = moe_scale(wave_max_f32(most));
+#pragma unroll
+    for (int u = 0; u < UPL; ++u) {
+      const int un = lane + 64 * u;
+      u32x4_t top, low;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = value(lo[u], i) * sc, y = value(hi[u], i) * sc;
+        const _Float16 xh = (_Float16)x, yh = (_Float16)y;
+        top[i] = f32_to_f16_bits((float)xh * S::unit(i)) | (uint32_t)f32_to_f16_bits((float)yh * S::unit(i)) << 16;
+        if constexpr (DOWN)
+          low[i] = f32_to_f16_bits((x - (float)xh) * S::unit(i)) |
+                   (uint32_t)f32_to_f16_bits((y - (float)yh) * S::unit(i)) << 16;
+      }
+      if (UNITS % 64 == 0 || un < UNITS) {
+        unsigned char* dst = xs + (un * rows + v) * 16;
+        *reinterpret_cast<u32x4_t*>(dst) = top;
+        if constexpr (DOWN) *reinterpret_cast<u32x4_t*>(dst + 16) = low;
+      }
+    }
+    return 1.f / sc;
+  }
+};
+
+template <bool DOWN>
+__device__ __forceinline__ const void* moe_source(const MoeArgs& a, int pair) {
+  pair = __builtin_amdgcn_readfirstlane(pair);
+  return DOWN ? (const void*)(a.h + (long)pair * a.I) : (const void*)((const uint16_t*)a.x + (long)(pair / a.top_k) * a.N);
 }
 
 // ---- the stream of weights ------------------------------------------------
-
-typedef __attribute__((ext_vector_type(2), aligned(4))) uint32_t u32x2_a4;
-typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_a4;
 
 // A wave's view of NT tiles of 16 rows of one expert's matrix.
 template <int BITS, int G, bool F16_, int NT>
@@ -223,75 +234,82 @@ struct Stream {
   static constexpr int COLS = 4 * S::CODES;    // columns of a quad
   struct Quad {
     u32x4_t w[4][NT];
-    uint32_t p[QG / 2];  // two groups of this lane's plane: scales, biases of tile 0, of tile 1 by h (of one tile, by h % 2)
+    uint32_t s[QG / 2 + 1], b[QG / 2 + 1];  // two groups each, of tile h % NT; a word more for rows that start between words
   };
-  __amdgpu_buffer_rsrc_t rw[NT];
-  const uint16_t* plane;
-  uint32_t woff;
-  int row_bytes, ng, h;
+  __amdgpu_buffer_rsrc_t rw[NT], rs, rb;
+  uint32_t woff, poff;
+  int row_bytes, h;
 
   __device__ __forceinline__ void open(const uint32_t* packed, const uint16_t* scales, const uint16_t* biases, long row0,
                                        long row1, int K, int lane) {
-    const int c = lane & 15;
+    const int c = lane & 15, ng = K / G;
     h = lane >> 4;
     row_bytes = K * BITS / 8;
-    ng = K / G;
     rw[0] = make_rsrc((const char*)packed + row0 * row_bytes, 16u * (uint32_t)row_bytes);
     if constexpr (NT == 2) rw[1] = make_rsrc((const char*)packed + row1 * row_bytes, 16u * (uint32_t)row_bytes);
     woff = (uint32_t)(c * row_bytes + h * 16);
-    plane = ((h & 1) ? biases : scales) + ((NT == 2 && (h >> 1) ? row1 : row0) + c) * ng;
+    const uint32_t apart = (uint32_t)(row1 - row0);
+    rs = make_rsrc(scales + row0 * ng, (apart + 16u) * (uint32_t)ng * 2u);
+    rb = make_rsrc(biases + row0 * ng, (apart + 16u) * (uint32_t)ng * 2u);
+    poff = ((NT == 2 && (h & 1) ? apart : 0u) + (uint32_t)c) * (uint32_t)ng * 2u;
   }
 
+  __device__ __forceinline__ void params(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t (&d)[QG / 2 + 1]) const {
+    constexpr int N = QG / 2;
+    if constexpr (N == 1) {
+      const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+      d[0] = v[0];
+      d[1] = v[1];
+    } else {
+      if constexpr (N == 2) {
+        const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+        d[0] = v[0];
+        d[1] = v[1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+          const u32x4_t v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + 16 * i), 0, 0));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[4 * i + k] = v[k];
+        }
+      }
+      d[N] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)(off + 4 * N), 0, 0);
+    }
+  }
+
+  // quad q; past the rows' end (q of the row's number of quads, say): zeros, and nothing is read
   __device__ __forceinline__ void load(int q, Quad& d) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = (4 * q + i) * 64;
-      const uint32_t off = at + h * 16 < row_bytes ? woff + (uint32_t)at : MOE_OOB;  // (past a row's end: zeros)
+      const uint32_t off = at + h * 16 < row_bytes ? woff + (uint32_t)at : MOE_OOB;
 #pragma unroll
       for (int t = 0; t < NT; ++t) d.w[i][t] = moe_ld128(rw[t], off);
     }
-    const int g0 = q * QG;
-    if (g0 + QG <= ng && !(ng & 1)) {  // (rows of an odd number of groups start between words)
-      const uint16_t* p = plane + g0;
-      if constexpr (QG == 2) {
-        d.p[0] = *reinterpret_cast<const uint32_t*>(p);
-      } else if constexpr (QG == 4) {
-        const u32x2_a4 v = *reinterpret_cast<const u32x2_a4*>(p);
-        d.p[0] = v[0];
-        d.p[1] = v[1];
-      } else {
-#pragma unroll
-        for (int i = 0; i < QG / 8; ++i) {
-          const u32x4_a4 v = reinterpret_cast<const u32x4_a4*>(p)[i];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) d.p[4 * i + k] = v[k];
-        }
-      }
-    } else {  // a row's last group in the place of those behind it, which meet codes and x of zero
-#pragma unroll
-      for (int i = 0; i < QG / 2; ++i)
-        d.p[i] = plane[min(g0 + 2 * i, ng - 1)] | (uint32_t)plane[min(g0 + 2 * i + 1, ng - 1)] << 16;
-    }
+    const uint32_t off = q * 256 < row_bytes ? (poff + (uint32_t)(q * QG * 2)) & ~3u : MOE_OOB;
+    params(rs, off, d.s);
+    params(rb, off, d.b);
   }
 
-  // acc += quad times x; xa: this lane's x of the quad's first fragment, `stride` bytes from one instruction to the next
+  // acc += quad times x; xa: this lane's x of the quad's first fragment, `stride` bytes from one instruction to the next.
+  // left: groups of the row from the quad on.
   template <int NI>
-  __device__ __forceinline__ void compute(Quad& d, const unsigned char* xa, int stride, float (&acc)[NT][NI]) const {
+  __device__ __forceinline__ void compute(Quad& d, const unsigned char* xa, int stride, int left, float (&acc)[NT][NI]) const {
     const uint32_t half = (h >> 1) ? 0x0c030c02u : 0x0c010c00u;
     const f16x8_t ones = __builtin_bit_cast(f16x8_t, u32x4_t{S::ones(0), S::ones(1), S::ones(2), S::ones(3)});
-    uint32_t pl[2 * NT];
+    const uint32_t odd = (poff & 2u) * 8u;  // bits that this lane's parameters are off by
+    uint32_t ps[2], pb[2];
 #pragma unroll
     for (int gi = 0; gi < QG; ++gi) {
       if ((gi & 1) == 0) {
-        uint32_t a = d.p[gi / 2];
+        // (behind a row's end lies the next one's, which may not be finite; codes and x are zeros there)
+        const uint32_t there = gi + 1 < left ? 0xffffffffu : gi < left ? 0xffffu : 0u;
+        ps[0] = ps[1] = __builtin_amdgcn_alignbit(d.s[gi / 2 + 1], d.s[gi / 2], odd) & there;
+        pb[0] = pb[1] = __builtin_amdgcn_alignbit(d.b[gi / 2 + 1], d.b[gi / 2], odd) & there;
         if constexpr (NT == 2) {
-          uint32_t b = a;
-          swap32(a, b);
-          pl[2] = pl[3] = b;
-          swap16(pl[2], pl[3]);
+          swap16(ps[0], ps[1]);
+          swap16(pb[0], pb[1]);
         }
-        pl[0] = pl[1] = a;
-        swap16(pl[0], pl[1]);
       }
       f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, dot[NT];
 #pragma unroll
@@ -315,57 +333,41 @@ struct Stream {
           const uint32_t b = (gi & 1) ? v >> 16 : v & 0xffffu;
           return F16_ ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
         };
-        const float s = value(pl[2 * t]), b = value(pl[2 * t + 1]);
+        const float s = value(ps[t]), b = value(pb[t]);
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[t][i] = fmaf(s, dot[t][i], fmaf(b, sum[i], acc[t][i]));
       }
+      if ((gi + 1) * MPG % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // (else x and codes of many groups are made at once)
     }
+    // (sums that only some lanes go on to use would be put off until then, and every group's kept in registers: 284, not 160)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(acc[t][i]));
   }
 };
 
-// acc += quads [q0, q1) of the stream, x from LDS (xa as in compute, for quad q0)
-template <int NI, class St, int NT>
-__device__ __forceinline__ void moe_quads(const St& st, int q0, int q1, typename St::Quad& a, const unsigned char* xa, int stride,
-                                          float (&acc)[NT][NI]) {
-  // `a` holds quad q0 already
-  typename St::Quad b;
-  const int quad = St::QG * St::MPG * stride;
-  for (int q = q0; q < q1; q += 2, xa += 2 * quad) {
-    if (q + 1 < q1) st.load(q + 1, b);
-    st.template compute<NI>(a, xa, stride, acc);
-    if (q + 1 < q1) {
-      if (q + 2 < q1) st.load(q + 2, a);
-      st.template compute<NI>(b, xa + quad, stride, acc);
-    }
-  }
-}
-
-// ---- routing of a few tokens ----------------------------------------------
+// ---- routing ----------------------------------------------------------------
 
 constexpr int MOE_FEW = 4;  // tokens whose experts each workgroup finds for itself
 
-// The r-th choice of token m, found by every workgroup of its slot: the expert
-// and the pairs of the tokens that chose it too, when m is the first of them.
-// z: [M, E] logits in LDS.  The slot's first workgroup leaves what down needs.
 struct MoeFew {
   int found, count;
-  int list[MOE_FEW], rank[MOE_FEW];
+  int pair[MOE_FEW];  // of each token, -1 where it has not chosen the expert
+  int rank[MOE_FEW];
   float weight[MOE_FEW];
   float part[4];
   int cpart[4];
 };
-__device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, float* z, MoeFew& l) {
+
+// The expert of slot m * top_k + r, the r-th choice of token m, found by every
+// workgroup of the slot, and which tokens chose it; count = 0 unless m is the
+// first of them.  z: [M, E] logits, a NaN as minus infinity, in LDS; nan: one
+// of token m's that this thread loaded was.  The slot's first workgroup
+// (leave) writes what down needs.
+__device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, const float* z, bool nan, MoeFew& l) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m = slot / a.top_k, r = slot - m * a.top_k;
-  bool nan = false;
-  if (threadIdx.x == 0) l.found = -1;
-  for (int i = threadIdx.x; i < a.M * a.E; i += 256) {
-    const float v = load_as_f32(a.logits, i, a.logit_dt);
-    z[i] = v == v ? v : -__builtin_inff();
-    nan |= v != v && i / a.E == m;
-  }
-  __syncthreads();
-  // every expert's place among token m's
   const float* zm = z + m * a.E;
   float sum = 0.f, top = -__builtin_inff();
   int chosen = 0;
@@ -376,7 +378,11 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
   for (int e = threadIdx.x; e < a.E; e += 256) {
     const float z0 = zm[e];
     int rank = 0;
-    for (int o = 0; o < a.E; ++o) rank += zm[o] > z0 || (zm[o] == z0 && o < e);
+#pragma unroll 8
+    for (int o = 0; o < a.E; ++o) {
+      const float v = zm[o];
+      rank += v > z0 || (v == z0 && o < e);
+    }
     const bool there = z0 > -__builtin_inff();
     if (rank == r && there) l.found = e;
     if (there && (rank < a.top_k || !a.renormalize)) sum += expf(z0 - top);
@@ -395,10 +401,10 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
   __syncthreads();
   if (meta && threadIdx.x == 0) {
     a.sums[m] = l.part[0] + l.part[1] + l.part[2] + l.part[3];
-    a.choices[m] = l.cpart[0] + l.cpart[1] + l.cpart[2] + l.cpart[3];
+    a.chosen[m] = l.cpart[0] + l.cpart[1] + l.cpart[2] + l.cpart[3];
   }
   const int e = l.found;
-  if (wave < a.M && e >= 0) {  // where token `wave` has the expert
+  if (wave < a.M && e >= 0 && (a.M > 1 || leave)) {  // where token `wave` has the expert
     const float* zt = z + wave * a.E;
     const float z0 = zt[e];
     int rank = 0;
@@ -415,28 +421,66 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
       l.weight[wave] = expf(z0 - most);
     }
   }
-  __syncthreads();
+  if (a.M > 1 || leave) __syncthreads();
   if (threadIdx.x == 0) {
     int count = 0, first = -1;
-    for (int t = 0; t < a.M && e >= 0; ++t)
-      if (l.rank[t] < a.top_k) {
-        if (first < 0) first = t;
-        l.list[count] = t * a.top_k + l.rank[t];
-        if (leave) a.weights[t * a.top_k + l.rank[t]] = l.weight[t];
-        ++count;
+    for (int t = 0; t < MOE_FEW; ++t) {
+      int pair = -1;
+      if (t < a.M && e >= 0) {
+        const int rank = a.M > 1 ? l.rank[t] : r;
+        if (rank < a.top_k) {
+          if (first < 0) first = t;
+          pair = t * a.top_k + rank;
+          if (leave) a.weights[pair] = l.weight[t];
+          ++count;
+        }
       }
-    l.count = first == m ? count : 0;  // (else an earlier token's slot takes the expert)
+      l.pair[t] = pair;
+    }
+    if (first != m) count = 0;  // an earlier token's slot takes the expert
+    l.count = count;
     if (leave) {
-      a.counts[2 * slot] = l.count;
+      a.counts[2 * slot] = count;
       a.counts[2 * slot + 1] = e;
-      for (int i = 0; i < l.count; ++i) a.lists[slot * a.M + i] = l.list[i];
+      for (int t = 0, i = 0; t < MOE_FEW; ++t)
+        if (count && l.pair[t] >= 0) a.lists[slot * a.M + i++] = l.pair[t];
     }
   }
   __syncthreads();
   return e;
 }
 
-// ---- kernels ---------------------------------------------------------------
+// The slot's expert and its pairs in the order of the tokens, from every
+// pair's choice: list[0 .. count), at most M of them.  Slots are experts, or,
+// where there are fewer, pairs, the first of which takes its expert.
+__device__ __forceinline__ int moe_collect(const MoeArgs& a, const MoeShape& s, int slot, int* list, int* part, int* expert) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.M * a.top_k;
+  const int e = s.pairs ? a.choice[slot] : slot;
+  *expert = e;
+  if (e == 0xffff) return 0;
+  int count = 0;
+  bool earlier = false;
+  for (int base = 0; base < pairs; base += 256) {
+    const int i = base + (int)threadIdx.x;
+    const bool mine = i < pairs && a.choice[i] == e;
+    const uint64_t all = __ballot(mine);
+    __syncthreads();
+    if (lane == 0) part[wave] = __builtin_popcountll(all);
+    __syncthreads();
+    int at = count + __builtin_popcountll(all & ((1ull << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) at += part[w];
+      count += part[w];
+    }
+    if (mine) list[at] = i;
+  }
+  __syncthreads();
+  if (s.pairs && count) earlier = list[0] < slot;
+  return earlier ? 0 : count;
+}
+
+// ---- products ---------------------------------------------------------------
 
 // Up (DOWN = false): x rows of the activation type; a tile is 16 rows of G and
 // the same 16 of U.  Down: h rows of f32 as two f16 rows each; a tile is 32
@@ -450,113 +494,162 @@ __device__ __forceinline__ void moe_open(const MoeArgs& a, int e, int tile, int 
           DOWN ? a.down_biases : a.gate_up_biases, row0, row0 + (DOWN ? 16 : a.I), K, lane);
 }
 
-template <bool DOWN>
-__device__ __forceinline__ const void* moe_source(const MoeArgs& a, int pair) {
-  return DOWN ? (const void*)(a.h + (long)pair * a.I) : (const void*)((const uint16_t*)a.x + (long)(pair / a.top_k) * a.N);
-}
+__device__ __forceinline__ int moe_vrow(int c, int vrows) { return min((c >> 2) + 4 * (c & 3), vrows - 1); }
 
-// whole rows a wave (KS = 1): the workgroup's x in LDS, then every wave its tiles
+// whole rows a wave (KS = 1), x of all quads in LDS; back: [quad][16 tokens]
 template <int BITS, int G, bool F16_, bool DOWN, int NI>
 __device__ __forceinline__ void moe_rows(const MoeArgs& a, const MoeShape& s, int e, const int* list, int tokens,
-                                         const float* row_scale, const unsigned char* xs, int tile0, int tile1) {
+                                         const float* back, const unsigned char* xs, int tile0, int tile1) {
   using St = Stream<BITS, G, F16_, 2>;
+  if (tile0 >= tile1) return;
   const int lane = threadIdx.x & 63;
   const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens;
-  const int quads = (s.K + St::COLS - 1) / St::COLS;
-  const unsigned char* xa = xs + (h * s.rows + min((c >> 2) + 4 * (c & 3), vrows - 1)) * 16;
-  float back[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) back[i] = 0x1p24f / row_scale[DOWN ? (4 * i + h) / 2 : 4 * i + h];
+  const int quads = (s.K + St::COLS - 1) / St::COLS, ng = s.K / G, stride = 4 * s.rows * 16;
+  const unsigned char* x0 = xs + (h * s.rows + moe_vrow(c, vrows)) * 16;
   St st;
-  typename St::Quad w;
-  if (tile0 >= tile1) return;
+  typename St::Quad w0, w1;
+  int lt = tile0, lq = 0;  // what is loaded next
   moe_open<BITS, G, F16_, DOWN>(a, e, tile0, s.K, lane, st);
-  st.load(0, w);
-  for (int tile = tile0; tile < tile1; ++tile) {
+  const auto next = [&](typename St::Quad& d) __attribute__((always_inline)) {
+    st.load(lt < tile1 ? lq : quads, d);
+    if (++lq == quads) {
+      lq = 0;
+      if (++lt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, lt, s.K, lane, st);
+    }
+  };
+  int tile = tile0, q = 0;  // what is computed next
+  float total[2][NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) total[0][i] = total[1][i] = 0.f;
+  const auto step = [&](typename St::Quad& d) __attribute__((always_inline)) {
     float acc[2][NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
-    moe_quads<NI>(st, 0, quads, w, xa, 4 * s.rows * 16, acc);
-    if (tile + 1 < tile1) {
-      moe_open<BITS, G, F16_, DOWN>(a, e, tile + 1, s.K, lane, st);
-      st.load(0, w);
+    st.template compute<NI>(d, x0 + (size_t)q * St::S::NJ * 4 * stride, stride, ng - q * St::QG, acc);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float f = back[16 * q + (DOWN ? (4 * i + h) / 2 : 4 * i + h)];
+      total[0][i] = fmaf(acc[0][i] * 0x1p24f, f, total[0][i]);
+      total[1][i] = fmaf(acc[1][i] * 0x1p24f, f, total[1][i]);
     }
+    if (++q < quads) return;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int v = 4 * i + h;
       if constexpr (DOWN) {
         // the high and the low part's sums are neighbours: lanes of even h take tile 0's total, of odd h tile 1's
-        uint32_t p = __float_as_uint(acc[0][i]), q = __float_as_uint(acc[1][i]);
-        swap16(p, q);
-        const float sum = __uint_as_float(p) + __uint_as_float(q);
-        if (v / 2 < tokens) a.part[(long)list[v / 2] * a.N + 32 * tile + 16 * (h & 1) + c] = sum * back[i];
+        uint32_t p = __float_as_uint(total[0][i]), r = __float_as_uint(total[1][i]);
+        swap16(p, r);
+        if (v / 2 < tokens)
+          a.part[(long)list[v / 2] * a.N + 32 * tile + 16 * (h & 1) + c] = __uint_as_float(p) + __uint_as_float(r);
       } else {
-        const float g = acc[0][i] * back[i], u = acc[1][i] * back[i];
+        const float g = total[0][i], u = total[1][i];
         if (v < tokens) a.h[(long)list[v] * a.I + 16 * tile + c] = g / (1.f + expf(-g)) * u;
       }
+      total[0][i] = total[1][i] = 0.f;
     }
+    q = 0;
+    ++tile;
+  };
+  next(w0);
+  const int all = (tile1 - tile0) * quads;
+  for (int i = 0; i < all; i += 2) {
+    next(w1);
+    step(w0);
+    next(w0);
+    if (i + 1 < all) step(w1);
   }
 }
 
-// a part of the columns a wave (KS = 4), each with its own x
+// a part of the columns a wave (KS = 4), each with its own x: this wave's sums of its quads of tile `tile`
 template <int BITS, int G, bool F16_, bool DOWN, int NI>
-__device__ __forceinline__ void moe_parts(const MoeArgs& a, const MoeShape& s, int e, const int* list, int tokens,
-                                          unsigned char* xs, float* row_scale, float* red, int tile) {
+__device__ __forceinline__ void moe_part(const MoeArgs& a, const MoeShape& s, int e, const int* list, int tokens,
+                                         unsigned char* mine, float* back, int tile, float (&total)[2][NI]) {
   using St = Stream<BITS, G, F16_, 2>;
+  using Xq = XQuad<BITS, G, F16_, DOWN>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens;
-  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4;
+  const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens, stride = 4 * s.rows * 16;
+  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4, ng = s.K / G;
   const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
+  const unsigned char* xa = mine + (h * s.rows + moe_vrow(c, vrows)) * 16;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) total[0][i] = total[1][i] = 0.f;
   St st;
-  typename St::Quad w;
+  typename St::Quad w0, w1;
+  Xq x0, x1;  // the next quad's x of two tokens
   moe_open<BITS, G, F16_, DOWN>(a, e, tile, s.K, lane, st);
-  if (q0 < q1) st.load(q0, w);
-  unsigned char* mine = xs + wave * s.x_bytes;
-  float* scale = row_scale + 16 * wave;
-  for (int t = 0; t < tokens; ++t) {
-    const float most = moe_amax<DOWN, F16_>(moe_source<DOWN>(a, list[t]), q0 * St::COLS + 4 * lane, min(q1 * St::COLS, s.K), 256);
-    const float sc = moe_row_scale(wave_max_f32(most));
-    if (lane == 0) scale[t] = sc;
-  }
-  float acc[2][NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
-  const unsigned char* xa = mine + (h * s.rows + min((c >> 2) + 4 * (c & 3), vrows - 1)) * 16;
-  for (int q = q0; q < q1; q += s.chunk) {
-    const int end = min(q + s.chunk, q1), units = (end - q) * 4 * St::S::NJ * 4;
-    __builtin_amdgcn_wave_barrier();  // (LDS of this wave alone, whose operations stay in order)
-    for (int t = 0; t < tokens; ++t)
-      moe_stage<BITS, G, F16_, DOWN>(moe_source<DOWN>(a, list[t]), scale[t], q * St::COLS, s.K, lane, 64, units, mine, s.rows,
-                                     DOWN ? 2 * t : t);
+  const void* first = moe_source<DOWN>(a, list[0]);
+  const void* second = moe_source<DOWN>(a, list[min(1, tokens - 1)]);
+  x0.load(first, s.K, q0, lane, q0 < q1);
+  x1.load(second, s.K, q0, lane, q0 < q1 && tokens > 1);
+  st.load(q0 < q1 ? q0 : quads, w0);
+  const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+    // (LDS of this wave alone, whose operations stay in order)
+    float f = x0.put(mine, s.rows, 0, lane);
+    if (lane == 0) back[0] = f;
+    if (tokens > 1) {
+      f = x1.put(mine, s.rows, DOWN ? 2 : 1, lane);
+      if (lane == 0) back[1] = f;
+    }
+    for (int t = 2; t < tokens; t += 2) {
+      x0.load(moe_source<DOWN>(a, list[t]), s.K, q, lane, true);
+      x1.load(moe_source<DOWN>(a, list[min(t + 1, tokens - 1)]), s.K, q, lane, true);
+      f = x0.put(mine, s.rows, DOWN ? 2 * t : t, lane);
+      if (lane == 0) back[t] = f;
+      if (t + 1 < tokens) {
+        f = x1.put(mine, s.rows, DOWN ? 2 * t + 2 : t + 1, lane);
+        if (lane == 0) back[t + 1] = f;
+      }
+    }
+    const bool more = q + 1 < q1;
+    st.load(more ? q + 1 : quads, ahead);
+    x0.load(first, s.K, q + 1, lane, more);
+    x1.load(second, s.K, q + 1, lane, more && tokens > 1);
     __builtin_amdgcn_wave_barrier();
-    if (q > q0) st.load(q, w);
-    moe_quads<NI>(st, q, end, w, xa, 4 * s.rows * 16, acc);
-  }
-  // the waves' sums, each over its own power of two
+    float acc[2][NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int v = 4 * i + h, t = DOWN ? v / 2 : v;
-    const float back = q0 < q1 && t < tokens ? 0x1p24f / scale[t] : 0.f;
+    for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
+    st.template compute<NI>(d, xa, stride, ng - q * St::QG, acc);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) red[((wave * 2 + k) * NI + i) * 64 + lane] = t < tokens ? acc[k][i] * back : 0.f;
+    for (int i = 0; i < NI; ++i) {
+      const int v = 4 * i + h;
+      const float k = back[DOWN ? v / 2 : v];
+      total[0][i] = fmaf(acc[0][i] * 0x1p24f, k, total[0][i]);
+      total[1][i] = fmaf(acc[1][i] * 0x1p24f, k, total[1][i]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  for (int q = q0; q < q1; q += 2) {
+    step(q, w0, w1);
+    if (q + 1 < q1) step(q + 1, w1, w0);
   }
+}
+
+// the four waves' sums added, and the tile's outputs; out: a token's pair, or -1
+template <bool DOWN, int NI>
+__device__ __forceinline__ void moe_finish(const MoeArgs& a, const int* out, int tokens, float* red, int tile, const float (&total)[2][NI]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) red[((wave * 2 + k) * NI + i) * 64 + lane] = total[k][i];
   __syncthreads();
-  const auto total = [&](int k, int v, int col) {
-    float sum = 0.f;
+  const auto sum = [&](int k, int v, int col) {
+    float r = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum += red[((q * 2 + k) * NI + (v >> 2)) * 64 + (v & 3) * 16 + col];
-    return sum;
+    for (int q = 0; q < 4; ++q) r += red[((q * 2 + k) * NI + (v >> 2)) * 64 + (v & 3) * 16 + col];
+    return r;
   };
   if constexpr (DOWN) {
     for (int i = threadIdx.x; i < 32 * tokens; i += 256) {
       const int t = i >> 5, n = i & 31;
-      a.part[(long)list[t] * a.N + 32 * tile + n] = total(n >> 4, 2 * t, n & 15) + total(n >> 4, 2 * t + 1, n & 15);
+      a.part[(long)out[t] * a.N + 32 * tile + n] = sum(n >> 4, 2 * t, n & 15) + sum(n >> 4, 2 * t + 1, n & 15);
     }
   } else {
     const int t = threadIdx.x >> 4, n = threadIdx.x & 15;
-    if (t < tokens) {
-      const float g = total(0, t, n), u = total(1, t, n);
-      a.h[(long)list[t] * a.I + 16 * tile + n] = g / (1.f + expf(-g)) * u;
+    if (t < tokens && out[t] >= 0) {
+      const float g = sum(0, t, n), u = sum(1, t, n);
+      a.h[(long)out[t] * a.I + 16 * tile + n] = g / (1.f + expf(-g)) * u;
     }
   }
   __syncthreads();
@@ -565,123 +658,213 @@ __device__ __forceinline__ void moe_parts(const MoeArgs& a, const MoeShape& s, i
 template <int BITS, int G, bool F16_, bool DOWN, int KS>
 __global__ __launch_bounds__(256) void moe_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 2>;
+  using Xq = XQuad<BITS, G, F16_, DOWN>;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int list[16];
-  __shared__ float row_scale[KS == 4 ? 64 : 16];
-  __shared__ float red[KS == 4 ? 2048 : 64];
+  __shared__ int list[256];
+  __shared__ int part[4];
+  __shared__ float own_back[KS == 4 ? 64 : 1];
+  __shared__ float red[KS == 4 ? 2048 : 1];
   const int slot = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int count = a.counts[2 * slot], e = a.counts[2 * slot + 1];
+  int count, e;
+  if constexpr (DOWN) {
+    count = a.counts[2 * slot];
+    e = a.counts[2 * slot + 1];
+    for (int i = threadIdx.x; i < count; i += 256) list[i] = a.lists[(long)slot * a.M + i];
+    __syncthreads();
+  } else {
+    count = moe_collect(a, s, slot, list, part, &e);
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) {
+        a.counts[2 * slot] = count;
+        a.counts[2 * slot + 1] = e;
+      }
+      for (int i = threadIdx.x; i < count; i += 256) a.lists[(long)slot * a.M + i] = list[i];
+    }
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  count = __builtin_amdgcn_readfirstlane(count);
   const int per_pass = DOWN ? s.rows / 2 : s.rows;
   for (int first = 0; first < count; first += per_pass) {
     const int tokens = min(per_pass, count - first);
-    if (threadIdx.x < 16) list[threadIdx.x] = a.lists[(long)slot * a.M + min(first + (int)threadIdx.x, count - 1)];
-    __syncthreads();
+    const int* mine = list + first;
+    const bool small = (DOWN ? 2 * tokens : tokens) <= 4;
     if constexpr (KS == 4) {
-      if ((DOWN ? 2 * tokens : tokens) <= 4) moe_parts<BITS, G, F16_, DOWN, 1>(a, s, e, list, tokens, lds, row_scale, red, blockIdx.x);
-      else moe_parts<BITS, G, F16_, DOWN, 4>(a, s, e, list, tokens, lds, row_scale, red, blockIdx.x);
+      const auto run = [&](auto n) __attribute__((always_inline)) {
+        float total[2][n.value];
+        moe_part<BITS, G, F16_, DOWN, n.value>(a, s, e, mine, tokens, lds + wave * s.x_bytes, own_back + 16 * wave, blockIdx.x, total);
+        moe_finish<DOWN, n.value>(a, mine, tokens, red, blockIdx.x, total);
+      };
+      if (small) run(std::integral_constant<int, 1>{});
+      else run(std::integral_constant<int, 4>{});
     } else {
-      const int quads = (s.K + St::COLS - 1) / St::COLS, units = quads * 4 * St::S::NJ * 4;
-      for (int t = 0; t < tokens; ++t) {
-        const float most = wave_max_f32(moe_amax<DOWN, F16_>(moe_source<DOWN>(a, list[t]), 4 * (int)threadIdx.x, s.K, 1024));
-        if (lane == 0) red[4 * t + wave] = most;
+      // x: quads of tokens, dealt to the waves, two in flight
+      const int quads = (s.K + St::COLS - 1) / St::COLS, jobs = tokens * quads;
+      float* back = reinterpret_cast<float*>(lds + s.x_bytes);
+      for (int j = wave; j < jobs; j += 8) {
+        const int t0 = j / quads, q0 = j - t0 * quads, k = min(j + 4, jobs - 1), t1 = k / quads, q1 = k - t1 * quads;
+        Xq x0, x1;
+        x0.load(moe_source<DOWN>(a, mine[t0]), s.K, q0, lane, true);
+        x1.load(moe_source<DOWN>(a, mine[t1]), s.K, q1, lane, true);
+        float f = x0.put(lds + (size_t)q0 * Xq::UNITS * s.rows * 16, s.rows, DOWN ? 2 * t0 : t0, lane);
+        if (lane == 0) back[16 * q0 + t0] = f;
+        if (j + 4 < jobs) {
+          f = x1.put(lds + (size_t)q1 * Xq::UNITS * s.rows * 16, s.rows, DOWN ? 2 * t1 : t1, lane);
+          if (lane == 0) back[16 * q1 + t1] = f;
+        }
       }
-      __syncthreads();
-      if (threadIdx.x < 16) {
-        const int t = min((int)threadIdx.x, tokens - 1);
-        row_scale[threadIdx.x] = moe_row_scale(nan_max(nan_max(red[4 * t], red[4 * t + 1]), nan_max(red[4 * t + 2], red[4 * t + 3])));
-      }
-      __syncthreads();
-      for (int t = 0; t < tokens; ++t)
-        moe_stage<BITS, G, F16_, DOWN>(moe_source<DOWN>(a, list[t]), row_scale[t], 0, s.K, threadIdx.x, 256, units, lds, s.rows,
-                                       DOWN ? 2 * t : t);
       __syncthreads();
       const int tile0 = (blockIdx.x * 4 + wave) * s.tiles, tile1 = min(tile0 + s.tiles, DOWN ? a.N / 32 : a.I / 16);
-      if ((DOWN ? 2 * tokens : tokens) <= 4) moe_rows<BITS, G, F16_, DOWN, 1>(a, s, e, list, tokens, row_scale, lds, tile0, tile1);
-      else moe_rows<BITS, G, F16_, DOWN, 4>(a, s, e, list, tokens, row_scale, lds, tile0, tile1);
+      if (small) moe_rows<BITS, G, F16_, DOWN, 1>(a, s, e, mine, tokens, back, lds, tile0, tile1);
+      else moe_rows<BITS, G, F16_, DOWN, 4>(a, s, e, mine, tokens, back, lds, tile0, tile1);
       __syncthreads();
     }
   }
 }
 
-// up for a few tokens: a slot is a pair of token and choice
-template <int BITS, int G, bool F16_>
+// Up for a few tokens: a slot is a pair of token and choice.  x of every token
+// is loaded ahead of the routing, on which it does not depend.
+template <int BITS, int G, bool F16_, int TOK>
 __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) {
+  using St = Stream<BITS, G, F16_, 2>;
+  using Xq = XQuad<BITS, G, F16_, false>;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ float row_scale[64];
+  __shared__ float own_back[4][MOE_FEW];
   __shared__ float red[512];
   __shared__ MoeFew l;
-  const int e = moe_find(a, blockIdx.y, blockIdx.x == 0, reinterpret_cast<float*>(lds), l);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, h = lane >> 4, stride = 4 * TOK * 16;
+  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4, ng = s.K / G;
+  const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
+  float* z = reinterpret_cast<float*>(lds + 4 * s.x_bytes);
+  bool nan = false;
+  if (threadIdx.x == 0) l.found = -1;
+  const int m0 = blockIdx.y / a.top_k;
+  for (int i = threadIdx.x; i < a.M * a.E; i += 256) {
+    const float v = load_as_f32(a.logits, i, a.logit_dt);
+    z[i] = v == v ? v : -__builtin_inff();
+    nan |= v != v && i / a.E == m0;
+  }
+  Xq x[TOK];
+  const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < TOK; ++t)
+      x[t].load((const uint16_t*)a.x + (long)min(t, a.M - 1) * a.N, s.K, q, lane, there && t < a.M);
+  };
+  load_x(q0, q0 < q1);
+  __syncthreads();
+  const int e = __builtin_amdgcn_readfirstlane(moe_find(a, blockIdx.y, blockIdx.x == 0, z, nan, l));
   if (l.count == 0) return;
-  moe_parts<BITS, G, F16_, false, 1>(a, s, e, l.list, l.count, lds, row_scale, red, blockIdx.x);
+  unsigned char* mine = lds + wave * s.x_bytes;
+  const unsigned char* xa = mine + (h * TOK + moe_vrow(c, TOK)) * 16;
+  float total[2][1] = {{0.f}, {0.f}};
+  St st;
+  typename St::Quad w0, w1;
+  moe_open<BITS, G, F16_, false>(a, e, blockIdx.x, s.K, lane, st);
+  st.load(q0 < q1 ? q0 : quads, w0);
+  const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+      const float f = x[t].put(mine, TOK, t, lane);
+      if (lane == 0) own_back[wave][t] = f;
+    }
+    const bool more = q + 1 < q1;
+    st.load(more ? q + 1 : quads, ahead);
+    load_x(q + 1, more);
+    __builtin_amdgcn_wave_barrier();
+    float acc[2][1] = {{0.f}, {0.f}};
+    st.template compute<1>(d, xa, stride, ng - q * St::QG, acc);
+    const float k = own_back[wave][min(h, TOK - 1)];
+    total[0][0] = fmaf(acc[0][0] * 0x1p24f, k, total[0][0]);
+    total[1][0] = fmaf(acc[1][0] * 0x1p24f, k, total[1][0]);
+    __builtin_amdgcn_wave_barrier();
+  };
+  for (int q = q0; q < q1; q += 2) {
+    step(q, w0, w1);
+    if (q + 1 < q1) step(q + 1, w1, w0);
+  }
+  moe_finish<false, 1>(a, l.pair, TOK, red, blockIdx.x, total);
 }
 
-// down for a few tokens: 16 rows of D for all slots, and y
+// Down for a few tokens: 16 rows of D of all slots, whose quads the waves
+// share evenly, and y.
 constexpr int MOE_FEW_WAVES = 8;
-template <int BITS, int G, bool F16_>
+template <int BITS, int G, bool F16_, int TOK>
 __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 1>;
-  constexpr int NI = 2;  // eight x rows: four tokens' two parts
+  using Xq = XQuad<BITS, G, F16_, true>;
+  constexpr int NI = (2 * TOK + 3) / 4, ROWS = 2 * TOK;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ float red[MOE_FEW_WAVES * NI * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4;
-  const int slots = a.M * a.top_k, quads = (a.I + St::COLS - 1) / St::COLS;
+  const int c = lane & 15, h = lane >> 4, stride = 4 * ROWS * 16;
+  // the output that this thread finishes
+  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+  const long at_y = (long)min(m, a.M - 1) * a.N + 16 * blockIdx.x + n;
+  const float resid = a.resid ? load_as_f32(a.resid, at_y, a.act_dt) : 0.f;
+  const float sum = a.sums[min(m, a.M - 1)];
+  const int chosen = a.chosen[min(m, a.M - 1)];
+  const int slots = a.M * a.top_k, quads = (a.I + St::COLS - 1) / St::COLS, ng = a.I / G;
   unsigned char* mine = lds + wave * s.x_bytes;
-  float total[NI] = {0.f, 0.f};
-  // this wave's share of all slots' quads
+  const unsigned char* xa = mine + (h * ROWS + moe_vrow(c, ROWS)) * 16;
+  float total[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) total[i] = 0.f;
   const int all = slots * quads, from = wave * all / MOE_FEW_WAVES, to = (wave + 1) * all / MOE_FEW_WAVES;
   for (int at = from; at < to;) {
     const int slot = at / quads, q0 = at - slot * quads, q1 = min(quads, q0 + to - at);
     at += q1 - q0;
     const int count = a.counts[2 * slot], e = a.counts[2 * slot + 1];
     if (count == 0) continue;
+    int pair[TOK];
+    float weight[TOK];
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+      pair[t] = a.lists[slot * a.M + min(t, count - 1)];
+      weight[t] = a.weights[pair[t]];
+    }
     St st;
-    typename St::Quad w;
+    typename St::Quad w0, w1;
+    Xq x[TOK];
     const long row0 = (long)e * a.N + 16 * blockIdx.x;
     st.open(a.down_packed, a.down_scales, a.down_biases, row0, row0, a.I, lane);
-    st.load(q0, w);
-    float acc[1][NI] = {{0.f, 0.f}};
-    const int* list = a.lists + slot * a.M;
-    const unsigned char* xa = mine + (h * s.rows + min((c >> 2) + 4 * (c & 3), 2 * count - 1)) * 16;
-    float scale[MOE_FEW];
+    const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < MOE_FEW; ++t) {
-      scale[t] = 1.f;
-      if (t < count) {
-        const int pair = list[t];
-        const float most = moe_amax<true, F16_>(moe_source<true>(a, pair), q0 * St::COLS + 4 * lane, min(q1 * St::COLS, a.I), 256);
-        scale[t] = moe_row_scale(wave_max_f32(most));
+      for (int t = 0; t < TOK; ++t) x[t].load(moe_source<true>(a, pair[t]), a.I, q, lane, there && t < count);
+    };
+    st.load(q0, w0);
+    load_x(q0, true);
+    const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+      float back[TOK];
+#pragma unroll
+      for (int t = 0; t < TOK; ++t) back[t] = x[t].put(mine, ROWS, 2 * t, lane) * weight[t];
+      const bool more = q + 1 < q1;
+      st.load(more ? q + 1 : quads, ahead);
+      load_x(q + 1, more);
+      __builtin_amdgcn_wave_barrier();
+      float acc[1][NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[0][i] = 0.f;
+      st.template compute<NI>(d, xa, stride, ng - q * St::QG, acc);
+      // x row 4 i + h holds part h % 2 of the list's token t = 2 i + h / 2, whose sums go to row 2 token + part
+#pragma unroll
+      for (int t = 0; t < TOK; ++t) {
+        const int tok = pair[t] / a.top_k;
+        float v = acc[0][t >> 1];
+        if constexpr (TOK > 1) v = __shfl(v, 16 * ((2 * t + (h & 1)) & 3) + c);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (t < count && 4 * i + h == 2 * tok + (h & 1)) total[i] = fmaf(v * 0x1p24f, back[t], total[i]);
       }
-    }
-    for (int q = q0; q < q1; q += s.chunk) {
-      const int end = min(q + s.chunk, q1), units = (end - q) * 4 * St::S::NJ * 4;
       __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int t = 0; t < MOE_FEW; ++t)
-        if (t < count)
-          moe_stage<BITS, G, F16_, true>(moe_source<true>(a, list[t]), scale[t], q * St::COLS, a.I, lane, 64, units, mine, s.rows,
-                                         2 * t);
-      __builtin_amdgcn_wave_barrier();
-      if (q > q0) st.load(q, w);
-      moe_quads<NI>(st, q, end, w, xa, 4 * s.rows * 16, acc);
-    }
-    // x row v = 4 i + h holds part h % 2 of the list's token 2 i + h / 2; that token's sums go to row 2 token + part
-#pragma unroll
-    for (int t = 0; t < MOE_FEW; ++t) {
-      if (t >= count) break;
-      const int pair = list[t], m = pair / a.top_k;
-      const float f = a.weights[pair] * (0x1p24f / scale[t]);
-      // lane row h of register i is 4 i + h: take row 2 t + part to 2 m + part
-      const float v = __shfl(acc[0][t >> 1], 16 * ((2 * t + (h & 1)) & 3) + c);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (4 * i + h == 2 * m + (h & 1)) total[i] = fmaf(f, v, total[i]);
+    };
+    for (int q = q0; q < q1; q += 2) {
+      step(q, w0, w1);
+      if (q + 1 < q1) step(q + 1, w1, w0);
     }
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) red[(wave * NI + i) * 64 + lane] = total[i];
   __syncthreads();
-  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
   if (m >= a.M) return;
   float v = 0.f;
 #pragma unroll
@@ -689,12 +872,9 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
     const float* p = red + (q * NI + (m >> 1)) * 64 + 32 * (m & 1) + n;  // rows 2 m and 2 m + 1
     v += p[0] + p[16];
   }
-  const long at = (long)m * a.N + 16 * blockIdx.x + n;
-  const float sum = a.sums[m];
-  float y = a.resid ? load_as_f32(a.resid, at, a.act_dt) : 0.f;
-  if (a.choices[m]) y = fmaf(a.scale / sum, v, y);
+  float y = chosen ? fmaf(a.scale / sum, v, resid) : resid;
   if (sum != sum) y = __builtin_nanf("");
-  ((uint16_t*)a.y)[at] = f32_to_act_bits(y, F16_);
+  ((uint16_t*)a.y)[at_y] = f32_to_act_bits(y, F16_);
 }
 
 template <int BITS, int G, bool F16_>
@@ -703,39 +883,44 @@ hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   MoeShape s{};
   const bool down = step == MOE_DOWN || step == MOE_FEW_DOWN;
   s.K = down ? a.I : a.N;
-  const int quads = (s.K + St::COLS - 1) / St::COLS;
-  if (step == MOE_FEW_DOWN) {
-    s.rows = 2 * a.M;
-    s.chunk = a.M <= 2 ? 2 : 1;
-    s.x_bytes = s.chunk * St::COLS * 2 * s.rows;
-    hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_>), dim3((unsigned)(a.N / 16)), dim3(64 * MOE_FEW_WAVES),
-                       MOE_FEW_WAVES * s.x_bytes, st, a, s);
+  const int quads = (s.K + St::COLS - 1) / St::COLS, tiles = down ? a.N / 32 : a.I / 16;
+  constexpr int QUAD = St::COLS * 2;  // bytes of a quad of a row of x
+  if (step == MOE_FEW_UP) {
+    s.x_bytes = QUAD * (a.M == 1 ? 1 : MOE_FEW);
+    const dim3 grid((unsigned)tiles, (unsigned)(a.M * a.top_k));
+    const int lds = 4 * s.x_bytes + 4 * a.M * a.E;
+    if (a.M == 1) hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, 1>), grid, dim3(256), lds, st, a, s);
+    else hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, MOE_FEW>), grid, dim3(256), lds, st, a, s);
     return hipGetLastError();
   }
-  const int slots = (int)std::min<int64_t>((int64_t)a.M * a.top_k, a.E), tiles = down ? a.N / 32 : a.I / 16;
+  if (step == MOE_FEW_DOWN) {
+    s.x_bytes = QUAD * 2 * (a.M == 1 ? 1 : MOE_FEW);
+    const dim3 grid((unsigned)(a.N / 16)), block(64 * MOE_FEW_WAVES);
+    const int lds = MOE_FEW_WAVES * s.x_bytes;
+    if (a.M == 1) hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, 1>), grid, block, lds, st, a, s);
+    else hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, MOE_FEW>), grid, block, lds, st, a, s);
+    return hipGetLastError();
+  }
+  s.pairs = (int64_t)a.M * a.top_k < a.E;
+  const int slots = s.pairs ? a.M * a.top_k : a.E;
   // x rows a pass: eight where an expert has four tokens or fewer on average (a second pass reads the weights again, from the caches)
   const int most = (int64_t)a.M * a.top_k <= 4 * (int64_t)a.E ? 8 : 16;
   s.rows = down ? std::min(2 * a.M, 16) : std::min(a.M, most);
-  if (step == MOE_FEW_UP) s.rows = a.M;
-  const int row_bytes = quads * St::COLS * 2;  // of x in LDS
-  const bool whole = step != MOE_FEW_UP && s.rows * row_bytes <= 65536 && (int64_t)tiles * slots >= 2048;
-  if (whole) {
+  if (s.rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 2048) {
     // 512 workgroups or more
     s.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)tiles * slots / 2048));
+    s.x_bytes = s.rows * quads * QUAD;
     const dim3 grid((unsigned)((tiles + 4 * s.tiles - 1) / (4 * s.tiles)), (unsigned)slots);
-    if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 1>), grid, dim3(256), s.rows * row_bytes, st, a, s);
-    else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 1>), grid, dim3(256), s.rows * row_bytes, st, a, s);
+    const int lds = s.x_bytes + 64 * quads;
+    if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 1>), grid, dim3(256), lds, st, a, s);
+    else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 1>), grid, dim3(256), lds, st, a, s);
     return hipGetLastError();
   }
-  // a wave's part of x: as many quads as fit 12 KiB, one at least
-  const int quad_bytes = St::COLS * 2 * s.rows;
-  s.chunk = std::max(1, std::min((quads + 3) / 4, 12288 / quad_bytes));
-  s.x_bytes = s.chunk * quad_bytes;
-  const dim3 grid((unsigned)tiles, (unsigned)(step == MOE_FEW_UP ? a.M * a.top_k : slots));
-  const int lds = std::max(4 * s.x_bytes, step == MOE_FEW_UP ? a.M * a.E * 4 : 0);
-  if (step == MOE_FEW_UP) hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_>), grid, dim3(256), lds, st, a, s);
-  else if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 4>), grid, dim3(256), lds, st, a, s);
-  else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 4>), grid, dim3(256), lds, st, a, s);
+  s.rows = std::min(s.rows, 16384 / QUAD);  // a quad of every wave's x in 64 KiB
+  s.x_bytes = s.rows * QUAD;
+  const dim3 grid((unsigned)tiles, (unsigned)slots);
+  if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 4>), grid, dim3(256), 4 * s.x_bytes, st, a, s);
+  else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 4>), grid, dim3(256), 4 * s.x_bytes, st, a, s);
   return hipGetLastError();
 }
 

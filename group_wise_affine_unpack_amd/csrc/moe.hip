@@ -14,111 +14,68 @@ hipError_t launch_moe_product(const MoeArgs& a, MoeStep step, hipStream_t s) {
   return a.bits == 2 ? launch_moe_b2(a, step, s) : a.bits == 4 ? launch_moe_b4(a, step, s) : launch_moe_b8(a, step, s);
 }
 
-// One workgroup.  A wave takes a token: its largest logit top_k times (the
-// lowest index first among equal ones), the r-th choice in lane r.  Then the
-// chosen experts get slots in the order of their index, and their tokens, which
-// a bit a token marks, places in the order of theirs.  A few microseconds of
-// dependent steps; in every workgroup of the products (as for a few tokens) it
-// cost the batch of 16 more than this launch does.
-constexpr int ROUTE_WAVES = 16;
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(MoeArgs a, int slots) {
-  extern __shared__ uint32_t lds[];
-  uint32_t* marks = lds;                                         // [E][8] tokens that chose the expert
-  uint16_t* slot_of = (uint16_t*)(lds + 8 * a.E);                // [E]
-  uint16_t* choice = slot_of + ((a.E + 1) & ~1);                 // [pairs] expert, 0xffff for none
-  __shared__ uint32_t part[ROUTE_WAVES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.M * a.top_k;
-  for (int i = threadIdx.x; i < 8 * a.E; i += 64 * ROUTE_WAVES) marks[i] = 0;
-  __syncthreads();
-  for (int m = wave; m < a.M; m += ROUTE_WAVES) {
-    float z[16];
-    bool nan = false;
-    float all = 0.f, top = 0.f;
+// A wave takes a token: its largest logit top_k times (the lowest index first
+// among equal ones), the r-th choice in lane r.  A chain of dependent steps,
+// about 200 cycles a choice; a launch of its own, since done in every
+// workgroup of the products it cost a batch of 16 more than the launch does.
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (m >= a.M) return;
+  float z[16];
+  bool nan = false;
+  float all = 0.f, top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      z[i] = -__builtin_inff();
-      if (64 * i + lane < a.E) {
-        const float v = load_as_f32(a.logits, (long)m * a.E + 64 * i + lane, a.logit_dt);
-        nan |= v != v;
-        z[i] = v == v ? v : -__builtin_inff();
+  for (int i = 0; i < 16; ++i) {
+    z[i] = -__builtin_inff();
+    if (64 * i + lane < a.E) {
+      const float v = load_as_f32(a.logits, (long)m * a.E + 64 * i + lane, a.logit_dt);
+      nan |= v != v;
+      z[i] = v == v ? v : -__builtin_inff();
+    }
+  }
+  nan = __ballot(nan) != 0;
+  int mine = -1, chosen = 0;
+  float weight = 0.f;
+  for (int r = 0; r < a.top_k; ++r) {
+    float most = z[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i)
+      if (64 * i < a.E) most = fmaxf(most, z[i]);
+    most = wave_max_f32(most);
+    if (r == 0) {
+      top = most;
+      if (!a.renormalize) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (64 * i < a.E) all += z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.f;
       }
     }
-    nan = __ballot(nan) != 0;
-    int mine = -1, chosen = 0;
-    float weight = 0.f;
-    for (int r = 0; r < a.top_k; ++r) {
-      float most = z[0];
+    if (!(most > -__builtin_inff())) break;
+    int e = -1;
 #pragma unroll
-      for (int i = 1; i < 16; ++i)
-        if (64 * i < a.E) most = fmaxf(most, z[i]);
-      most = wave_max_f32(most);
-      if (r == 0) {
-        top = most;
-        if (!a.renormalize) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (64 * i < a.E) all += z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.f;
+    for (int i = 0; i < 16; ++i)
+      if (64 * i < a.E && e < 0) {
+        const uint64_t at = __ballot(z[i] == most);
+        if (at) {
+          const int l = __builtin_ctzll(at);
+          e = 64 * i + l;
+          if (lane == l) z[i] = -__builtin_inff();
         }
       }
-      if (!(most > -__builtin_inff())) break;
-      int e = -1;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (64 * i < a.E && e < 0) {
-          const uint64_t at = __ballot(z[i] == most);
-          if (at) {
-            const int l = __builtin_ctzll(at);
-            e = 64 * i + l;
-            if (lane == l) z[i] = -__builtin_inff();
-          }
-        }
-      if (lane == r) {
-        mine = e;
-        weight = expf(most - top);
-      }
-      ++chosen;
+    if (lane == r) {
+      mine = e;
+      weight = expf(most - top);
     }
-    const float sum = wave_sum(a.renormalize ? weight : all);
-    if (lane == 0) {
-      a.choices[m] = chosen;
-      a.sums[m] = nan ? __builtin_nanf("") : sum;
-    }
-    if (lane < a.top_k) {
-      choice[m * a.top_k + lane] = (uint16_t)mine;
-      a.weights[m * a.top_k + lane] = weight;
-      if (mine >= 0) atomicOr(&marks[8 * mine + (m >> 5)], 1u << (m & 31));
-    }
+    ++chosen;
   }
-  __syncthreads();
-  // slots: an exclusive count over the experts that are chosen
-  const int e = threadIdx.x;
-  uint32_t count = 0;
-  if (e < a.E) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) count += __builtin_popcount(marks[8 * e + i]);
+  const float sum = wave_sum(a.renormalize ? weight : all);
+  if (lane == 0) {
+    a.chosen[m] = chosen;
+    a.sums[m] = nan ? __builtin_nanf("") : sum;
   }
-  const uint64_t there = __ballot(count != 0);
-  if (lane == 0) part[wave] = __builtin_popcountll(there);
-  __syncthreads();
-  uint32_t slot = __builtin_popcountll(there & ((1ull << lane) - 1)), active = 0;
-#pragma unroll
-  for (int w = 0; w < ROUTE_WAVES; ++w) {
-    if (w < wave) slot += part[w];
-    active += part[w];
-  }
-  if (count) {
-    slot_of[e] = (uint16_t)slot;
-    a.counts[2 * slot] = (int)count;
-    a.counts[2 * slot + 1] = e;
-  }
-  for (int i = active + threadIdx.x; i < slots; i += 64 * ROUTE_WAVES) a.counts[2 * i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += 64 * ROUTE_WAVES) {
-    const int x = choice[i], m = i / a.top_k;
-    if (x == 0xffff) continue;
-    uint32_t at = __builtin_popcount(marks[8 * x + (m >> 5)] & ((1u << (m & 31)) - 1));
-    for (int w = 0; w < (m >> 5); ++w) at += __builtin_popcount(marks[8 * x + w]);
-    a.lists[(long)slot_of[x] * a.M + at] = i;
+  if (lane < a.top_k) {
+    a.choice[m * a.top_k + lane] = (uint16_t)mine;
+    a.weights[m * a.top_k + lane] = weight;
   }
 }
 
@@ -126,7 +83,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void moe_route_kernel(MoeArgs a, 
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
   const int m = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (n >= a.N) return;
-  const int choices = a.choices[m];
+  const int choices = a.chosen[m];
   const float sum = a.sums[m], f = a.scale / sum;
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   for (int r = 0; r < choices; ++r) {
@@ -155,8 +112,8 @@ hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
   const bool few = a.M <= 4 && a.M * a.E <= 1024;
   const size_t pairs = (size_t)a.M * a.top_k, slots = few || pairs < (size_t)a.E ? pairs : (size_t)a.E;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  const size_t sizes[7] = {up(8 * slots), up(4 * slots * a.M), up(4 * (size_t)a.M), up(4 * (size_t)a.M), up(4 * pairs),
-                           up(4 * pairs * a.I), few ? 0 : up(4 * pairs * a.N)};
+  const size_t sizes[8] = {up(8 * slots), up(4 * slots * a.M), up(4 * (size_t)a.M), up(4 * (size_t)a.M), up(4 * pairs),
+                           up(2 * pairs), up(4 * pairs * a.I), few ? 0 : up(4 * pairs * a.N)};
   size_t total = 0;
   for (size_t n : sizes) total += n;
   void* p = nullptr;
@@ -170,17 +127,17 @@ hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
   };
   a.counts = reinterpret_cast<int*>(take(0));
   a.lists = reinterpret_cast<int*>(take(1));
-  a.choices = reinterpret_cast<int*>(take(2));
+  a.chosen = reinterpret_cast<int*>(take(2));
   a.sums = reinterpret_cast<float*>(take(3));
   a.weights = reinterpret_cast<float*>(take(4));
-  a.h = reinterpret_cast<float*>(take(5));
-  a.part = reinterpret_cast<float*>(take(6));
+  a.choice = reinterpret_cast<uint16_t*>(take(5));
+  a.h = reinterpret_cast<float*>(take(6));
+  a.part = reinterpret_cast<float*>(take(7));
   if (few) {
     e = launch_moe_product(a, MOE_FEW_UP, s);
     return e == hipSuccess ? launch_moe_product(a, MOE_FEW_DOWN, s) : e;
   }
-  const size_t lds = 32 * (size_t)a.E + 2 * ((a.E + 1) & ~1) + 2 * pairs;
-  hipLaunchKernelGGL(moe_route_kernel, dim3(1), dim3(1024), (unsigned)lds, s, a, (int)slots);
+  hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
   e = hipGetLastError();
   if (e == hipSuccess) e = launch_moe_product(a, MOE_UP, s);
   if (e == hipSuccess) e = launch_moe_product(a, MOE_DOWN, s);
