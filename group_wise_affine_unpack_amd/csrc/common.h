@@ -332,6 +332,8 @@ struct MoeShape {
   int x_bytes;  // x in LDS, a wave's where it takes a part of the columns
 };
 enum MoeStep : int { MOE_UP, MOE_DOWN, MOE_FEW_UP, MOE_FEW_DOWN };
+// up to how many tokens take the two kernels of a few (2-bit codes: the x rows of four would not fit LDS)
+constexpr int moe_few(int bits) { return bits == 2 ? 2 : 4; }
 hipError_t launch_moe(MoeArgs& a, hipStream_t s);
 
 struct PagedAttnArgs {

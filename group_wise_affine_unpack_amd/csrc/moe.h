@@ -24,11 +24,9 @@
 //
 // Bound by memory: every chosen expert's weights once.  A wave streams 16 or
 // 32 rows of weights in quads of four spans, a span being 64 bytes of every
-// row: a quad's loads are issued before the one ahead of it is computed, and
+// row: two quads are under way or being computed, their loads issued
 // unconditionally (past the end they address nothing and return zeros), since
-// a load that may not have been issued makes the compiler wait for all.  The
-// parameters of a row's groups come with them, a lane taking scales and biases
-// of one of two tiles for its neighbour too.  A matrix instruction takes codes of one group only, so
+// a load that may not have been issued makes the compiler wait for all.  A matrix instruction takes codes of one group only, so
 // the 16-byte pieces that the four lanes of a row hold are exchanged (two or
 // four swaps per four words) where a span is longer than a group.  With many
 // rows a wave takes whole rows (KS = 1) and x, shared by the workgroup, fills
@@ -37,6 +35,8 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "common.h"
 
@@ -46,7 +46,7 @@ namespace {
 constexpr uint32_t MOE_OOB = 0x80000000u;  // past the end of any tile's rows
 
 __device__ __forceinline__ u32x4_t moe_ld128(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));  // streamed once
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
@@ -225,91 +225,91 @@ __device__ __forceinline__ const void* moe_source(const MoeArgs& a, int pair) {
 
 // ---- the stream of weights ------------------------------------------------
 
-// A wave's view of NT tiles of 16 rows of one expert's matrix.
+// A wave's view of NT tiles of 16 rows of one expert's matrix.  A lane loads
+// the 16 bytes of its row that it uses, 64 bytes of 16 rows an instruction; the
+// parameters come 32 groups of all rows at a time and go through LDS.  (With the loads alone, 16x2048, 8 of 64 experts:
+// 25 us; with 16 bytes of parameters a row and quad loaded beside them, 33.  A
+// load of 256 bytes of four rows, put in order through LDS, is 6% faster alone,
+// but its 8 KiB a wave cost the waves that hide the products: 44 against 37.)
 template <int BITS, int G, bool F16_, int NT>
 struct Stream {
   using S = Span<BITS, G>;
-  static constexpr int QG = 4 * S::CODES / G;  // groups of a quad: 2 to 32
-  static constexpr int MPG = G / 32;           // matrix instructions of a group
-  static constexpr int COLS = 4 * S::CODES;    // columns of a quad
+  static constexpr int QG = 4 * S::CODES / G;      // groups of a quad: 2 to 32
+  static constexpr int MPG = G / 32;               // matrix instructions of a group
+  static constexpr int COLS = 4 * S::CODES;        // columns of a quad
+  static constexpr int QPB = 32 / QG;              // quads of a block of 32 groups
+  static constexpr int BYTES = NT * 2048;          // of LDS a wave
   struct Quad {
     u32x4_t w[4][NT];
-    uint32_t s[QG / 2 + 1], b[QG / 2 + 1];  // two groups each, of tile h % NT; a word more for rows that start between words
+  };
+  struct Params {
+    u32x4_t v[2 * NT];   // scales of tile 0, biases, of tile 1
+    uint32_t over[2 * NT];  // the word behind, for rows that start between words
   };
   __amdgpu_buffer_rsrc_t rw[NT], rs, rb;
-  uint32_t woff, poff;
-  int row_bytes, h;
+  unsigned char* buf;
+  uint32_t apart;
+  int row_bytes, ng, lane;
 
   __device__ __forceinline__ void open(const uint32_t* packed, const uint16_t* scales, const uint16_t* biases, long row0,
-                                       long row1, int K, int lane) {
-    const int c = lane & 15, ng = K / G;
-    h = lane >> 4;
+                                       long row1, int K) {
     row_bytes = K * BITS / 8;
+    ng = K / G;
     rw[0] = make_rsrc((const char*)packed + row0 * row_bytes, 16u * (uint32_t)row_bytes);
     if constexpr (NT == 2) rw[1] = make_rsrc((const char*)packed + row1 * row_bytes, 16u * (uint32_t)row_bytes);
-    woff = (uint32_t)(c * row_bytes + h * 16);
-    const uint32_t apart = (uint32_t)(row1 - row0);
-    rs = make_rsrc(scales + row0 * ng, (apart + 16u) * (uint32_t)ng * 2u);
-    rb = make_rsrc(biases + row0 * ng, (apart + 16u) * (uint32_t)ng * 2u);
-    poff = ((NT == 2 && (h & 1) ? apart : 0u) + (uint32_t)c) * (uint32_t)ng * 2u;
+    apart = (uint32_t)(row1 - row0) * (uint32_t)ng * 2u;
+    rs = make_rsrc(scales + row0 * ng, apart + 32u * (uint32_t)ng);
+    rb = make_rsrc(biases + row0 * ng, apart + 32u * (uint32_t)ng);
   }
 
-  __device__ __forceinline__ void params(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t (&d)[QG / 2 + 1]) const {
-    constexpr int N = QG / 2;
-    if constexpr (N == 1) {
-      const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-      d[0] = v[0];
-      d[1] = v[1];
-    } else {
-      if constexpr (N == 2) {
-        const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-        d[0] = v[0];
-        d[1] = v[1];
-      } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-          const u32x4_t v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + 16 * i), 0, 0));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) d[4 * i + k] = v[k];
-        }
-      }
-      d[N] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)(off + 4 * N), 0, 0);
-    }
-  }
-
-  // quad q; past the rows' end (q of the row's number of quads, say): zeros, and nothing is read
+  // quad q; past the rows' end: zeros, and nothing is read
   __device__ __forceinline__ void load(int q, Quad& d) const {
+    const int at = q * 256 + (lane >> 4) * 16;
+    const uint32_t off = (uint32_t)((lane & 15) * row_bytes + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int at = (4 * q + i) * 64;
-      const uint32_t off = at + h * 16 < row_bytes ? woff + (uint32_t)at : MOE_OOB;
+      const uint32_t o = at + 64 * i < row_bytes ? off + 64 * i : MOE_OOB;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) d.w[i][t] = moe_ld128(rw[t], off);
+      for (int t = 0; t < NT; ++t) d.w[i][t] = moe_ld128(rw[t], o);
     }
-    const uint32_t off = q * 256 < row_bytes ? (poff + (uint32_t)(q * QG * 2)) & ~3u : MOE_OOB;
-    params(rs, off, d.s);
-    params(rb, off, d.b);
+  }
+  // block b of 32 groups, 64 bytes of every row, and into LDS as [plane][pair of groups][row], a word each
+  __device__ __forceinline__ void load(int b, Params& d) const {
+    const int at = b * 64 + (lane & 3) * 16;
+    const uint32_t off = at < 2 * ng ? (uint32_t)((lane >> 2) * ng * 2 + at) & ~3u : MOE_OOB;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      d.v[2 * t] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off + t * apart), 0, 0));
+      d.v[2 * t + 1] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(off + t * apart), 0, 0));
+      d.over[2 * t] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off + 16u + t * apart), 0, 0);
+      d.over[2 * t + 1] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rb, (int)(off + 16u + t * apart), 0, 0);
+    }
+  }
+  __device__ __forceinline__ void put(const Params& d) const {
+    const uint32_t odd = ((lane >> 2) & ng & 1) * 16u;  // bits that this lane's row starts behind the word
+    unsigned char* to = buf + (lane & 3) * 256 + (lane >> 2) * 4;
+#pragma unroll
+    for (int p = 0; p < 2 * NT; ++p)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint32_t*>(to + p * 1024 + k * 64) = __builtin_amdgcn_alignbit(k < 3 ? d.v[p][k < 3 ? k + 1 : 3] : d.over[p], d.v[p][k], odd);
   }
 
-  // acc += quad times x; xa: this lane's x of the quad's first fragment, `stride` bytes from one instruction to the next.
-  // left: groups of the row from the quad on.
-  template <int NI>
-  __device__ __forceinline__ void compute(Quad& d, const unsigned char* xa, int stride, int left, float (&acc)[NT][NI]) const {
+  // acc += quad q times x; xa: this lane's x of the quad's first fragment, in rows of ROWS
+  template <int NI, int ROWS>
+  __device__ __forceinline__ void compute(int q, Quad& d, const unsigned char* xa, float (&acc)[NT][NI]) const {
+    const int c = lane & 15, h = lane >> 4, left = ng - q * QG;  // groups from the quad on
     const uint32_t half = (h >> 1) ? 0x0c030c02u : 0x0c010c00u;
     const f16x8_t ones = __builtin_bit_cast(f16x8_t, u32x4_t{S::ones(0), S::ones(1), S::ones(2), S::ones(3)});
-    const uint32_t odd = (poff & 2u) * 8u;  // bits that this lane's parameters are off by
-    uint32_t ps[2], pb[2];
+    const unsigned char* prm = buf + c * 4 + (q % QPB) * QG * 32;
+    uint32_t pr[2 * NT];
 #pragma unroll
     for (int gi = 0; gi < QG; ++gi) {
       if ((gi & 1) == 0) {
         // (behind a row's end lies the next one's, which may not be finite; codes and x are zeros there)
         const uint32_t there = gi + 1 < left ? 0xffffffffu : gi < left ? 0xffffu : 0u;
-        ps[0] = ps[1] = __builtin_amdgcn_alignbit(d.s[gi / 2 + 1], d.s[gi / 2], odd) & there;
-        pb[0] = pb[1] = __builtin_amdgcn_alignbit(d.b[gi / 2 + 1], d.b[gi / 2], odd) & there;
-        if constexpr (NT == 2) {
-          swap16(ps[0], ps[1]);
-          swap16(pb[0], pb[1]);
-        }
+#pragma unroll
+        for (int p = 0; p < 2 * NT; ++p) pr[p] = *reinterpret_cast<const uint32_t*>(prm + p * 1024 + gi * 32) & there;
       }
       f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, dot[NT];
 #pragma unroll
@@ -321,7 +321,7 @@ struct Stream {
 #pragma unroll
           for (int t = 0; t < NT; ++t) S::exchange(d.w[sp][t]);
         }
-        const f16x8_t x = *reinterpret_cast<const f16x8_t*>(xa + mm * stride);
+        const f16x8_t x = *reinterpret_cast<const f16x8_t*>(xa + mm * 64 * ROWS);
         sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, ones, sum, 0, 0, 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -333,13 +333,13 @@ struct Stream {
           const uint32_t b = (gi & 1) ? v >> 16 : v & 0xffffu;
           return F16_ ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
         };
-        const float s = value(ps[t]), b = value(pb[t]);
+        const float s = value(pr[2 * t]), b = value(pr[2 * t + 1]);
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[t][i] = fmaf(s, dot[t][i], fmaf(b, sum[i], acc[t][i]));
       }
       if ((gi + 1) * MPG % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // (else x and codes of many groups are made at once)
     }
-    // (sums that only some lanes go on to use would be put off until then, and every group's kept in registers: 284, not 160)
+    // (sums that only some lanes go on to use would be put off until then, and every group's kept in registers)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -349,7 +349,7 @@ struct Stream {
 
 // ---- routing ----------------------------------------------------------------
 
-constexpr int MOE_FEW = 4;  // tokens whose experts each workgroup finds for itself
+constexpr int MOE_FEW = 4;  // tokens whose experts each workgroup finds for itself, at most
 
 struct MoeFew {
   int found, count;
@@ -453,6 +453,7 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
 // The slot's expert and its pairs in the order of the tokens, from every
 // pair's choice: list[0 .. count), at most M of them.  Slots are experts, or,
 // where there are fewer, pairs, the first of which takes its expert.
+template <int WAVES>
 __device__ __forceinline__ int moe_collect(const MoeArgs& a, const MoeShape& s, int slot, int* list, int* part, int* expert) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.M * a.top_k;
   const int e = s.pairs ? a.choice[slot] : slot;
@@ -460,7 +461,7 @@ __device__ __forceinline__ int moe_collect(const MoeArgs& a, const MoeShape& s, 
   if (e == 0xffff) return 0;
   int count = 0;
   bool earlier = false;
-  for (int base = 0; base < pairs; base += 256) {
+  for (int base = 0; base < pairs; base += 64 * WAVES) {
     const int i = base + (int)threadIdx.x;
     const bool mine = i < pairs && a.choice[i] == e;
     const uint64_t all = __ballot(mine);
@@ -469,7 +470,7 @@ __device__ __forceinline__ int moe_collect(const MoeArgs& a, const MoeShape& s, 
     __syncthreads();
     int at = count + __builtin_popcountll(all & ((1ull << lane) - 1));
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       if (w < wave) at += part[w];
       count += part[w];
     }
@@ -488,51 +489,100 @@ __device__ __forceinline__ int moe_collect(const MoeArgs& a, const MoeShape& s, 
 // 4 of the matrix instruction, so that the first four rows' results lie in one
 // register.
 template <int BITS, int G, bool F16_, bool DOWN>
-__device__ __forceinline__ void moe_open(const MoeArgs& a, int e, int tile, int K, int lane, Stream<BITS, G, F16_, 2>& st) {
+__device__ __forceinline__ void moe_open(const MoeArgs& a, int e, int tile, int K, Stream<BITS, G, F16_, 2>& st) {
   const long row0 = (long)e * (DOWN ? a.N : 2 * a.I) + (DOWN ? 32 * tile : 16 * tile);
   st.open(DOWN ? a.down_packed : a.gate_up_packed, DOWN ? a.down_scales : a.gate_up_scales,
-          DOWN ? a.down_biases : a.gate_up_biases, row0, row0 + (DOWN ? 16 : a.I), K, lane);
+          DOWN ? a.down_biases : a.gate_up_biases, row0, row0 + (DOWN ? 16 : a.I), K);
 }
 
 __device__ __forceinline__ int moe_vrow(int c, int vrows) { return min((c >> 2) + 4 * (c & 3), vrows - 1); }
 
-// whole rows a wave (KS = 1), x of all quads in LDS; back: [quad][16 tokens]
-template <int BITS, int G, bool F16_, bool DOWN, int NI>
-__device__ __forceinline__ void moe_rows(const MoeArgs& a, const MoeShape& s, int e, const int* list, int tokens,
-                                         const float* back, const unsigned char* xs, int tile0, int tile1) {
+// whole rows a wave (KS = 1): what is loaded next of the quads and of the blocks of parameters of tiles [tile0, tile1)
+template <int BITS, int G, bool F16_, bool DOWN>
+struct RowLoader {
   using St = Stream<BITS, G, F16_, 2>;
+  St st, sp;
+  typename St::Quad w;
+  typename St::Params pr;
+  int e, K, quads, blocks, tile1, lt, lq, pt, pb, left, pleft;
+
+  // the quad, and block of parameters, that a tile's sums begin with
+  __device__ __forceinline__ int first_block(int tile) const { return blocks > 1 ? tile % blocks : 0; }
+  __device__ __forceinline__ int first_quad(int tile) const { return blocks > 1 ? tile % blocks * St::QPB : tile % quads; }
+
+  __device__ __forceinline__ void begin(const MoeArgs& a, const MoeShape& s, int expert, unsigned char* buf, int tile0, int end) {
+    e = expert;
+    K = s.K;
+    quads = (K + St::COLS - 1) / St::COLS;
+    blocks = (quads + St::QPB - 1) / St::QPB;
+    tile1 = end;
+    lt = pt = tile0;
+    lq = first_quad(tile0);
+    pb = first_block(tile0);
+    left = quads;
+    pleft = blocks;
+    st.buf = sp.buf = buf;
+    st.lane = sp.lane = threadIdx.x & 63;
+    if (tile0 >= tile1) return;
+    moe_open<BITS, G, F16_, DOWN>(a, e, tile0, K, st);
+    moe_open<BITS, G, F16_, DOWN>(a, e, tile0, K, sp);
+    next_params(a);
+    next(a);
+  }
+  __device__ __forceinline__ void next(const MoeArgs& a) {
+    st.load(lt < tile1 ? lq : quads, w);
+    if (++lq == quads) lq = 0;
+    if (--left == 0) {
+      left = quads;
+      lq = first_quad(++lt);
+      if (lt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, lt, K, st);
+    }
+  }
+  __device__ __forceinline__ void next_params(const MoeArgs& a) {
+    sp.load(pt < tile1 ? pb : blocks, pr);
+    if (++pb == blocks) pb = 0;
+    if (--pleft == 0) {
+      pleft = blocks;
+      pb = first_block(++pt);
+      if (pt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, pt, K, sp);
+    }
+  }
+};
+
+// the sums of those tiles, x of all quads in LDS; back: [quad][16 tokens]
+template <int BITS, int G, bool F16_, bool DOWN, int ROWS>
+__device__ __forceinline__ void moe_rows(const MoeArgs& a, const int* list, int tokens, const float* back, const unsigned char* xs,
+                                         RowLoader<BITS, G, F16_, DOWN>& ld, int tile0, int tile1) {
+  using St = Stream<BITS, G, F16_, 2>;
+  constexpr int NI = ROWS / 4;
   if (tile0 >= tile1) return;
   const int lane = threadIdx.x & 63;
-  const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens;
-  const int quads = (s.K + St::COLS - 1) / St::COLS, ng = s.K / G, stride = 4 * s.rows * 16;
-  const unsigned char* x0 = xs + (h * s.rows + moe_vrow(c, vrows)) * 16;
-  St st;
-  typename St::Quad w0, w1;
-  int lt = tile0, lq = 0;  // what is loaded next
-  moe_open<BITS, G, F16_, DOWN>(a, e, tile0, s.K, lane, st);
-  const auto next = [&](typename St::Quad& d) __attribute__((always_inline)) {
-    st.load(lt < tile1 ? lq : quads, d);
-    if (++lq == quads) {
-      lq = 0;
-      if (++lt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, lt, s.K, lane, st);
-    }
-  };
-  int tile = tile0, q = 0;  // what is computed next
+  const int c = lane & 15, h = lane >> 4, quads = ld.quads;
+  const unsigned char* x0 = xs + (h * ROWS + moe_vrow(c, DOWN ? 2 * tokens : tokens)) * 16;
+  int tile = tile0, q = ld.first_quad(tile0), left = quads;  // what is computed next
   float total[2][NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) total[0][i] = total[1][i] = 0.f;
-  const auto step = [&](typename St::Quad& d) __attribute__((always_inline)) {
+  const auto step = [&]() __attribute__((always_inline)) {
+    if (q % St::QPB == 0 || left == quads) {
+      ld.sp.put(ld.pr);
+      ld.next_params(a);
+    }
+    __builtin_amdgcn_wave_barrier();  // (LDS of this wave alone, whose operations stay in order)
     float acc[2][NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
-    st.template compute<NI>(d, x0 + (size_t)q * St::S::NJ * 4 * stride, stride, ng - q * St::QG, acc);
+    ld.st.template compute<NI, ROWS>(q, ld.w, x0 + q * (St::S::NJ * 256 * ROWS), acc);
+    __builtin_amdgcn_wave_barrier();
+    ld.next(a);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const float f = back[16 * q + (DOWN ? (4 * i + h) / 2 : 4 * i + h)];
       total[0][i] = fmaf(acc[0][i] * 0x1p24f, f, total[0][i]);
       total[1][i] = fmaf(acc[1][i] * 0x1p24f, f, total[1][i]);
     }
-    if (++q < quads) return;
+    if (++q == quads) q = 0;
+    if (--left) return;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int v = 4 * i + h;
@@ -548,68 +598,73 @@ __device__ __forceinline__ void moe_rows(const MoeArgs& a, const MoeShape& s, in
       }
       total[0][i] = total[1][i] = 0.f;
     }
-    q = 0;
-    ++tile;
+    q = ld.first_quad(++tile);
+    left = quads;
   };
-  next(w0);
   const int all = (tile1 - tile0) * quads;
-  for (int i = 0; i < all; i += 2) {
-    next(w1);
-    step(w0);
-    next(w0);
-    if (i + 1 < all) step(w1);
-  }
+  for (int i = 0; i < all; ++i) step();
 }
 
 // a part of the columns a wave (KS = 4), each with its own x: this wave's sums of its quads of tile `tile`
-template <int BITS, int G, bool F16_, bool DOWN, int NI>
+template <int BITS, int G, bool F16_, bool DOWN, int ROWS>
 __device__ __forceinline__ void moe_part(const MoeArgs& a, const MoeShape& s, int e, const int* list, int tokens,
-                                         unsigned char* mine, float* back, int tile, float (&total)[2][NI]) {
+                                         unsigned char* mine, unsigned char* buf, float* back, int tile, float (&total)[2][ROWS / 4]) {
   using St = Stream<BITS, G, F16_, 2>;
   using Xq = XQuad<BITS, G, F16_, DOWN>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens, stride = 4 * s.rows * 16;
-  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4, ng = s.K / G;
+  const int c = lane & 15, h = lane >> 4, vrows = DOWN ? 2 * tokens : tokens;
+  constexpr int NI = ROWS / 4;
+  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4;
   const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
-  const unsigned char* xa = mine + (h * s.rows + moe_vrow(c, vrows)) * 16;
+  const unsigned char* xa = mine + (h * ROWS + moe_vrow(c, vrows)) * 16;
 #pragma unroll
   for (int i = 0; i < NI; ++i) total[0][i] = total[1][i] = 0.f;
   St st;
+  st.buf = buf;
+  st.lane = lane;
   typename St::Quad w0, w1;
+  typename St::Params pr;
   Xq x0, x1;  // the next quad's x of two tokens
-  moe_open<BITS, G, F16_, DOWN>(a, e, tile, s.K, lane, st);
+  moe_open<BITS, G, F16_, DOWN>(a, e, tile, s.K, st);
+  st.load(q0 < q1 ? q0 / St::QPB : quads, pr);
   const void* first = moe_source<DOWN>(a, list[0]);
   const void* second = moe_source<DOWN>(a, list[min(1, tokens - 1)]);
   x0.load(first, s.K, q0, lane, q0 < q1);
   x1.load(second, s.K, q0, lane, q0 < q1 && tokens > 1);
   st.load(q0 < q1 ? q0 : quads, w0);
-  const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+  st.load(q0 + 1 < q1 ? q0 + 1 : quads, w1);
+  const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
     // (LDS of this wave alone, whose operations stay in order)
-    float f = x0.put(mine, s.rows, 0, lane);
+    float f = x0.put(mine, ROWS, 0, lane);
     if (lane == 0) back[0] = f;
     if (tokens > 1) {
-      f = x1.put(mine, s.rows, DOWN ? 2 : 1, lane);
+      f = x1.put(mine, ROWS, DOWN ? 2 : 1, lane);
       if (lane == 0) back[1] = f;
     }
     for (int t = 2; t < tokens; t += 2) {
       x0.load(moe_source<DOWN>(a, list[t]), s.K, q, lane, true);
       x1.load(moe_source<DOWN>(a, list[min(t + 1, tokens - 1)]), s.K, q, lane, true);
-      f = x0.put(mine, s.rows, DOWN ? 2 * t : t, lane);
+      f = x0.put(mine, ROWS, DOWN ? 2 * t : t, lane);
       if (lane == 0) back[t] = f;
       if (t + 1 < tokens) {
-        f = x1.put(mine, s.rows, DOWN ? 2 * t + 2 : t + 1, lane);
+        f = x1.put(mine, ROWS, DOWN ? 2 * t + 2 : t + 1, lane);
         if (lane == 0) back[t + 1] = f;
       }
     }
     const bool more = q + 1 < q1;
-    st.load(more ? q + 1 : quads, ahead);
+    if (q == q0 || q % St::QPB == 0) {
+      st.put(pr);
+      const int next = (q / St::QPB + 1) * St::QPB;
+      st.load(next < q1 ? next / St::QPB : quads, pr);
+    }
     x0.load(first, s.K, q + 1, lane, more);
     x1.load(second, s.K, q + 1, lane, more && tokens > 1);
     __builtin_amdgcn_wave_barrier();
     float acc[2][NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
-    st.template compute<NI>(d, xa, stride, ng - q * St::QG, acc);
+    st.template compute<NI, ROWS>(q, d, xa, acc);
+    st.load(q + 2 < q1 ? q + 2 : quads, d);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int v = 4 * i + h;
@@ -620,8 +675,8 @@ __device__ __forceinline__ void moe_part(const MoeArgs& a, const MoeShape& s, in
     __builtin_amdgcn_wave_barrier();
   };
   for (int q = q0; q < q1; q += 2) {
-    step(q, w0, w1);
-    if (q + 1 < q1) step(q + 1, w1, w0);
+    step(q, w0);
+    if (q + 1 < q1) step(q + 1, w1);
   }
 }
 
@@ -655,67 +710,65 @@ __device__ __forceinline__ void moe_finish(const MoeArgs& a, const int* out, int
   __syncthreads();
 }
 
-template <int BITS, int G, bool F16_, bool DOWN, int KS>
-__global__ __launch_bounds__(256) void moe_kernel(MoeArgs a, MoeShape s) {
+template <int BITS, int G, bool F16_, bool DOWN, int KS, int ROWS>
+__global__ __launch_bounds__(256, KS == 1 ? 4 : 3) void moe_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 2>;
   using Xq = XQuad<BITS, G, F16_, DOWN>;
+  constexpr int WAVES = 4, NI = ROWS / 4;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int list[256];
-  __shared__ int part[4];
+  __shared__ int part[WAVES];
   __shared__ float own_back[KS == 4 ? 64 : 1];
-  __shared__ float red[KS == 4 ? 2048 : 1];
+  __shared__ float red[KS == 4 ? 512 * NI : 1];
   const int slot = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int count, e;
   if constexpr (DOWN) {
     count = a.counts[2 * slot];
     e = a.counts[2 * slot + 1];
-    for (int i = threadIdx.x; i < count; i += 256) list[i] = a.lists[(long)slot * a.M + i];
+    for (int i = threadIdx.x; i < count; i += 64 * WAVES) list[i] = a.lists[(long)slot * a.M + i];
     __syncthreads();
   } else {
-    count = moe_collect(a, s, slot, list, part, &e);
+    count = moe_collect<WAVES>(a, s, slot, list, part, &e);
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) {
         a.counts[2 * slot] = count;
         a.counts[2 * slot + 1] = e;
       }
-      for (int i = threadIdx.x; i < count; i += 256) a.lists[(long)slot * a.M + i] = list[i];
+      for (int i = threadIdx.x; i < count; i += 64 * WAVES) a.lists[(long)slot * a.M + i] = list[i];
     }
   }
   e = __builtin_amdgcn_readfirstlane(e);
   count = __builtin_amdgcn_readfirstlane(count);
-  const int per_pass = DOWN ? s.rows / 2 : s.rows;
+  constexpr int per_pass = DOWN ? ROWS / 2 : ROWS;
   for (int first = 0; first < count; first += per_pass) {
     const int tokens = min(per_pass, count - first);
     const int* mine = list + first;
-    const bool small = (DOWN ? 2 * tokens : tokens) <= 4;
     if constexpr (KS == 4) {
-      const auto run = [&](auto n) __attribute__((always_inline)) {
-        float total[2][n.value];
-        moe_part<BITS, G, F16_, DOWN, n.value>(a, s, e, mine, tokens, lds + wave * s.x_bytes, own_back + 16 * wave, blockIdx.x, total);
-        moe_finish<DOWN, n.value>(a, mine, tokens, red, blockIdx.x, total);
-      };
-      if (small) run(std::integral_constant<int, 1>{});
-      else run(std::integral_constant<int, 4>{});
+      float total[2][NI];
+      moe_part<BITS, G, F16_, DOWN, ROWS>(a, s, e, mine, tokens, lds + wave * s.x_bytes, lds + 4 * s.x_bytes + wave * St::BYTES,
+                                          own_back + 16 * wave, blockIdx.x, total);
+      moe_finish<DOWN, NI>(a, mine, tokens, red, blockIdx.x, total);
     } else {
+      const int tile0 = (blockIdx.x * WAVES + wave) * s.tiles, tile1 = min(tile0 + s.tiles, DOWN ? a.N / 32 : a.I / 16);
+      RowLoader<BITS, G, F16_, DOWN> ld;
+      ld.begin(a, s, e, lds + s.x_bytes + wave * St::BYTES, tile0, tile1);
       // x: quads of tokens, dealt to the waves, two in flight
-      const int quads = (s.K + St::COLS - 1) / St::COLS, jobs = tokens * quads;
-      float* back = reinterpret_cast<float*>(lds + s.x_bytes);
-      for (int j = wave; j < jobs; j += 8) {
-        const int t0 = j / quads, q0 = j - t0 * quads, k = min(j + 4, jobs - 1), t1 = k / quads, q1 = k - t1 * quads;
+      const int quads = ld.quads, jobs = tokens * quads;
+      float* back = reinterpret_cast<float*>(lds + s.x_bytes + WAVES * St::BYTES);
+      for (int j = wave; j < jobs; j += 2 * WAVES) {
+        const int t0 = j / quads, q0 = j - t0 * quads, k = min(j + WAVES, jobs - 1), t1 = k / quads, q1 = k - t1 * quads;
         Xq x0, x1;
         x0.load(moe_source<DOWN>(a, mine[t0]), s.K, q0, lane, true);
         x1.load(moe_source<DOWN>(a, mine[t1]), s.K, q1, lane, true);
-        float f = x0.put(lds + (size_t)q0 * Xq::UNITS * s.rows * 16, s.rows, DOWN ? 2 * t0 : t0, lane);
+        float f = x0.put(lds + q0 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t0 : t0, lane);
         if (lane == 0) back[16 * q0 + t0] = f;
-        if (j + 4 < jobs) {
-          f = x1.put(lds + (size_t)q1 * Xq::UNITS * s.rows * 16, s.rows, DOWN ? 2 * t1 : t1, lane);
+        if (j + WAVES < jobs) {
+          f = x1.put(lds + q1 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t1 : t1, lane);
           if (lane == 0) back[16 * q1 + t1] = f;
         }
       }
       __syncthreads();
-      const int tile0 = (blockIdx.x * 4 + wave) * s.tiles, tile1 = min(tile0 + s.tiles, DOWN ? a.N / 32 : a.I / 16);
-      if (small) moe_rows<BITS, G, F16_, DOWN, 1>(a, s, e, mine, tokens, back, lds, tile0, tile1);
-      else moe_rows<BITS, G, F16_, DOWN, 4>(a, s, e, mine, tokens, back, lds, tile0, tile1);
+      moe_rows<BITS, G, F16_, DOWN, ROWS>(a, mine, tokens, back, lds, ld, tile0, tile1);
       __syncthreads();
     }
   }
@@ -732,10 +785,10 @@ __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) 
   __shared__ float red[512];
   __shared__ MoeFew l;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4, stride = 4 * TOK * 16;
-  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4, ng = s.K / G;
+  const int c = lane & 15, h = lane >> 4;
+  const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4;
   const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
-  float* z = reinterpret_cast<float*>(lds + 4 * s.x_bytes);
+  float* z = reinterpret_cast<float*>(lds + 4 * (s.x_bytes + St::BYTES));
   bool nan = false;
   if (threadIdx.x == 0) l.found = -1;
   const int m0 = blockIdx.y / a.top_k;
@@ -758,29 +811,38 @@ __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) 
   const unsigned char* xa = mine + (h * TOK + moe_vrow(c, TOK)) * 16;
   float total[2][1] = {{0.f}, {0.f}};
   St st;
+  st.buf = lds + 4 * s.x_bytes + wave * St::BYTES;
+  st.lane = lane;
   typename St::Quad w0, w1;
-  moe_open<BITS, G, F16_, false>(a, e, blockIdx.x, s.K, lane, st);
+  typename St::Params pr;
+  moe_open<BITS, G, F16_, false>(a, e, blockIdx.x, s.K, st);
+  st.load(q0 < q1 ? q0 / St::QPB : quads, pr);
   st.load(q0 < q1 ? q0 : quads, w0);
-  const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+  st.load(q0 + 1 < q1 ? q0 + 1 : quads, w1);
+  const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < TOK; ++t) {
       const float f = x[t].put(mine, TOK, t, lane);
       if (lane == 0) own_back[wave][t] = f;
     }
-    const bool more = q + 1 < q1;
-    st.load(more ? q + 1 : quads, ahead);
-    load_x(q + 1, more);
+    if (q == q0 || q % St::QPB == 0) {
+      st.put(pr);
+      const int next = (q / St::QPB + 1) * St::QPB;
+      st.load(next < q1 ? next / St::QPB : quads, pr);
+    }
+    load_x(q + 1, q + 1 < q1);
     __builtin_amdgcn_wave_barrier();
     float acc[2][1] = {{0.f}, {0.f}};
-    st.template compute<1>(d, xa, stride, ng - q * St::QG, acc);
+    st.template compute<1, TOK>(q, d, xa, acc);
+    st.load(q + 2 < q1 ? q + 2 : quads, d);
     const float k = own_back[wave][min(h, TOK - 1)];
     total[0][0] = fmaf(acc[0][0] * 0x1p24f, k, total[0][0]);
     total[1][0] = fmaf(acc[1][0] * 0x1p24f, k, total[1][0]);
     __builtin_amdgcn_wave_barrier();
   };
   for (int q = q0; q < q1; q += 2) {
-    step(q, w0, w1);
-    if (q + 1 < q1) step(q + 1, w1, w0);
+    step(q, w0);
+    if (q + 1 < q1) step(q + 1, w1);
   }
   moe_finish<false, 1>(a, l.pair, TOK, red, blockIdx.x, total);
 }
@@ -796,14 +858,14 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ float red[MOE_FEW_WAVES * NI * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4, stride = 4 * ROWS * 16;
+  const int c = lane & 15, h = lane >> 4;
   // the output that this thread finishes
   const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
   const long at_y = (long)min(m, a.M - 1) * a.N + 16 * blockIdx.x + n;
   const float resid = a.resid ? load_as_f32(a.resid, at_y, a.act_dt) : 0.f;
   const float sum = a.sums[min(m, a.M - 1)];
   const int chosen = a.chosen[min(m, a.M - 1)];
-  const int slots = a.M * a.top_k, quads = (a.I + St::COLS - 1) / St::COLS, ng = a.I / G;
+  const int slots = a.M * a.top_k, quads = (a.I + St::COLS - 1) / St::COLS;
   unsigned char* mine = lds + wave * s.x_bytes;
   const unsigned char* xa = mine + (h * ROWS + moe_vrow(c, ROWS)) * 16;
   float total[NI];
@@ -823,28 +885,37 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
       weight[t] = a.weights[pair[t]];
     }
     St st;
+    st.buf = lds + MOE_FEW_WAVES * s.x_bytes + wave * St::BYTES;
+    st.lane = lane;
     typename St::Quad w0, w1;
+    typename St::Params pr;
     Xq x[TOK];
     const long row0 = (long)e * a.N + 16 * blockIdx.x;
-    st.open(a.down_packed, a.down_scales, a.down_biases, row0, row0, a.I, lane);
+    st.open(a.down_packed, a.down_scales, a.down_biases, row0, row0, a.I);
     const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < TOK; ++t) x[t].load(moe_source<true>(a, pair[t]), a.I, q, lane, there && t < count);
     };
-    st.load(q0, w0);
+    st.load(q0 / St::QPB, pr);
     load_x(q0, true);
-    const auto step = [&](int q, typename St::Quad& d, typename St::Quad& ahead) __attribute__((always_inline)) {
+    st.load(q0, w0);
+    st.load(q0 + 1 < q1 ? q0 + 1 : quads, w1);
+      const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
       float back[TOK];
 #pragma unroll
       for (int t = 0; t < TOK; ++t) back[t] = x[t].put(mine, ROWS, 2 * t, lane) * weight[t];
-      const bool more = q + 1 < q1;
-      st.load(more ? q + 1 : quads, ahead);
-      load_x(q + 1, more);
+      if (q == q0 || q % St::QPB == 0) {
+        st.put(pr);
+        const int next = (q / St::QPB + 1) * St::QPB;
+        st.load(next < q1 ? next / St::QPB : quads, pr);
+      }
+      load_x(q + 1, q + 1 < q1);
       __builtin_amdgcn_wave_barrier();
       float acc[1][NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) acc[0][i] = 0.f;
-      st.template compute<NI>(d, xa, stride, ng - q * St::QG, acc);
+      st.template compute<NI, ROWS>(q, d, xa, acc);
+      st.load(q + 2 < q1 ? q + 2 : quads, d);
       // x row 4 i + h holds part h % 2 of the list's token t = 2 i + h / 2, whose sums go to row 2 token + part
 #pragma unroll
       for (int t = 0; t < TOK; ++t) {
@@ -858,8 +929,8 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
       __builtin_amdgcn_wave_barrier();
     };
     for (int q = q0; q < q1; q += 2) {
-      step(q, w0, w1);
-      if (q + 1 < q1) step(q + 1, w1, w0);
+      step(q, w0);
+      if (q + 1 < q1) step(q + 1, w1);
     }
   }
 #pragma unroll
@@ -885,42 +956,52 @@ hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   s.K = down ? a.I : a.N;
   const int quads = (s.K + St::COLS - 1) / St::COLS, tiles = down ? a.N / 32 : a.I / 16;
   constexpr int QUAD = St::COLS * 2;  // bytes of a quad of a row of x
+  constexpr int FEW = moe_few(BITS);
   if (step == MOE_FEW_UP) {
-    s.x_bytes = QUAD * (a.M == 1 ? 1 : MOE_FEW);
+    s.x_bytes = QUAD * (a.M == 1 ? 1 : FEW);
     const dim3 grid((unsigned)tiles, (unsigned)(a.M * a.top_k));
-    const int lds = 4 * s.x_bytes + 4 * a.M * a.E;
+    const int lds = 4 * (s.x_bytes + St::BYTES) + 4 * a.M * a.E;
     if (a.M == 1) hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, 1>), grid, dim3(256), lds, st, a, s);
-    else hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, MOE_FEW>), grid, dim3(256), lds, st, a, s);
+    else hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, FEW>), grid, dim3(256), lds, st, a, s);
     return hipGetLastError();
   }
   if (step == MOE_FEW_DOWN) {
-    s.x_bytes = QUAD * 2 * (a.M == 1 ? 1 : MOE_FEW);
+    s.x_bytes = QUAD * 2 * (a.M == 1 ? 1 : FEW);
     const dim3 grid((unsigned)(a.N / 16)), block(64 * MOE_FEW_WAVES);
-    const int lds = MOE_FEW_WAVES * s.x_bytes;
+    const int lds = MOE_FEW_WAVES * (s.x_bytes + Stream<BITS, G, F16_, 1>::BYTES);
     if (a.M == 1) hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, 1>), grid, block, lds, st, a, s);
-    else hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, MOE_FEW>), grid, block, lds, st, a, s);
+    else hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, FEW>), grid, block, lds, st, a, s);
     return hipGetLastError();
   }
   s.pairs = (int64_t)a.M * a.top_k < a.E;
   const int slots = s.pairs ? a.M * a.top_k : a.E;
-  // x rows a pass: eight where an expert has four tokens or fewer on average (a second pass reads the weights again, from the caches)
-  const int most = (int64_t)a.M * a.top_k <= 4 * (int64_t)a.E ? 8 : 16;
-  s.rows = down ? std::min(2 * a.M, 16) : std::min(a.M, most);
-  if (s.rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 2048) {
-    // 512 workgroups or more
-    s.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)tiles * slots / 2048));
-    s.x_bytes = s.rows * quads * QUAD;
-    const dim3 grid((unsigned)((tiles + 4 * s.tiles - 1) / (4 * s.tiles)), (unsigned)slots);
-    const int lds = s.x_bytes + 64 * quads;
-    if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 1>), grid, dim3(256), lds, st, a, s);
-    else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 1>), grid, dim3(256), lds, st, a, s);
-    return hipGetLastError();
+  // x rows a pass: a few times what an expert has on average, since a second pass reads the weights again (from the caches)
+  const int64_t pairs = (int64_t)a.M * a.top_k;
+  const int most = 2 * pairs <= 3 * (int64_t)a.E ? 4 : pairs <= 4 * (int64_t)a.E ? 8 : 16;
+  const int rows = down ? std::min(2 * most, 16) : most;
+  const bool whole = rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 2048;
+  // A tile a wave, or two where that leaves a second round of workgroups less than half full (three a CU; 16 tokens, 8 of
+  // 64 experts, 2048 x 1024: 1.2 rounds, 38 us with one and 33 with two; 64 tokens, 8 of 128, 2048 x 768: 2.0 rounds, 67
+  // and 76).  Experts in use: what independent tokens would reach.
+  const double used = s.pairs ? slots : a.E * (1.0 - std::pow(1.0 - (double)a.top_k / a.E, (double)a.M));
+  const double rounds = used * ((tiles + 3) / 4) / 768.0;
+  s.tiles = rounds > 1.0 && rounds < 1.5 ? 2 : 1;
+  s.x_bytes = whole ? rows * quads * QUAD : 8 * QUAD;
+  const dim3 grid((unsigned)(whole ? (tiles + 4 * s.tiles - 1) / (4 * s.tiles) : tiles), (unsigned)slots);
+  const int lds = whole ? s.x_bytes + 4 * St::BYTES + 64 * quads : 4 * (s.x_bytes + St::BYTES);
+#define QAFF_MOE(DOWN, KS, ROWS) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, DOWN, KS, ROWS>), grid, dim3(256), lds, st, a, s)
+  if (!whole) {
+    if (down) QAFF_MOE(true, 4, 8);
+    else QAFF_MOE(false, 4, 8);
+  } else if (down) {
+    if (rows == 8) QAFF_MOE(true, 1, 8);
+    else QAFF_MOE(true, 1, 16);
+  } else {
+    if (rows == 4) QAFF_MOE(false, 1, 4);
+    else if (rows == 8) QAFF_MOE(false, 1, 8);
+    else QAFF_MOE(false, 1, 16);
   }
-  s.rows = std::min(s.rows, 16384 / QUAD);  // a quad of every wave's x in 64 KiB
-  s.x_bytes = s.rows * QUAD;
-  const dim3 grid((unsigned)tiles, (unsigned)slots);
-  if (down) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, true, 4>), grid, dim3(256), 4 * s.x_bytes, st, a, s);
-  else hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, false, 4>), grid, dim3(256), 4 * s.x_bytes, st, a, s);
+#undef QAFF_MOE
   return hipGetLastError();
 }
 

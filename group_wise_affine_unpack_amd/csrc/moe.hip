@@ -18,14 +18,15 @@ hipError_t launch_moe_product(const MoeArgs& a, MoeStep step, hipStream_t s) {
 // among equal ones), the r-th choice in lane r.  A chain of dependent steps,
 // about 200 cycles a choice; a launch of its own, since done in every
 // workgroup of the products it cost a batch of 16 more than the launch does.
-__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
-  const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (m >= a.M) return;
-  float z[16];
+// NZ: logits a lane
+template <int NZ>
+__global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a) {
+  const int lane = threadIdx.x, m = blockIdx.x;
+  float z[NZ];
   bool nan = false;
   float all = 0.f, top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < NZ; ++i) {
     z[i] = -__builtin_inff();
     if (64 * i + lane < a.E) {
       const float v = load_as_f32(a.logits, (long)m * a.E + 64 * i + lane, a.logit_dt);
@@ -39,29 +40,26 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
   for (int r = 0; r < a.top_k; ++r) {
     float most = z[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i)
-      if (64 * i < a.E) most = fmaxf(most, z[i]);
+    for (int i = 1; i < NZ; ++i) most = fmaxf(most, z[i]);
     most = wave_max_f32(most);
     if (r == 0) {
       top = most;
       if (!a.renormalize) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (64 * i < a.E) all += z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.f;
+        for (int i = 0; i < NZ; ++i) all += z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.f;
       }
     }
     if (!(most > -__builtin_inff())) break;
     int e = -1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (64 * i < a.E && e < 0) {
-        const uint64_t at = __ballot(z[i] == most);
-        if (at) {
-          const int l = __builtin_ctzll(at);
-          e = 64 * i + l;
-          if (lane == l) z[i] = -__builtin_inff();
-        }
+    for (int i = 0; i < NZ; ++i) {
+      const uint64_t at = __ballot(z[i] == most);
+      if (e < 0 && at) {
+        const int l = __builtin_ctzll(at);
+        e = 64 * i + l;
+        if (lane == l) z[i] = -__builtin_inff();
       }
+    }
     if (lane == r) {
       mine = e;
       weight = expf(most - top);
@@ -80,25 +78,34 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
 }
 
 // y = resid + scale / sum * (sum over a token's choices, in their order, of weight * part), four columns a thread
-__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
-  const int m = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
+template <int BLOCK>
+__global__ __launch_bounds__(BLOCK) void moe_join_kernel(MoeArgs a) {
+  const int m = blockIdx.y, n = (blockIdx.x * BLOCK + threadIdx.x) * 4;
   if (n >= a.N) return;
-  const int choices = a.chosen[m];
-  const float sum = a.sums[m], f = a.scale / sum;
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < choices; ++r) {
-    const int pair = m * a.top_k + r;
-    const float w = a.weights[pair];
-    const f32x4_t p = *reinterpret_cast<const f32x4_t*>(a.part + (long)pair * a.N + n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fmaf(w, p[i], v[i]);
-  }
+  // (every load is under way before the first is used; pairs behind the last choice hold what an earlier call left)
+  const float* part = a.part + (long)m * a.top_k * a.N + n;
   const bool f16 = a.act_dt == F16;
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.resid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = load_as_f32(a.resid, (long)m * a.N + n + i, a.act_dt);
+  }
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  const int chosen = a.chosen[m];
+  const float sum = a.sums[m], f = a.scale / sum;
+#pragma unroll 8
+  for (int k = 0; k < a.top_k; ++k) {
+    const float w = a.weights[m * a.top_k + k];
+    const f32x4_t p = *reinterpret_cast<const f32x4_t*>(part + (long)k * a.N);
+    if (k < chosen) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(w, p[i], v[i]);
+    }
+  }
   uint32_t e[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float r = a.resid ? load_as_f32(a.resid, (long)m * a.N + n + i, a.act_dt) : 0.f;
-    float y = choices ? fmaf(f, v[i], r) : r;
+    float y = chosen ? fmaf(f, v[i], r[i]) : r[i];
     if (sum != sum) y = __builtin_nanf("");
     e[i] = f32_to_act_bits(y, f16);
   }
@@ -109,7 +116,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
 
 hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
   // a few tokens find their experts in the products themselves
-  const bool few = a.M <= 4 && a.M * a.E <= 1024;
+  const bool few = a.M <= moe_few(a.bits) && a.M * a.E <= 1024;
   const size_t pairs = (size_t)a.M * a.top_k, slots = few || pairs < (size_t)a.E ? pairs : (size_t)a.E;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t sizes[8] = {up(8 * slots), up(4 * slots * a.M), up(4 * (size_t)a.M), up(4 * (size_t)a.M), up(4 * pairs),
@@ -137,12 +144,16 @@ hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
     e = launch_moe_product(a, MOE_FEW_UP, s);
     return e == hipSuccess ? launch_moe_product(a, MOE_FEW_DOWN, s) : e;
   }
-  hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
+  const dim3 tokens((unsigned)a.M);
+  if (a.E <= 64) hipLaunchKernelGGL(moe_route_kernel<1>, tokens, dim3(64), 0, s, a);
+  else if (a.E <= 128) hipLaunchKernelGGL(moe_route_kernel<2>, tokens, dim3(64), 0, s, a);
+  else if (a.E <= 256) hipLaunchKernelGGL(moe_route_kernel<4>, tokens, dim3(64), 0, s, a);
+  else hipLaunchKernelGGL(moe_route_kernel<16>, tokens, dim3(64), 0, s, a);
   e = hipGetLastError();
   if (e == hipSuccess) e = launch_moe_product(a, MOE_UP, s);
   if (e == hipSuccess) e = launch_moe_product(a, MOE_DOWN, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.N + 1023) / 1024), (unsigned)a.M), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(moe_join_kernel<64>, dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 
