@@ -373,7 +373,8 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
   int chosen = 0;
   const bool meta = leave && r == 0;
   if (meta) {
-    for (int o = 0; o < a.E; ++o) top = fmaxf(top, zm[o]);
+    for (int o = lane; o < a.E; o += 64) top = fmaxf(top, zm[o]);
+    top = wave_max_f32(top);
   }
   for (int e = threadIdx.x; e < a.E; e += 256) {
     const float z0 = zm[e];
@@ -447,6 +448,69 @@ __device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, 
     }
   }
   __syncthreads();
+  return e;
+}
+
+// The same for one token, by every wave for itself, without a barrier: the
+// largest of the logits that the lanes hold, r + 1 times.  A wave of the first
+// slot's first workgroup goes on to the last choice for what the weights are
+// divided by.
+constexpr int MOE_ONE_E = 256;  // experts that this is made for
+__device__ __forceinline__ int moe_find_one(const MoeArgs& a, int r, bool leave) {
+  constexpr int NZ = MOE_ONE_E / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float z[NZ], all = 0.f, top = 0.f, sum = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NZ; ++i) {
+    z[i] = -__builtin_inff();
+    if (64 * i + lane < a.E) {
+      const float v = load_as_f32(a.logits, 64 * i + lane, a.logit_dt);
+      nan |= v != v;
+      z[i] = v == v ? v : -__builtin_inff();
+    }
+  }
+  const bool meta = leave && r == 0 && wave == 3;
+  int e = -1, chosen = 0;
+  const int last = meta ? a.top_k - 1 : r;
+  for (int k = 0; k <= last; ++k) {
+    float most = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    most = wave_max_f32(most);
+    if (k == 0) top = most;
+    if (k == 0 && meta && !a.renormalize) {
+#pragma unroll
+      for (int i = 0; i < NZ; ++i) all += z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.f;
+      all = wave_sum(all);
+    }
+    if (!(most > -__builtin_inff())) break;
+    int at_k = -1;
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) {
+      const uint64_t at = __ballot(z[i] == most);
+      if (at_k < 0 && at) {
+        const int l = __builtin_ctzll(at);
+        at_k = 64 * i + l;
+        if (lane == l) z[i] = -__builtin_inff();
+      }
+    }
+    if (k == r) {
+      e = at_k;
+      if (leave && wave == 0 && lane == 0) a.weights[r] = expf(most - top);
+    }
+    sum += expf(most - top);
+    ++chosen;
+  }
+  if (leave && wave == 0 && lane == 0) {
+    a.counts[2 * r] = e >= 0;
+    a.counts[2 * r + 1] = e;
+  }
+  if (meta) {
+    nan = __ballot(nan) != 0;
+    if (lane == 0) {
+      a.chosen[0] = chosen;
+      a.sums[0] = nan ? __builtin_nanf("") : a.renormalize ? sum : all;
+    }
+  }
   return e;
 }
 
@@ -790,12 +854,14 @@ __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) 
   const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
   float* z = reinterpret_cast<float*>(lds + 4 * (s.x_bytes + St::BYTES));
   bool nan = false;
-  if (threadIdx.x == 0) l.found = -1;
-  const int m0 = blockIdx.y / a.top_k;
-  for (int i = threadIdx.x; i < a.M * a.E; i += 256) {
-    const float v = load_as_f32(a.logits, i, a.logit_dt);
-    z[i] = v == v ? v : -__builtin_inff();
-    nan |= v != v && i / a.E == m0;
+  if constexpr (TOK > 1) {
+    if (threadIdx.x == 0) l.found = -1;
+    const int m0 = blockIdx.y / a.top_k;
+    for (int i = threadIdx.x; i < a.M * a.E; i += 256) {
+      const float v = load_as_f32(a.logits, i, a.logit_dt);
+      z[i] = v == v ? v : -__builtin_inff();
+      nan |= v != v && i / a.E == m0;
+    }
   }
   Xq x[TOK];
   const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
@@ -804,9 +870,17 @@ __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) 
       x[t].load((const uint16_t*)a.x + (long)min(t, a.M - 1) * a.N, s.K, q, lane, there && t < a.M);
   };
   load_x(q0, q0 < q1);
-  __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane(moe_find(a, blockIdx.y, blockIdx.x == 0, z, nan, l));
-  if (l.count == 0) return;
+  int e;
+  if constexpr (TOK > 1) {
+    __syncthreads();
+    e = moe_find(a, blockIdx.y, blockIdx.x == 0, z, nan, l);
+    if (l.count == 0) return;
+  } else {
+    e = moe_find_one(a, blockIdx.y, blockIdx.x == 0);
+    if (threadIdx.x == 0) l.pair[0] = blockIdx.y;
+    if (__builtin_amdgcn_readfirstlane(e) < 0) return;  // (in every wave alike)
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
   unsigned char* mine = lds + wave * s.x_bytes;
   const unsigned char* xa = mine + (h * TOK + moe_vrow(c, TOK)) * 16;
   float total[2][1] = {{0.f}, {0.f}};
@@ -881,7 +955,7 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
     float weight[TOK];
 #pragma unroll
     for (int t = 0; t < TOK; ++t) {
-      pair[t] = a.lists[slot * a.M + min(t, count - 1)];
+      pair[t] = TOK > 1 ? a.lists[slot * a.M + min(t, count - 1)] : slot;
       weight[t] = a.weights[pair[t]];
     }
     St st;
@@ -960,7 +1034,7 @@ hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   if (step == MOE_FEW_UP) {
     s.x_bytes = QUAD * (a.M == 1 ? 1 : FEW);
     const dim3 grid((unsigned)tiles, (unsigned)(a.M * a.top_k));
-    const int lds = 4 * (s.x_bytes + St::BYTES) + 4 * a.M * a.E;
+    const int lds = 4 * (s.x_bytes + St::BYTES) + (a.M == 1 ? 0 : 4 * a.M * a.E);
     if (a.M == 1) hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, 1>), grid, dim3(256), lds, st, a, s);
     else hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, FEW>), grid, dim3(256), lds, st, a, s);
     return hipGetLastError();

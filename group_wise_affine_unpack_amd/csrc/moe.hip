@@ -116,7 +116,7 @@ __global__ __launch_bounds__(BLOCK) void moe_join_kernel(MoeArgs a) {
 
 hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
   // a few tokens find their experts in the products themselves
-  const bool few = a.M <= moe_few(a.bits) && a.M * a.E <= 1024;
+  const bool few = a.M == 1 ? a.E <= 256 : a.M <= moe_few(a.bits) && a.M * a.E <= 1024;
   const size_t pairs = (size_t)a.M * a.top_k, slots = few || pairs < (size_t)a.E ? pairs : (size_t)a.E;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t sizes[8] = {up(8 * slots), up(4 * slots * a.M), up(4 * (size_t)a.M), up(4 * (size_t)a.M), up(4 * pairs),
