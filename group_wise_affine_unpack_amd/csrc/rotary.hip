@@ -41,7 +41,9 @@ template <bool F16_>
 __device__ __forceinline__ uint32_t round_f64(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   const uint32_t hi = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
-  return f32_to_act_bits((float)__builtin_bit_cast(double, (uint64_t)hi << 32), F16_);
+  float f = (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
+  asm("" : "+v"(f));  // (else f16 comes from the double in some 60 integer steps)
+  return f32_to_act_bits(f, F16_);
 }
 
 template <bool F16_>
@@ -100,81 +102,122 @@ __device__ __forceinline__ void make_angles(const RotArgs& a, const RotGrid& g, 
 }
 
 // Rows whose 8-column chunks are 16-byte aligned and hold no pair's end.
-// Units of a head: half layout R/16 pairs of chunks, then the chunks that
-// stay; interleaved, chunks.  BITS = 0: q and k to dense arrays; else k and v
-// go to the cache, chunk by chunk.
+// Items of q (and of k where it goes to a dense array): in the half layout
+// R/16 pairs of chunks a head, then the chunks that stay; interleaved, chunks.
+// BITS = 0: q and k to dense arrays; else k and v go to the cache, chunk by
+// chunk.  An item's loads are issued before the one ahead of it is computed,
+// and the first item's before the angles are.
 template <bool F16_, int BITS, int G>
 __global__ __launch_bounds__(256) void rotary_kernel(RotArgs a, RotGrid g, KvCache c) {
   extern __shared__ double2 cs[];  // [tokens][R/2]
-  const uint32_t t0 = blockIdx.x * g.tokens;
-  make_angles(a, g, t0, cs);
-  __syncthreads();
-  const uint32_t R = 2 * g.half.d, chunks = g.chunks.d, end = min((blockIdx.y + 1) * g.per_wg, g.tokens * g.items.d);
-  for (uint32_t i = blockIdx.y * g.per_wg + threadIdx.x; i < end; i += 256u) {
-    const uint32_t t = g.items.div(i), it = i - t * g.items.d, tok = t0 + t;
-    if (tok >= (uint32_t)a.T) break;
-    const double2* angles = cs + t * g.half.d;
+  const uint32_t t0 = blockIdx.x * g.tokens, R = 2 * g.half.d, chunks = g.chunks.d;
+  const uint32_t end = min((blockIdx.y + 1) * g.per_wg, min(g.tokens, (uint32_t)a.T - t0) * g.items.d);
+  enum Kind : uint32_t { NONE, DENSE, KEY, VALUE };
+  struct Item {
+    Kind kind;
+    uint32_t t, h, u;  // token of the workgroup, head, unit or chunk
+    bool is_k;
+    int64_t slot;
+    u32x4_t own, other;
+  };
+  const auto fetch = [&](uint32_t i, Item& d) __attribute__((always_inline)) {
+    d.kind = NONE;
+    d.slot = 0;
+    if (i >= end) return;
+    d.t = g.items.div(i);
+    const uint32_t it = i - d.t * g.items.d, tok = t0 + d.t;
+    const uint16_t* own;
+    const uint16_t* other;
     if (BITS == 0 || it < g.q_items) {
-      uint32_t h = g.units.div(it);
-      const uint32_t u = it - h * g.units.d;
-      const bool is_k = BITS == 0 && h >= (uint32_t)a.heads;
-      if (is_k) h -= a.heads;
-      if (BITS != 0 && h >= (uint32_t)a.heads) continue;  // (the padding of q's items)
-      const uint16_t* src = (const uint16_t*)(is_k ? a.k : a.q) + (int64_t)tok * (is_k ? a.kts : a.qts) + (int64_t)h * (is_k ? a.khs : a.qhs);
-      uint16_t* dst = (uint16_t*)(is_k ? a.ko : a.qo) + (int64_t)tok * (is_k ? a.kots : a.qots) + (int64_t)h * (is_k ? a.kohs : a.qohs);
-      uint32_t e[8];
-      if (a.interleaved) {
-        u32x4_t own = *reinterpret_cast<const u32x4_t*>(src + 8 * u);
-        if (8 * u < R) {
-          turn_pairs<F16_>(own, angles + 4 * u, e);
-          own = pack8(e);
-        }
-        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = own;
-      } else if (16 * u < R) {
-        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 8 * u);
-        const u32x4_t y = *reinterpret_cast<const u32x4_t*>(src + 8 * u + R / 2);
-        turn_half<F16_, false>(x, y, angles + 8 * u, e);
-        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = pack8(e);
-        turn_half<F16_, true>(y, x, angles + 8 * u, e);
-        *reinterpret_cast<u32x4_t*>(dst + 8 * u + R / 2) = pack8(e);
-      } else {
-        const uint32_t at = 8 * u + R / 2;
-        *reinterpret_cast<u32x4_t*>(dst + at) = *reinterpret_cast<const u32x4_t*>(src + at);
-      }
-    } else if constexpr (BITS != 0) {
-      // a row's chunk into the cache; the lanes of a group are neighbours and share their token, head and kind
+      d.h = g.units.div(it);
+      d.u = it - d.h * g.units.d;
+      d.is_k = BITS == 0 && d.h >= (uint32_t)a.heads;
+      if (d.is_k) d.h -= a.heads;
+      if (BITS != 0 && d.h >= (uint32_t)a.heads) return;  // (the padding of q's items)
+      d.kind = DENSE;
+      const uint16_t* src = (const uint16_t*)(d.is_k ? a.k : a.q) + (int64_t)tok * (d.is_k ? a.kts : a.qts) + (int64_t)d.h * (d.is_k ? a.khs : a.qhs);
+      const bool pair = !a.interleaved && 16 * d.u < R;
+      own = src + 8 * d.u + (a.interleaved || pair ? 0 : R / 2);
+      other = pair ? own + R / 2 : own;
+    } else {
       const uint32_t kv = it - g.q_items;
       const bool is_v = kv >= g.k_items;
-      const uint32_t j = is_v ? kv - g.k_items : kv, h = g.chunks.div(j), ch = j - h * chunks;
-      if (h >= (uint32_t)c.kv_heads) continue;  // (the padding of a token's items)
-      const int64_t slot = a.slots[tok];
-      if (slot < 0 || slot >= c.num_slots) continue;
-      const uint16_t* src = is_v ? (const uint16_t*)a.v + (int64_t)tok * a.vts + (int64_t)h * a.vhs
-                                 : (const uint16_t*)a.k + (int64_t)tok * a.kts + (int64_t)h * a.khs;
-      u32x4_t own = *reinterpret_cast<const u32x4_t*>(src + 8 * ch);
-      if (!is_v && 8 * ch < R) {
-        uint32_t e[8];
-        if (a.interleaved) {
-          turn_pairs<F16_>(own, angles + 4 * ch, e);
-        } else {
-          const bool second = 16 * ch >= R;
-          const uint32_t first = second ? ch - R / 16 : ch;
-          const u32x4_t other = *reinterpret_cast<const u32x4_t*>(src + 8 * first + (second ? 0 : R / 2));
-          if (second) turn_half<F16_, true>(own, other, angles + 8 * first, e);
-          else turn_half<F16_, false>(own, other, angles + 8 * first, e);
-        }
-        own = pack8(e);
-      }
-      float x[8];
-      unpack8<F16_>(own, x);
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-        if constexpr (!F16_) x[m] = __builtin_canonicalizef(x[m]);  // only quiet NaN stay out of the minimum
-      const uint32_t pg = g.page.div((uint32_t)slot), off = (uint32_t)slot - pg * g.page.d;
-      const KvRowAt at{((size_t)pg * c.kv_heads + h) * c.page_size + off, ch, chunks};
-      write_codes<BITS, G, F16_>(x, at, is_v ? c.v_packed : c.k_packed, is_v ? c.v_scales : c.k_scales,
-                                 is_v ? c.v_biases : c.k_biases);
+      const uint32_t j = is_v ? kv - g.k_items : kv;
+      d.h = g.chunks.div(j);
+      d.u = j - d.h * chunks;
+      d.is_k = !is_v;
+      if (d.h >= (uint32_t)c.kv_heads) return;  // (the padding of a token's items)
+      d.slot = a.slots[tok];
+      d.kind = is_v ? VALUE : KEY;
+      const uint16_t* src = is_v ? (const uint16_t*)a.v + (int64_t)tok * a.vts + (int64_t)d.h * a.vhs
+                                 : (const uint16_t*)a.k + (int64_t)tok * a.kts + (int64_t)d.h * a.khs;
+      own = src + 8 * d.u;
+      other = own;
+      if (!is_v && !a.interleaved && 8 * d.u < R) other = 16 * d.u < R ? own + R / 2 : own - R / 2;
     }
+    d.own = *reinterpret_cast<const u32x4_t*>(own);
+    d.other = *reinterpret_cast<const u32x4_t*>(other);
+  };
+  const uint32_t first = blockIdx.y * g.per_wg + threadIdx.x;
+  Item now, next;
+  fetch(first, now);
+  make_angles(a, g, t0, cs);
+  __syncthreads();
+  for (uint32_t i = first; i < end; i += 256u) {
+    fetch(i + 256u, next);
+    const double2* angles = cs + now.t * g.half.d;
+    const uint32_t u = now.u;
+    uint32_t e[8];
+    if (now.kind == DENSE) {
+      uint16_t* dst = (uint16_t*)(now.is_k ? a.ko : a.qo) + (int64_t)(t0 + now.t) * (now.is_k ? a.kots : a.qots) + (int64_t)now.h * (now.is_k ? a.kohs : a.qohs);
+      if (a.interleaved) {
+        if (8 * u < R) {
+          turn_pairs<F16_>(now.own, angles + 4 * u, e);
+          now.own = pack8(e);
+        }
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = now.own;
+      } else if (16 * u < R) {
+        turn_half<F16_, false>(now.own, now.other, angles + 8 * u, e);
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u) = pack8(e);
+        turn_half<F16_, true>(now.other, now.own, angles + 8 * u, e);
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u + R / 2) = pack8(e);
+      } else {
+        *reinterpret_cast<u32x4_t*>(dst + 8 * u + R / 2) = now.own;
+      }
+    } else if (BITS != 0 && now.kind != NONE && now.slot >= 0 && now.slot < c.num_slots) {
+      // a row's chunk into the cache; the lanes of a group are neighbours and share their token, head and kind
+      if constexpr (BITS != 0) {
+        const bool is_v = now.kind == VALUE;
+        if (!is_v && 8 * u < R) {
+          if (a.interleaved) {
+            turn_pairs<F16_>(now.own, angles + 4 * u, e);
+          } else {
+            // a second chunk is b c + a s, a first one a c + b (-s): one code for both, the sign in s
+            const bool second = 16 * u >= R;
+            const double2* cs8 = angles + 8 * (second ? u - R / 16 : u);
+            float x[8], y[8];
+            unpack8<F16_>(now.own, x);
+            unpack8<F16_>(now.other, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const double2 t = cs8[j];
+              e[j] = round_f64<F16_>((double)x[j] * t.x + (double)y[j] * (second ? t.y : -t.y));
+            }
+          }
+          now.own = pack8(e);
+        }
+        float x[8];
+        unpack8<F16_>(now.own, x);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if constexpr (!F16_) x[m] = __builtin_canonicalizef(x[m]);  // only quiet NaN stay out of the minimum
+        const uint32_t pg = g.page.div((uint32_t)now.slot), off = (uint32_t)now.slot - pg * g.page.d;
+        const KvRowAt at{((size_t)pg * c.kv_heads + now.h) * c.page_size + off, u, chunks};
+        write_codes<BITS, G, F16_>(x, at, is_v ? c.v_packed : c.k_packed, is_v ? c.v_scales : c.k_scales,
+                                   is_v ? c.v_biases : c.k_biases);
+      }
+    }
+    now = next;
   }
 }
 
