@@ -216,6 +216,14 @@ def _row_ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+def _rows(t: torch.Tensor, dense: bool = False):
+    """Address and strides of rows [T, heads, D]; `dense`: the call has just made it."""
+    if dense:
+        _, m, d = t.shape
+        return t.data_ptr(), m * d, d
+    return (_row_ptr(t), *_strides(t))
+
+
 def _strides(t: torch.Tensor):
     """Strides of the two leading dimensions; 0 where one has a single entry, whose stride means nothing."""
     a, b = t.stride()[:2]
@@ -714,10 +722,10 @@ def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rot: Rotar
     if k.dtype != q.dtype:
         raise ValueError("q and k must have one dtype")
     _check_positions(q, rot, positions)
-    q_out, k_out = _out(q_out, q), _out(k_out, k)
-    _run("rotary", q.device, rot.ref, _row_ptr(q), *_strides(q), _row_ptr(k), *_strides(k), _row_ptr(q_out), *_strides(q_out),
-         _row_ptr(k_out), *_strides(k_out), _ptr(positions), T, H, HK, D, _dt(q))
-    return q_out, k_out
+    qo, ko = _out(q_out, q), _out(k_out, k)
+    _run("rotary", q.device, rot.ref, *_rows(q), *_rows(k), *_rows(qo, q_out is None), *_rows(ko, k_out is None),
+         _ptr(positions), T, H, HK, D, _dt(q))
+    return qo, ko
 
 
 def kv_cache_append_rotary_affine(cache: AffineKVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -734,8 +742,8 @@ def kv_cache_append_rotary_affine(cache: AffineKVCache, q: torch.Tensor, k: torc
         raise ValueError(f"q, k and v must be {cache.dtype}, slots int64")
     _check_positions(q, rot, positions)
     o = _out(q_out, q)
-    _run("kv_cache_append_rotary_affine", dev, cache.ref, rot.ref, _row_ptr(q), *_strides(q), _row_ptr(k), *_strides(k),
-         _row_ptr(v), *_strides(v), _row_ptr(o), *_strides(o), _ptr(positions), _ptr(slots), T, H)
+    _run("kv_cache_append_rotary_affine", dev, cache.ref, rot.ref, *_rows(q), *_rows(k), *_rows(v), *_rows(o, q_out is None),
+         _ptr(positions), _ptr(slots), T, H)
     return o
 
 
