@@ -327,13 +327,11 @@ struct MoeArgs {
 struct MoeShape {
   int K;        // columns of the product
   int pairs;    // slots are pairs, not experts
-  int rows;     // x rows a pass
   int tiles;    // a wave's, where it takes whole rows
   int x_bytes;  // x in LDS, a wave's where it takes a part of the columns
 };
-enum MoeStep : int { MOE_UP, MOE_DOWN, MOE_FEW_UP, MOE_FEW_DOWN };
-// up to how many tokens take the two kernels of a few (2-bit codes: the x rows of four would not fit LDS)
-constexpr int moe_few(int bits) { return bits == 2 ? 2 : 4; }
+enum MoeStep : int { MOE_UP, MOE_DOWN, MOE_ONE_UP, MOE_ONE_DOWN };
+constexpr int MOE_ONE_E = 256;  // experts that the kernels of one token are made for
 hipError_t launch_moe(MoeArgs& a, hipStream_t s);
 
 struct PagedAttnArgs {

@@ -7,10 +7,10 @@
 // Kernels, for a batch: route (a wave a token: its choices), up (G, U and
 // silu: one f32 row h of each pair of token and choice), down (D on those rows:
 // one f32 partial row a pair), join (a token's pairs added in the order of
-// their logits, the residual, the one rounding).  For up to four tokens two:
-// up, each workgroup of which finds its expert itself, and down, whose
-// workgroups go through all chosen experts and finish y.  No atomics: the same
-// call gives the same bits.
+// their logits, the residual, the one rounding).  For one token two: up, each
+// wave of which finds its expert itself, and down, whose workgroups go through
+// all chosen experts and finish y.  No atomics: the same call gives the same
+// bits.
 //
 // The products run on the matrix cores for every number of tokens, 16 weight
 // rows a tile and 16 rows of x (M = 1 uses one of them: the matrix cores are
@@ -349,113 +349,10 @@ struct Stream {
 
 // ---- routing ----------------------------------------------------------------
 
-constexpr int MOE_FEW = 4;  // tokens whose experts each workgroup finds for itself, at most
-
-struct MoeFew {
-  int found, count;
-  int pair[MOE_FEW];  // of each token, -1 where it has not chosen the expert
-  int rank[MOE_FEW];
-  float weight[MOE_FEW];
-  float part[4];
-  int cpart[4];
-};
-
-// The expert of slot m * top_k + r, the r-th choice of token m, found by every
-// workgroup of the slot, and which tokens chose it; count = 0 unless m is the
-// first of them.  z: [M, E] logits, a NaN as minus infinity, in LDS; nan: one
-// of token m's that this thread loaded was.  The slot's first workgroup
-// (leave) writes what down needs.
-__device__ __forceinline__ int moe_find(const MoeArgs& a, int slot, bool leave, const float* z, bool nan, MoeFew& l) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m = slot / a.top_k, r = slot - m * a.top_k;
-  const float* zm = z + m * a.E;
-  float sum = 0.f, top = -__builtin_inff();
-  int chosen = 0;
-  const bool meta = leave && r == 0;
-  if (meta) {
-    for (int o = lane; o < a.E; o += 64) top = fmaxf(top, zm[o]);
-    top = wave_max_f32(top);
-  }
-  for (int e = threadIdx.x; e < a.E; e += 256) {
-    const float z0 = zm[e];
-    int rank = 0;
-#pragma unroll 8
-    for (int o = 0; o < a.E; ++o) {
-      const float v = zm[o];
-      rank += v > z0 || (v == z0 && o < e);
-    }
-    const bool there = z0 > -__builtin_inff();
-    if (rank == r && there) l.found = e;
-    if (there && (rank < a.top_k || !a.renormalize)) sum += expf(z0 - top);
-    chosen += there && rank < a.top_k;
-  }
-  if (meta) {  // token m's number of choices, and what its weights are divided by
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) chosen += __shfl_xor(chosen, d);
-    nan = __ballot(nan) != 0;
-    if (lane == 0) {
-      l.part[wave] = nan ? __builtin_nanf("") : sum;
-      l.cpart[wave] = chosen;
-    }
-  }
-  __syncthreads();
-  if (meta && threadIdx.x == 0) {
-    a.sums[m] = l.part[0] + l.part[1] + l.part[2] + l.part[3];
-    a.chosen[m] = l.cpart[0] + l.cpart[1] + l.cpart[2] + l.cpart[3];
-  }
-  const int e = l.found;
-  if (wave < a.M && e >= 0 && (a.M > 1 || leave)) {  // where token `wave` has the expert
-    const float* zt = z + wave * a.E;
-    const float z0 = zt[e];
-    int rank = 0;
-    float most = -__builtin_inff();
-    for (int i = 0; i < a.E; i += 64) {
-      const int o = i + lane;
-      const float v = o < a.E ? zt[o] : -__builtin_inff();
-      rank += __builtin_popcountll(__ballot(o < a.E && (v > z0 || (v == z0 && o < e))));
-      most = fmaxf(most, v);
-    }
-    most = wave_max_f32(most);
-    if (lane == 0) {
-      l.rank[wave] = z0 > -__builtin_inff() ? rank : a.E;
-      l.weight[wave] = expf(z0 - most);
-    }
-  }
-  if (a.M > 1 || leave) __syncthreads();
-  if (threadIdx.x == 0) {
-    int count = 0, first = -1;
-    for (int t = 0; t < MOE_FEW; ++t) {
-      int pair = -1;
-      if (t < a.M && e >= 0) {
-        const int rank = a.M > 1 ? l.rank[t] : r;
-        if (rank < a.top_k) {
-          if (first < 0) first = t;
-          pair = t * a.top_k + rank;
-          if (leave) a.weights[pair] = l.weight[t];
-          ++count;
-        }
-      }
-      l.pair[t] = pair;
-    }
-    if (first != m) count = 0;  // an earlier token's slot takes the expert
-    l.count = count;
-    if (leave) {
-      a.counts[2 * slot] = count;
-      a.counts[2 * slot + 1] = e;
-      for (int t = 0, i = 0; t < MOE_FEW; ++t)
-        if (count && l.pair[t] >= 0) a.lists[slot * a.M + i++] = l.pair[t];
-    }
-  }
-  __syncthreads();
-  return e;
-}
-
-// The same for one token, by every wave for itself, without a barrier: the
-// largest of the logits that the lanes hold, r + 1 times.  A wave of the first
-// slot's first workgroup goes on to the last choice for what the weights are
-// divided by.
-constexpr int MOE_ONE_E = 256;  // experts that this is made for
+// One token: its r-th choice, found by every wave for itself without a barrier,
+// the largest of the logits that the lanes hold r + 1 times.  The slot's first
+// workgroup (leave) writes what down needs; of the first slot's, a wave goes on
+// to the last choice for what the weights are divided by.
 __device__ __forceinline__ int moe_find_one(const MoeArgs& a, int r, bool leave) {
   constexpr int NZ = MOE_ONE_E / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -838,51 +735,25 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 3) void moe_kernel(MoeArgs a, Mo
   }
 }
 
-// Up for a few tokens: a slot is a pair of token and choice.  x of every token
-// is loaded ahead of the routing, on which it does not depend.
-template <int BITS, int G, bool F16_, int TOK>
-__global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) {
+// Up for one token: a slot is a choice.  x is loaded ahead of the routing, on
+// which it does not depend.
+template <int BITS, int G, bool F16_>
+__global__ __launch_bounds__(256) void moe_one_up_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 2>;
   using Xq = XQuad<BITS, G, F16_, false>;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ float own_back[4][MOE_FEW];
   __shared__ float red[512];
-  __shared__ MoeFew l;
+  __shared__ int pair;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4;
   const int quads = (s.K + St::COLS - 1) / St::COLS, each = (quads + 3) / 4;
   const int q0 = min(wave * each, quads), q1 = min(q0 + each, quads);
-  float* z = reinterpret_cast<float*>(lds + 4 * (s.x_bytes + St::BYTES));
-  bool nan = false;
-  if constexpr (TOK > 1) {
-    if (threadIdx.x == 0) l.found = -1;
-    const int m0 = blockIdx.y / a.top_k;
-    for (int i = threadIdx.x; i < a.M * a.E; i += 256) {
-      const float v = load_as_f32(a.logits, i, a.logit_dt);
-      z[i] = v == v ? v : -__builtin_inff();
-      nan |= v != v && i / a.E == m0;
-    }
-  }
-  Xq x[TOK];
-  const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < TOK; ++t)
-      x[t].load((const uint16_t*)a.x + (long)min(t, a.M - 1) * a.N, s.K, q, lane, there && t < a.M);
-  };
-  load_x(q0, q0 < q1);
-  int e;
-  if constexpr (TOK > 1) {
-    __syncthreads();
-    e = moe_find(a, blockIdx.y, blockIdx.x == 0, z, nan, l);
-    if (l.count == 0) return;
-  } else {
-    e = moe_find_one(a, blockIdx.y, blockIdx.x == 0);
-    if (threadIdx.x == 0) l.pair[0] = blockIdx.y;
-    if (__builtin_amdgcn_readfirstlane(e) < 0) return;  // (in every wave alike)
-  }
-  e = __builtin_amdgcn_readfirstlane(e);
+  Xq x;
+  x.load(a.x, s.K, q0, lane, q0 < q1);
+  const int e = __builtin_amdgcn_readfirstlane(moe_find_one(a, blockIdx.y, blockIdx.x == 0));
+  if (e < 0) return;  // (in every wave alike)
+  if (threadIdx.x == 0) pair = blockIdx.y;
   unsigned char* mine = lds + wave * s.x_bytes;
-  const unsigned char* xa = mine + (h * TOK + moe_vrow(c, TOK)) * 16;
+  const unsigned char* xa = mine + (lane >> 4) * 16;
   float total[2][1] = {{0.f}, {0.f}};
   St st;
   st.buf = lds + 4 * s.x_bytes + wave * St::BYTES;
@@ -894,112 +765,79 @@ __global__ __launch_bounds__(256) void moe_few_up_kernel(MoeArgs a, MoeShape s) 
   st.load(q0 < q1 ? q0 : quads, w0);
   st.load(q0 + 1 < q1 ? q0 + 1 : quads, w1);
   const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      const float f = x[t].put(mine, TOK, t, lane);
-      if (lane == 0) own_back[wave][t] = f;
-    }
+    const float back = x.put(mine, 1, 0, lane);
     if (q == q0 || q % St::QPB == 0) {
       st.put(pr);
       const int next = (q / St::QPB + 1) * St::QPB;
       st.load(next < q1 ? next / St::QPB : quads, pr);
     }
-    load_x(q + 1, q + 1 < q1);
-    __builtin_amdgcn_wave_barrier();
+    x.load(a.x, s.K, q + 1, lane, q + 1 < q1);
+    __builtin_amdgcn_wave_barrier();  // (LDS of this wave alone, whose operations stay in order)
     float acc[2][1] = {{0.f}, {0.f}};
-    st.template compute<1, TOK>(q, d, xa, acc);
+    st.template compute<1, 1>(q, d, xa, acc);
     st.load(q + 2 < q1 ? q + 2 : quads, d);
-    const float k = own_back[wave][min(h, TOK - 1)];
-    total[0][0] = fmaf(acc[0][0] * 0x1p24f, k, total[0][0]);
-    total[1][0] = fmaf(acc[1][0] * 0x1p24f, k, total[1][0]);
+    total[0][0] = fmaf(acc[0][0] * 0x1p24f, back, total[0][0]);
+    total[1][0] = fmaf(acc[1][0] * 0x1p24f, back, total[1][0]);
     __builtin_amdgcn_wave_barrier();
   };
   for (int q = q0; q < q1; q += 2) {
     step(q, w0);
     if (q + 1 < q1) step(q + 1, w1);
   }
-  moe_finish<false, 1>(a, l.pair, TOK, red, blockIdx.x, total);
+  moe_finish<false, 1>(a, &pair, 1, red, blockIdx.x, total);
 }
 
-// Down for a few tokens: 16 rows of D of all slots, whose quads the waves
-// share evenly, and y.
-constexpr int MOE_FEW_WAVES = 8;
-template <int BITS, int G, bool F16_, int TOK>
-__global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArgs a, MoeShape s) {
+// Down for one token: 16 rows of D of all slots, whose quads the waves share
+// evenly, and y.
+constexpr int MOE_ONE_WAVES = 8;
+template <int BITS, int G, bool F16_>
+__global__ __launch_bounds__(64 * MOE_ONE_WAVES) void moe_one_down_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 1>;
   using Xq = XQuad<BITS, G, F16_, true>;
-  constexpr int NI = (2 * TOK + 3) / 4, ROWS = 2 * TOK;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ float red[MOE_FEW_WAVES * NI * 64];
+  __shared__ float red[MOE_ONE_WAVES * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
-  // the output that this thread finishes
-  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
-  const long at_y = (long)min(m, a.M - 1) * a.N + 16 * blockIdx.x + n;
+  const int n = threadIdx.x & 15;  // the output that the first threads finish
+  const long at_y = 16 * (long)blockIdx.x + n;
   const float resid = a.resid ? load_as_f32(a.resid, at_y, a.act_dt) : 0.f;
-  const float sum = a.sums[min(m, a.M - 1)];
-  const int chosen = a.chosen[min(m, a.M - 1)];
-  const int slots = a.M * a.top_k, quads = (a.I + St::COLS - 1) / St::COLS;
+  const float sum = a.sums[0];
+  const int chosen = a.chosen[0], quads = (a.I + St::COLS - 1) / St::COLS;
   unsigned char* mine = lds + wave * s.x_bytes;
-  const unsigned char* xa = mine + (h * ROWS + moe_vrow(c, ROWS)) * 16;
-  float total[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) total[i] = 0.f;
-  const int all = slots * quads, from = wave * all / MOE_FEW_WAVES, to = (wave + 1) * all / MOE_FEW_WAVES;
+  const unsigned char* xa = mine + (h * 2 + moe_vrow(c, 2)) * 16;
+  float total = 0.f;
+  const int all = chosen * quads, from = wave * all / MOE_ONE_WAVES, to = (wave + 1) * all / MOE_ONE_WAVES;
   for (int at = from; at < to;) {
     const int slot = at / quads, q0 = at - slot * quads, q1 = min(quads, q0 + to - at);
     at += q1 - q0;
-    const int count = a.counts[2 * slot], e = a.counts[2 * slot + 1];
-    if (count == 0) continue;
-    int pair[TOK];
-    float weight[TOK];
-#pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      pair[t] = TOK > 1 ? a.lists[slot * a.M + min(t, count - 1)] : slot;
-      weight[t] = a.weights[pair[t]];
-    }
+    const int e = __builtin_amdgcn_readfirstlane(a.counts[2 * slot + 1]);
+    const float weight = a.weights[slot];
     St st;
-    st.buf = lds + MOE_FEW_WAVES * s.x_bytes + wave * St::BYTES;
+    st.buf = lds + MOE_ONE_WAVES * s.x_bytes + wave * St::BYTES;
     st.lane = lane;
     typename St::Quad w0, w1;
     typename St::Params pr;
-    Xq x[TOK];
+    Xq x;
     const long row0 = (long)e * a.N + 16 * blockIdx.x;
+    const void* src = moe_source<true>(a, slot);
+    x.load(src, a.I, q0, lane, true);
     st.open(a.down_packed, a.down_scales, a.down_biases, row0, row0, a.I);
-    const auto load_x = [&](int q, bool there) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < TOK; ++t) x[t].load(moe_source<true>(a, pair[t]), a.I, q, lane, there && t < count);
-    };
     st.load(q0 / St::QPB, pr);
-    load_x(q0, true);
     st.load(q0, w0);
     st.load(q0 + 1 < q1 ? q0 + 1 : quads, w1);
-      const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
-      float back[TOK];
-#pragma unroll
-      for (int t = 0; t < TOK; ++t) back[t] = x[t].put(mine, ROWS, 2 * t, lane) * weight[t];
+    const auto step = [&](int q, typename St::Quad& d) __attribute__((always_inline)) {
+      const float back = x.put(mine, 2, 0, lane) * weight;
       if (q == q0 || q % St::QPB == 0) {
         st.put(pr);
         const int next = (q / St::QPB + 1) * St::QPB;
         st.load(next < q1 ? next / St::QPB : quads, pr);
       }
-      load_x(q + 1, q + 1 < q1);
+      x.load(src, a.I, q + 1, lane, q + 1 < q1);
       __builtin_amdgcn_wave_barrier();
-      float acc[1][NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[0][i] = 0.f;
-      st.template compute<NI, ROWS>(q, d, xa, acc);
+      float acc[1][1] = {{0.f}};
+      st.template compute<1, 2>(q, d, xa, acc);
       st.load(q + 2 < q1 ? q + 2 : quads, d);
-      // x row 4 i + h holds part h % 2 of the list's token t = 2 i + h / 2, whose sums go to row 2 token + part
-#pragma unroll
-      for (int t = 0; t < TOK; ++t) {
-        const int tok = pair[t] / a.top_k;
-        float v = acc[0][t >> 1];
-        if constexpr (TOK > 1) v = __shfl(v, 16 * ((2 * t + (h & 1)) & 3) + c);
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (t < count && 4 * i + h == 2 * tok + (h & 1)) total[i] = fmaf(v * 0x1p24f, back[t], total[i]);
-      }
+      total = fmaf(acc[0][0] * 0x1p24f, back, total);
       __builtin_amdgcn_wave_barrier();
     };
     for (int q = q0; q < q1; q += 2) {
@@ -1007,16 +845,12 @@ __global__ __launch_bounds__(64 * MOE_FEW_WAVES) void moe_few_down_kernel(MoeArg
       if (q + 1 < q1) step(q + 1, w1);
     }
   }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) red[(wave * NI + i) * 64 + lane] = total[i];
+  red[wave * 64 + lane] = total;
   __syncthreads();
-  if (m >= a.M) return;
+  if (threadIdx.x >= 16) return;
   float v = 0.f;
 #pragma unroll
-  for (int q = 0; q < MOE_FEW_WAVES; ++q) {
-    const float* p = red + (q * NI + (m >> 1)) * 64 + 32 * (m & 1) + n;  // rows 2 m and 2 m + 1
-    v += p[0] + p[16];
-  }
+  for (int q = 0; q < MOE_ONE_WAVES; ++q) v += red[q * 64 + n] + red[q * 64 + 16 + n];  // high and low part
   float y = chosen ? fmaf(a.scale / sum, v, resid) : resid;
   if (sum != sum) y = __builtin_nanf("");
   ((uint16_t*)a.y)[at_y] = f32_to_act_bits(y, F16_);
@@ -1026,25 +860,20 @@ template <int BITS, int G, bool F16_>
 hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   using St = Stream<BITS, G, F16_, 2>;
   MoeShape s{};
-  const bool down = step == MOE_DOWN || step == MOE_FEW_DOWN;
+  const bool down = step == MOE_DOWN || step == MOE_ONE_DOWN;
   s.K = down ? a.I : a.N;
   const int quads = (s.K + St::COLS - 1) / St::COLS, tiles = down ? a.N / 32 : a.I / 16;
   constexpr int QUAD = St::COLS * 2;  // bytes of a quad of a row of x
-  constexpr int FEW = moe_few(BITS);
-  if (step == MOE_FEW_UP) {
-    s.x_bytes = QUAD * (a.M == 1 ? 1 : FEW);
-    const dim3 grid((unsigned)tiles, (unsigned)(a.M * a.top_k));
-    const int lds = 4 * (s.x_bytes + St::BYTES) + (a.M == 1 ? 0 : 4 * a.M * a.E);
-    if (a.M == 1) hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, 1>), grid, dim3(256), lds, st, a, s);
-    else hipLaunchKernelGGL((moe_few_up_kernel<BITS, G, F16_, FEW>), grid, dim3(256), lds, st, a, s);
+  if (step == MOE_ONE_UP) {
+    s.x_bytes = QUAD;
+    hipLaunchKernelGGL((moe_one_up_kernel<BITS, G, F16_>), dim3((unsigned)tiles, (unsigned)a.top_k), dim3(256),
+                       4 * (s.x_bytes + St::BYTES), st, a, s);
     return hipGetLastError();
   }
-  if (step == MOE_FEW_DOWN) {
-    s.x_bytes = QUAD * 2 * (a.M == 1 ? 1 : FEW);
-    const dim3 grid((unsigned)(a.N / 16)), block(64 * MOE_FEW_WAVES);
-    const int lds = MOE_FEW_WAVES * (s.x_bytes + Stream<BITS, G, F16_, 1>::BYTES);
-    if (a.M == 1) hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, 1>), grid, block, lds, st, a, s);
-    else hipLaunchKernelGGL((moe_few_down_kernel<BITS, G, F16_, FEW>), grid, block, lds, st, a, s);
+  if (step == MOE_ONE_DOWN) {
+    s.x_bytes = 2 * QUAD;
+    hipLaunchKernelGGL((moe_one_down_kernel<BITS, G, F16_>), dim3((unsigned)(a.N / 16)), dim3(64 * MOE_ONE_WAVES),
+                       MOE_ONE_WAVES * (s.x_bytes + Stream<BITS, G, F16_, 1>::BYTES), st, a, s);
     return hipGetLastError();
   }
   s.pairs = (int64_t)a.M * a.top_k < a.E;
@@ -1053,7 +882,9 @@ hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   const int64_t pairs = (int64_t)a.M * a.top_k;
   const int most = 2 * pairs <= 3 * (int64_t)a.E ? 4 : pairs <= 4 * (int64_t)a.E ? 8 : 16;
   const int rows = down ? std::min(2 * most, 16) : most;
-  const bool whole = rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 2048;
+  // whole rows a wave from a wave a SIMD on (3 tokens, 8 of 64 experts, 2048 x 1024, 1536 tiles: 48 us in parts, 38 whole;
+  // 8 tokens, 2 of 8, 4096 x 1024, 8-bit, 512: 43 and 52)
+  const bool whole = rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 1024;
   // A tile a wave, or two where that leaves a second round of workgroups less than half full (three a CU; 16 tokens, 8 of
   // 64 experts, 2048 x 1024: 1.2 rounds, 38 us with one and 33 with two; 64 tokens, 8 of 128, 2048 x 768: 2.0 rounds, 67
   // and 76).  Experts in use: what independent tokens would reach.

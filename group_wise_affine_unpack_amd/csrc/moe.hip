@@ -115,12 +115,15 @@ __global__ __launch_bounds__(BLOCK) void moe_join_kernel(MoeArgs a) {
 }  // namespace
 
 hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
-  // a few tokens find their experts in the products themselves
-  const bool few = a.M == 1 ? a.E <= 256 : a.M <= moe_few(a.bits) && a.M * a.E <= 1024;
-  const size_t pairs = (size_t)a.M * a.top_k, slots = few || pairs < (size_t)a.E ? pairs : (size_t)a.E;
+  // One token finds its experts in the products themselves and needs two launches, not four (2048 x 1024, 8 of 64: 18 us
+  // against 24; 4096 x 14336, 2 of 8: 57 and 67).  Down then has 16 rows a workgroup, so with fewer rows than the chip has
+  // workgroups for and many columns it takes the longer of the two (2048 x 8192, 4 of 16, eight quads of 256 bytes a wave:
+  // 47 and 42; 384 x 11648, 11 quads: 49 and 35).
+  const bool one = a.M == 1 && a.E <= MOE_ONE_E && (a.N >= 4096 || a.top_k * ((a.I * a.bits / 8 + 255) / 256) <= 7 * 8);
+  const size_t pairs = (size_t)a.M * a.top_k, slots = one || pairs < (size_t)a.E ? pairs : (size_t)a.E;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t sizes[8] = {up(8 * slots), up(4 * slots * a.M), up(4 * (size_t)a.M), up(4 * (size_t)a.M), up(4 * pairs),
-                           up(2 * pairs), up(4 * pairs * a.I), few ? 0 : up(4 * pairs * a.N)};
+                           up(2 * pairs), up(4 * pairs * a.I), one ? 0 : up(4 * pairs * a.N)};
   size_t total = 0;
   for (size_t n : sizes) total += n;
   void* p = nullptr;
@@ -140,9 +143,9 @@ hipError_t launch_moe(MoeArgs& a, hipStream_t s) {
   a.choice = reinterpret_cast<uint16_t*>(take(5));
   a.h = reinterpret_cast<float*>(take(6));
   a.part = reinterpret_cast<float*>(take(7));
-  if (few) {
-    e = launch_moe_product(a, MOE_FEW_UP, s);
-    return e == hipSuccess ? launch_moe_product(a, MOE_FEW_DOWN, s) : e;
+  if (one) {
+    e = launch_moe_product(a, MOE_ONE_UP, s);
+    return e == hipSuccess ? launch_moe_product(a, MOE_ONE_DOWN, s) : e;
   }
   const dim3 tokens((unsigned)a.M);
   if (a.E <= 64) hipLaunchKernelGGL(moe_route_kernel<1>, tokens, dim3(64), 0, s, a);
