@@ -328,6 +328,7 @@ struct MoeShape {
   int K;        // columns of the product
   int pairs;    // slots are pairs, not experts
   int tiles;    // a wave's, where it takes whole rows
+  int chunk;    // quads of x in LDS at a time, there
   int x_bytes;  // x in LDS, a wave's where it takes a part of the columns
 };
 enum MoeStep : int { MOE_UP, MOE_DOWN, MOE_ONE_UP, MOE_ONE_DOWN };

@@ -459,29 +459,35 @@ __device__ __forceinline__ void moe_open(const MoeArgs& a, int e, int tile, int 
 __device__ __forceinline__ int moe_vrow(int c, int vrows) { return min((c >> 2) + 4 * (c & 3), vrows - 1); }
 
 // whole rows a wave (KS = 1): what is loaded next of the quads and of the blocks of parameters of tiles [tile0, tile1)
-template <int BITS, int G, bool F16_, bool DOWN>
+template <int BITS, int G, bool F16_, bool DOWN, bool PARTS>
 struct RowLoader {
   using St = Stream<BITS, G, F16_, 2>;
   St st, sp;
   typename St::Quad w;
   typename St::Params pr;
-  int e, K, quads, blocks, tile1, lt, lq, pt, pb, left, pleft;
+  int e, K, quads, blocks, tile1, lt, lq, pt, pb, left, pleft, fixed;
 
-  // the quad, and block of parameters, that a tile's sums begin with
-  __device__ __forceinline__ int first_block(int tile) const { return blocks > 1 ? tile % blocks : 0; }
-  __device__ __forceinline__ int first_quad(int tile) const { return blocks > 1 ? tile % blocks * St::QPB : tile % quads; }
-
-  __device__ __forceinline__ void begin(const MoeArgs& a, const MoeShape& s, int expert, unsigned char* buf, int tile0, int end) {
+  // The quad that a tile's sums begin with: another one for every tile, so that not all waves read the same columns (memory
+  // channels) at once, at a block of parameters where a row has several; or `fixed`, where x is in LDS by PARTS.
+  __device__ __forceinline__ int start(int tile) const {
+    return PARTS ? fixed : blocks > 1 ? tile % blocks * St::QPB : tile % quads;
+  }
+  __device__ __forceinline__ void start_params(int tile) {
+    pb = start(tile) / St::QPB;
+    pleft = blocks + (PARTS && blocks > 1 && fixed % St::QPB != 0);  // (its block once more at the end)
+  }
+  __device__ __forceinline__ void begin(const MoeArgs& a, const MoeShape& s, int expert, unsigned char* buf, int tile0, int end,
+                                        int first) {
     e = expert;
     K = s.K;
     quads = (K + St::COLS - 1) / St::COLS;
     blocks = (quads + St::QPB - 1) / St::QPB;
+    fixed = first;
     tile1 = end;
     lt = pt = tile0;
-    lq = first_quad(tile0);
-    pb = first_block(tile0);
+    lq = start(tile0);
     left = quads;
-    pleft = blocks;
+    start_params(tile0);
     st.buf = sp.buf = buf;
     st.lane = sp.lane = threadIdx.x & 63;
     if (tile0 >= tile1) return;
@@ -495,7 +501,7 @@ struct RowLoader {
     if (++lq == quads) lq = 0;
     if (--left == 0) {
       left = quads;
-      lq = first_quad(++lt);
+      lq = start(++lt);
       if (lt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, lt, K, st);
     }
   }
@@ -503,67 +509,66 @@ struct RowLoader {
     sp.load(pt < tile1 ? pb : blocks, pr);
     if (++pb == blocks) pb = 0;
     if (--pleft == 0) {
-      pleft = blocks;
-      pb = first_block(++pt);
+      start_params(++pt);
       if (pt < tile1) moe_open<BITS, G, F16_, DOWN>(a, e, pt, K, sp);
     }
   }
 };
 
-// the sums of those tiles, x of all quads in LDS; back: [quad][16 tokens]
-template <int BITS, int G, bool F16_, bool DOWN, int ROWS>
+// what a wave's sums have come to
+template <int NI>
+struct RowSums {
+  int tile, q, left;  // the quad next, and how many the tile still has
+  float total[2][NI];
+};
+
+// `steps` quads of those tiles; x from quad c0 on in LDS; back: [quad][16 tokens]
+template <int BITS, int G, bool F16_, bool DOWN, int ROWS, bool PARTS>
 __device__ __forceinline__ void moe_rows(const MoeArgs& a, const int* list, int tokens, const float* back, const unsigned char* xs,
-                                         RowLoader<BITS, G, F16_, DOWN>& ld, int tile0, int tile1) {
+                                         int c0, RowLoader<BITS, G, F16_, DOWN, PARTS>& ld, RowSums<ROWS / 4>& r, int steps) {
   using St = Stream<BITS, G, F16_, 2>;
   constexpr int NI = ROWS / 4;
-  if (tile0 >= tile1) return;
   const int lane = threadIdx.x & 63;
   const int c = lane & 15, h = lane >> 4, quads = ld.quads;
   const unsigned char* x0 = xs + (h * ROWS + moe_vrow(c, DOWN ? 2 * tokens : tokens)) * 16;
-  int tile = tile0, q = ld.first_quad(tile0), left = quads;  // what is computed next
-  float total[2][NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) total[0][i] = total[1][i] = 0.f;
-  const auto step = [&]() __attribute__((always_inline)) {
-    if (q % St::QPB == 0 || left == quads) {
+  for (int i = 0; i < steps; ++i) {
+    if (r.left == quads || (ld.blocks > 1 && r.q % St::QPB == 0)) {  // (a single block serves all quads, wherever they begin)
       ld.sp.put(ld.pr);
       ld.next_params(a);
     }
     __builtin_amdgcn_wave_barrier();  // (LDS of this wave alone, whose operations stay in order)
     float acc[2][NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) acc[0][i] = acc[1][i] = 0.f;
-    ld.st.template compute<NI, ROWS>(q, ld.w, x0 + q * (St::S::NJ * 256 * ROWS), acc);
+    for (int k = 0; k < NI; ++k) acc[0][k] = acc[1][k] = 0.f;
+    ld.st.template compute<NI, ROWS>(r.q, ld.w, x0 + (r.q - c0) * (St::S::NJ * 256 * ROWS), acc);
     __builtin_amdgcn_wave_barrier();
     ld.next(a);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const float f = back[16 * q + (DOWN ? (4 * i + h) / 2 : 4 * i + h)];
-      total[0][i] = fmaf(acc[0][i] * 0x1p24f, f, total[0][i]);
-      total[1][i] = fmaf(acc[1][i] * 0x1p24f, f, total[1][i]);
+    for (int k = 0; k < NI; ++k) {
+      const float f = back[16 * (r.q - c0) + (DOWN ? (4 * k + h) / 2 : 4 * k + h)];
+      r.total[0][k] = fmaf(acc[0][k] * 0x1p24f, f, r.total[0][k]);
+      r.total[1][k] = fmaf(acc[1][k] * 0x1p24f, f, r.total[1][k]);
     }
-    if (++q == quads) q = 0;
-    if (--left) return;
+    if (++r.q == quads) r.q = 0;
+    if (--r.left) continue;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int v = 4 * i + h;
+    for (int k = 0; k < NI; ++k) {
+      const int v = 4 * k + h;
       if constexpr (DOWN) {
         // the high and the low part's sums are neighbours: lanes of even h take tile 0's total, of odd h tile 1's
-        uint32_t p = __float_as_uint(total[0][i]), r = __float_as_uint(total[1][i]);
-        swap16(p, r);
+        uint32_t x = __float_as_uint(r.total[0][k]), y = __float_as_uint(r.total[1][k]);
+        swap16(x, y);
         if (v / 2 < tokens)
-          a.part[(long)list[v / 2] * a.N + 32 * tile + 16 * (h & 1) + c] = __uint_as_float(p) + __uint_as_float(r);
+          a.part[(long)list[v / 2] * a.N + 32 * r.tile + 16 * (h & 1) + c] = __uint_as_float(x) + __uint_as_float(y);
       } else {
-        const float g = total[0][i], u = total[1][i];
-        if (v < tokens) a.h[(long)list[v] * a.I + 16 * tile + c] = g / (1.f + expf(-g)) * u;
+        const float g = r.total[0][k], u = r.total[1][k];
+        if (v < tokens) a.h[(long)list[v] * a.I + 16 * r.tile + c] = g / (1.f + expf(-g)) * u;
       }
-      total[0][i] = total[1][i] = 0.f;
+      r.total[0][k] = r.total[1][k] = 0.f;
     }
-    q = ld.first_quad(++tile);
-    left = quads;
-  };
-  const int all = (tile1 - tile0) * quads;
-  for (int i = 0; i < all; ++i) step();
+    r.q = ld.start(++r.tile);
+    r.left = quads;
+  }
 }
 
 // a part of the columns a wave (KS = 4), each with its own x: this wave's sums of its quads of tile `tile`
@@ -672,10 +677,11 @@ __device__ __forceinline__ void moe_finish(const MoeArgs& a, const int* out, int
 }
 
 template <int BITS, int G, bool F16_, bool DOWN, int KS, int ROWS>
-__global__ __launch_bounds__(256, KS == 1 ? 4 : 3) void moe_kernel(MoeArgs a, MoeShape s) {
+__global__ __launch_bounds__(256, KS == 4 ? 3 : 4) void moe_kernel(MoeArgs a, MoeShape s) {
   using St = Stream<BITS, G, F16_, 2>;
   using Xq = XQuad<BITS, G, F16_, DOWN>;
   constexpr int WAVES = 4, NI = ROWS / 4;
+  constexpr bool PARTS = KS == 2;  // whole rows a wave, a tile each, x in LDS part by part
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int list[256];
   __shared__ int part[WAVES];
@@ -711,25 +717,37 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 3) void moe_kernel(MoeArgs a, Mo
       moe_finish<DOWN, NI>(a, mine, tokens, red, blockIdx.x, total);
     } else {
       const int tile0 = (blockIdx.x * WAVES + wave) * s.tiles, tile1 = min(tile0 + s.tiles, DOWN ? a.N / 32 : a.I / 16);
-      RowLoader<BITS, G, F16_, DOWN> ld;
-      ld.begin(a, s, e, lds + s.x_bytes + wave * St::BYTES, tile0, tile1);
       // x: quads of tokens, dealt to the waves, two in flight
-      const int quads = ld.quads, jobs = tokens * quads;
+      const int quads = (s.K + St::COLS - 1) / St::COLS, chunk = PARTS ? s.chunk : quads;
+      const int chunks = PARTS ? (quads + chunk - 1) / chunk : 1, first_chunk = PARTS ? blockIdx.x % chunks : 0;
+      RowLoader<BITS, G, F16_, DOWN, PARTS> ld;
+      ld.begin(a, s, e, lds + s.x_bytes + wave * St::BYTES, tile0, tile1, first_chunk * chunk);
       float* back = reinterpret_cast<float*>(lds + s.x_bytes + WAVES * St::BYTES);
-      for (int j = wave; j < jobs; j += 2 * WAVES) {
-        const int t0 = j / quads, q0 = j - t0 * quads, k = min(j + WAVES, jobs - 1), t1 = k / quads, q1 = k - t1 * quads;
-        Xq x0, x1;
-        x0.load(moe_source<DOWN>(a, mine[t0]), s.K, q0, lane, true);
-        x1.load(moe_source<DOWN>(a, mine[t1]), s.K, q1, lane, true);
-        float f = x0.put(lds + q0 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t0 : t0, lane);
-        if (lane == 0) back[16 * q0 + t0] = f;
-        if (j + WAVES < jobs) {
-          f = x1.put(lds + q1 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t1 : t1, lane);
-          if (lane == 0) back[16 * q1 + t1] = f;
+      RowSums<NI> sums;
+      sums.tile = tile0;
+      sums.q = ld.start(tile0);
+      sums.left = quads;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) sums.total[0][k] = sums.total[1][k] = 0.f;
+      for (int ci = 0; ci < chunks; ++ci) {
+        const int ch = first_chunk + ci < chunks ? first_chunk + ci : first_chunk + ci - chunks;
+        const int c0 = ch * chunk, cq = min(chunk, quads - c0), jobs = tokens * cq;
+        if (ci) __syncthreads();
+        for (int j = wave; j < jobs; j += 2 * WAVES) {
+          const int t0 = j / cq, q0 = j - t0 * cq, k = min(j + WAVES, jobs - 1), t1 = k / cq, q1 = k - t1 * cq;
+          Xq x0, x1;
+          x0.load(moe_source<DOWN>(a, mine[t0]), s.K, c0 + q0, lane, true);
+          x1.load(moe_source<DOWN>(a, mine[t1]), s.K, c0 + q1, lane, true);
+          float f = x0.put(lds + q0 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t0 : t0, lane);
+          if (lane == 0) back[16 * q0 + t0] = f;
+          if (j + WAVES < jobs) {
+            f = x1.put(lds + q1 * (Xq::UNITS * 16 * ROWS), ROWS, DOWN ? 2 * t1 : t1, lane);
+            if (lane == 0) back[16 * q1 + t1] = f;
+          }
         }
+        __syncthreads();
+        moe_rows<BITS, G, F16_, DOWN, ROWS, PARTS>(a, mine, tokens, back, lds, c0, ld, sums, tile0 < tile1 ? (tile1 - tile0) * cq : 0);
       }
-      __syncthreads();
-      moe_rows<BITS, G, F16_, DOWN, ROWS>(a, mine, tokens, back, lds, ld, tile0, tile1);
       __syncthreads();
     }
   }
@@ -882,20 +900,26 @@ hipError_t launch_moe_dt(const MoeArgs& a, MoeStep step, hipStream_t st) {
   const int64_t pairs = (int64_t)a.M * a.top_k;
   const int most = 2 * pairs <= 3 * (int64_t)a.E ? 4 : pairs <= 4 * (int64_t)a.E ? 8 : 16;
   const int rows = down ? std::min(2 * most, 16) : most;
-  // whole rows a wave from a wave a SIMD on (3 tokens, 8 of 64 experts, 2048 x 1024, 1536 tiles: 48 us in parts, 38 whole;
-  // 8 tokens, 2 of 8, 4096 x 1024, 8-bit, 512: 43 and 52)
-  const bool whole = rows * quads * QUAD <= 65536 && (int64_t)tiles * slots >= 1024;
+  s.chunk = std::min(quads, 65536 / (rows * QUAD));  // quads of x in 64 KiB
+  // Whole rows a wave from a wave a SIMD on (3 tokens, 8 of 64 experts, 2048 x 1024, 1536 tiles: 48 us in parts, 38 whole;
+  // 8 tokens, 2 of 8, 4096 x 1024, 8-bit, 512: 43 and 52).  Where a row of x does not fit, x in parts for many tokens, which
+  // would be read again by every fourth of them (64 tokens, 2 of 8, 4096 x 4096: 255 and 188 us), but not for a few (13, 4
+  // of 16, 8192 x 2816: 252 and 272).
+  const bool many = (int64_t)tiles * slots >= 1024, whole = many && s.chunk == quads, parts = many && !whole && rows == 16;
   // A tile a wave, or two where that leaves a second round of workgroups less than half full (three a CU; 16 tokens, 8 of
   // 64 experts, 2048 x 1024: 1.2 rounds, 38 us with one and 33 with two; 64 tokens, 8 of 128, 2048 x 768: 2.0 rounds, 67
   // and 76).  Experts in use: what independent tokens would reach.
   const double used = s.pairs ? slots : a.E * (1.0 - std::pow(1.0 - (double)a.top_k / a.E, (double)a.M));
   const double rounds = used * ((tiles + 3) / 4) / 768.0;
-  s.tiles = rounds > 1.0 && rounds < 1.5 ? 2 : 1;
-  s.x_bytes = whole ? rows * quads * QUAD : 8 * QUAD;
-  const dim3 grid((unsigned)(whole ? (tiles + 4 * s.tiles - 1) / (4 * s.tiles) : tiles), (unsigned)slots);
-  const int lds = whole ? s.x_bytes + 4 * St::BYTES + 64 * quads : 4 * (s.x_bytes + St::BYTES);
+  s.tiles = whole && rounds > 1.0 && rounds < 1.5 ? 2 : 1;
+  s.x_bytes = whole || parts ? rows * s.chunk * QUAD : 8 * QUAD;
+  const dim3 grid((unsigned)(whole || parts ? (tiles + 4 * s.tiles - 1) / (4 * s.tiles) : tiles), (unsigned)slots);
+  const int lds = whole || parts ? s.x_bytes + 4 * St::BYTES + 64 * s.chunk : 4 * (s.x_bytes + St::BYTES);
 #define QAFF_MOE(DOWN, KS, ROWS) hipLaunchKernelGGL((moe_kernel<BITS, G, F16_, DOWN, KS, ROWS>), grid, dim3(256), lds, st, a, s)
-  if (!whole) {
+  if (parts) {
+    if (down) QAFF_MOE(true, 2, 16);
+    else QAFF_MOE(false, 2, 16);
+  } else if (!whole) {
     if (down) QAFF_MOE(true, 4, 8);
     else QAFF_MOE(false, 4, 8);
   } else if (down) {

@@ -273,30 +273,32 @@ def moe(x, logits, gate_up, down, dtype: str, G: int, bits: int, top_k: int, ren
     size, chosen = np.zeros_like(y), []
     inner = down[0].shape[2] * 32 // bits
 
-    def product(v, triple, e, err):
-        """v W^T and the size of its roundings; err: the size of v's own"""
-        w, s, b = (t[e] for t in triple)
-        c, sv, bv = codes(w, bits).astype(np.float64), oracle.to_f64(s, dtype), oracle.to_f64(b, dtype)
-        big = np.abs(np.repeat(sv, G, -1)) * c + np.repeat(np.abs(bv), G, -1)
-        full = c * np.repeat(sv, G, -1) + np.repeat(bv, G, -1)
-        return v @ full.T, np.abs(v) @ big.T + err @ np.abs(full).T
+    def dense(triple, e):
+        """the weight, and what its roundings go by: code |s| + |b|"""
+        w, sc, b = (t[e] for t in triple)
+        c, sv, bv = codes(w, bits).astype(np.float64), oracle.to_f64(sc, dtype), oracle.to_f64(b, dtype)
+        sv, bv = np.repeat(sv, G, -1), np.repeat(bv, G, -1)
+        return c * sv + bv, c * np.abs(sv) + np.abs(bv)
 
+    p = np.zeros((M, E))
     for m in range(M):
         z = logits[m]
         order = [e for e in sorted(range(E), key=lambda e: (-z[e], e)) if z[e] > -np.inf][:top_k]
         chosen.append(order)
-        if not order:
+        if order:
+            w = np.exp(z - z[order[0]])
+            p[m, order] = w[order] / (w[order].sum() if renormalize else w.sum()) * scale
+    for e in range(E):
+        rows = [m for m in range(M) if e in chosen[m]]
+        if not rows:
             continue
-        w = np.exp(z - z[order[0]])
-        total = w[order].sum() if renormalize else w.sum()
-        for e in order:
-            a, ea = product(xv[m:m + 1], gate_up, e, np.zeros_like(xv[m:m + 1]))
-            g, u = a[:, :inner], a[:, inner:]
-            sg = g / (1 + np.exp(-g))
-            h = sg * u
-            eh = 1.1 * ea[:, :inner] * np.abs(u) + ea[:, inner:] * np.abs(sg) + 4 * np.abs(h)
-            d, ed = product(h, down, e, eh)
-            p = w[e] / total * scale
-            y[m] += p * d[0]
-            size[m] += abs(p) * ed[0]
+        w, big = dense(gate_up, e)
+        a, ea = xv[rows] @ w.T, np.abs(xv[rows]) @ big.T
+        g, u = a[:, :inner], a[:, inner:]
+        sg = g * np.where(g > 0, 1.0, np.exp(np.minimum(g, 0))) / (1 + np.exp(-np.abs(g)))
+        h = sg * u
+        eh = 1.1 * ea[:, :inner] * np.abs(u) + ea[:, inner:] * np.abs(sg) + 4 * np.abs(h)
+        w, big = dense(down, e)
+        y[rows] += p[rows, e][:, None] * (h @ w.T)
+        size[rows] += np.abs(p[rows, e])[:, None] * (np.abs(h) @ big.T + eh @ np.abs(w).T)
     return y, size, chosen
