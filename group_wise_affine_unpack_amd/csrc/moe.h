@@ -19,7 +19,12 @@
 // the 2^s is taken out of the x entry that meets it.  x is scaled per row and
 // quad of columns by a power of two so that its largest entry there is near
 // 2^15 and held in f16, exact for entries down to 2^-25 of the largest; h, which
-// is f32, as two f16 rows, high and low part, 22 bits.  Per group of columns the scale
+// is f32, as two f16 rows, high and low part, 22 bits.  A matrix instruction
+// treats a subnormal operand as one of 2^-14 and cuts its products 24 bits below
+// that, so a code's product is held to 2^-14 or so of one step times the largest
+// x (measured, h before its rounding: 2^-16 with 2 bits, 2^-18 with 4, 2^-21
+// with 8), under the output's half step in each type; the sums of x, whose other
+// operand is normal, are not cut so.  Per group of columns the scale
 // multiplies the sum of codes * x, the bias the sum of x, both in fp32.
 //
 // Bound by memory: every chosen expert's weights once.  A wave streams 16 or
@@ -94,9 +99,11 @@ struct Span {
   __device__ static __forceinline__ float unit(int i) {
     return BITS == 8 ? 1.f : BITS == 4 ? ((i & 1) ? 0x1p-4f : 1.f) : (i == 0 ? 1.f : i == 1 ? 0x1p-2f : i == 2 ? 0x1p-4f : 0x1p-6f);
   }
-  // f16 bits of 2^-24 / unit, what a sum of x takes in the place of codes (subnormal, as they are)
+  // f16 bits of 1 / unit: what a sum of x takes in the place of codes.  (Normal numbers: with 2^-24
+  // itself, as subnormal as a code of one, the matrix cores left a sum 15 bits, and the block's output 2^-15 of h off.)
   __device__ static __forceinline__ uint32_t ones(int i) {
-    return (BITS == 8 ? 1u : BITS == 4 ? ((i & 1) ? 16u : 1u) : 1u << (2 * i)) * 0x10001u;
+    const uint32_t e = BITS == 8 ? 0 : BITS == 4 ? 4 * (i & 1) : 2 * i;
+    return (0x3C00u + (e << 10)) * 0x10001u;
   }
 
   // the four words of a lane exchanged so that word j (words 2j, 2j + 1 for 8 bits) holds codes of one group in every lane
@@ -333,7 +340,7 @@ struct Stream {
           const uint32_t b = (gi & 1) ? v >> 16 : v & 0xffffu;
           return F16_ ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
         };
-        const float s = value(pr[2 * t]), b = value(pr[2 * t + 1]);
+        const float s = value(pr[2 * t]), b = value(pr[2 * t + 1]) * 0x1p-24f;  // codes, and so acc, are 2^-24 of themselves
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[t][i] = fmaf(s, dot[t][i], fmaf(b, sum[i], acc[t][i]));
       }

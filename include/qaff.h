@@ -643,13 +643,13 @@ int kv_cache_append_rotary_affine(const qaff_kv_cache *cache, const qaff_rotary 
  *   128}), at most 65536, with rows of whole 16-byte chunks
  *   num_experts at most 1024; top_k at most 64 and num_experts; M at most 256
  *   (QAFF_E_UNSUPPORTED)
- * Accuracy: x is held exactly down to 2^-25 of its row's largest entry, the
- * inner row to 22 bits, sums in fp32, one rounding at the end; for finite
- * inputs within a few 2^-20 of the sum of the products' sizes, before it.  A
+ * Accuracy: x is held exactly down to 2^-25 of the largest entry of its 256 to
+ * 1024 columns, the inner row to 22 bits, sums in fp32, one rounding at the
+ * end; a product is held to 2^-13 of a step (a scale) times the largest x.  A
  * token whose logits hold a NaN, or whose x is not finite, gives a row that is
  * not finite (the former NaN); other tokens' rows are not touched by it.
- * Weights are read once per 16 tokens of an expert (Down: 8), only those of
- * chosen experts.  Uses library scratch: capture after an eager call of the
+ * Weights are read once per 4, 8 or 16 tokens of an expert (Down: 4 or 8), only
+ * those of chosen experts.  One token: two kernels, more: four.  Uses library scratch: capture after an eager call of the
  * same shapes.  The same call gives the same bits.
  */
 typedef struct qaff_experts {

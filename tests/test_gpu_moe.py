@@ -1,14 +1,16 @@
 """GPU tests of qmoe_affine against the fp64 definition (oracle.decoder.moe).
 
 Tolerance, derived from the kernel's roundings: a rounding of fp32 is u =
-2^-24 of what it rounds (2 u where the matrix cores may cut).  A group's sums
+2^-24 of what it rounds (2 u where the matrix cores may cut; products of codes, which are
+subnormal there, at 2^-14 of a code's step times the largest x, which for the
+random signs here adds below 2^-18 of the sizes even with 2 bits).  A group's sums
 of G products and the sum over K/G groups are taken as random walks with a
 factor 6, 6 (2 sqrt(G) + sqrt(K/G)) u of the sizes of what is added (for the
 larger of the two products' K): `size` of the oracle, which carries the first
 product's error through silu and the second product.  x is exact, h is held to
 2^-22, exp, the division and the weights are off by a few u: all below the
 factor's least value, 6 (2 sqrt(32) + 1) = 73.  Then half a step of the output
-type.  The tests show that a lost token's expert or a scale 5% off would fail."""
+type.  The tests show that a scale 5% off would fail."""
 import numpy as np
 import pytest
 import torch
@@ -302,3 +304,54 @@ def test_two_streams():
     torch.cuda.synchronize()
     for a, b in zip(want[0] + want[1], got[0] + got[1]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [2, 4, 8])
+@pytest.mark.parametrize("M,E", [(1, 8), (8, 64), (40, 64), (256, 8)])
+def test_inner_precision(M, E, bits):
+    """h and its sums beyond the output's 11 bits: Down copies h (code and scale 1), a second call with the first one's
+    output as the negative residual returns what the first rounding left, so h is seen to 2^-22.
+
+    Bound on the rms: a product of a code is cut at 2^-14 of the code's step s times the largest x, K independent cuts,
+    twice that; two fp32 roundings a group of sums that walk to sqrt(sum (w x)^2), 3 times that; h, silu and the
+    remainder's rounding at 2^-20 together.  (Sums of x left 2^-15 off would be twice the bound of 8 bits.)"""
+    dev = require_gpu()
+    K, G = 1024, 64
+    print(f"[case] moe precision M={M} E={E} bits={bits}", flush=True)
+    rng = np.random.default_rng((M, E, bits))
+    per = 32 // bits
+
+    def pack(c):
+        return (c.reshape(*c.shape[:-1], -1, per).astype(np.uint64) << (np.arange(per, dtype=np.uint64) * np.uint64(bits))).sum(-1).astype(np.uint32)
+
+    I = 256
+    q = rng.integers(0, 2**bits, (E, 2 * I, K))
+    s = (rng.uniform(0.5, 1.0, (E, 2 * I, K // G)) * 0.15 / 2**bits).astype(np.float16)
+    b = (-s.astype(np.float64) * (2**bits - 1) / 2).astype(np.float16)
+    d = np.zeros((E, K, I), np.int64)
+    n = np.arange(K)
+    d[:, n, n % I] = 1
+    triples = [(pack(q), s.view(np.uint16), b.view(np.uint16)),
+               (pack(d), np.ones((E, K, I // G), np.float16).view(np.uint16), np.zeros((E, K, I // G), np.uint16))]
+    ex = _to_device(triples, "f16", dev, G, bits)
+    x = rng.standard_normal((M, K)).astype(np.float16)
+    z = rng.standard_normal((M, E)).astype(np.float32)
+    xd, zd = torch.from_numpy(x).to(dev), torch.from_numpy(z).to(dev)
+    y0 = qa.qmoe_affine(xd, zd, ex, 1)
+    y1 = qa.qmoe_affine(xd, zd, ex, 1, resid=-y0)
+    got = host_f64(y0) + host_f64(y1)
+    x64 = x.astype(np.float64)
+    ref, var, size = np.empty((M, K)), [], []
+    for m, e in enumerate(z.argmax(1)):
+        step, off = s[e].astype(np.float64).repeat(G, -1), b[e].astype(np.float64).repeat(G, -1)
+        a = (q[e] * step + off) @ x64[m]
+        g, u = a[:I], a[I:]
+        silu = g / (1 + np.exp(-g))
+        ref[m] = (silu * u)[n % I]
+        walk = np.sqrt(((q[e] * step) ** 2) @ x64[m] ** 2).max() + np.sqrt((off**2) @ x64[m] ** 2).max()
+        delta = 2 * np.sqrt(K) * 2.0**-14 * step.max() * np.abs(x64[m]).max() + 3 * np.sqrt(2 * K / G) * U * walk
+        var.append(delta**2 * ((1.1 * u) ** 2 + silu**2).mean())
+    rms = np.sqrt(((got - ref) ** 2).mean())
+    tol = np.sqrt(np.mean(var)) + 2.0**-20 * np.sqrt((ref**2).mean())
+    print(f"[parity] rms {rms:.3g} of {np.sqrt((ref**2).mean()):.3g}, bound {tol:.3g}", flush=True)
+    assert rms <= tol
