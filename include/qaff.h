@@ -23,8 +23,9 @@
  *   - The caller owns every buffer; the library keeps no pointer to them
  *     after the call returns.  Internal scratch (GEMM pre-pass buffers and
  *     split-K partials, GPTQ partials and tables, permuted activations for
- *     k_perm, the parts of split sequences in paged_attention_affine) comes from a buffer the library keeps per (device, stream):
- *     calls on one stream reuse it in stream order, and once it is large
+ *     k_perm, the parts of split sequences in paged_attention_affine, the
+ *     choices, inner rows and partial rows of qmoe_affine) comes from a buffer
+ *     the library keeps per (device, stream): calls on one stream reuse it in stream order, and once it is large
  *     enough no call allocates.  It only grows, and growing is refused
  *     (QAFF_E_HIP) while `stream` is being captured into a graph: capture a
  *     call after one eager call of the same shapes on the same stream.
@@ -646,8 +647,8 @@ int kv_cache_append_rotary_affine(const qaff_kv_cache *cache, const qaff_rotary 
  * Accuracy: x is held exactly down to 2^-25 of the largest entry of its 256 to
  * 1024 columns, the inner row to 22 bits, sums in fp32, one rounding at the
  * end; a product is held to 2^-13 of a step (a scale) times the largest x.  A
- * token whose logits hold a NaN, or whose x is not finite, gives a row that is
- * not finite (the former NaN); other tokens' rows are not touched by it.
+ * token whose logits hold a NaN or a plus infinity, or whose x is not finite, gives a row that is
+ * not finite (NaN for the first two); other tokens' rows are not touched by it.
  * Weights are read once per 4, 8 or 16 tokens of an expert (Down: 4 or 8), only
  * those of chosen experts.  One token: two kernels, more: four.  Uses library scratch: capture after an eager call of the
  * same shapes.  The same call gives the same bits.
