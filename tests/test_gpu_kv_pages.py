@@ -206,3 +206,11 @@ def test_two_pools_on_two_streams():
         for a, b in zip(g, want[1:5]):
             assert np.array_equal(a.cpu().numpy(), b)
         x.check(want[6])
+
+
+def test_more_rows_than_a_pass_of_the_grid():
+    # 512 workgroups of 256 rows at most: beyond 131072 rows each goes round again
+    dev = require_gpu()
+    x = Batch([5, 0, 33], 12600, 16, 20000, dev)
+    x.assign([200000, 3, 100000], 300001, in_place=True)  # (and two rows cut)
+    x.trim([5, 0, 33], in_place=True)
